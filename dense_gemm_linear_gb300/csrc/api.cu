@@ -474,8 +474,10 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
       fill_decode_plan(pr.dtype, pr.out, pr.m, pr.n, pr.K, ds->num_sms, &plan);
     } else if (forced->path == DGL_PATH_TC) {
       if (!tc_supported_tile(forced->tile_m, forced->tile_n)) return DGL_ERR_UNSUPPORTED;
-      // 64-row tiles read K-major operands only
+      // 64-row tiles read K-major operands only; an MN-major B arrives in boxes
+      // of 64 columns, which each CTA's half of a 224-wide tile does not divide
       if (forced->tile_m == 64 && (pr.a_mn || pr.b_mn)) return DGL_ERR_UNSUPPORTED;
+      if (forced->tile_n == 224 && pr.b_mn) return DGL_ERR_UNSUPPORTED;
       if (linear && !tc_supported_epi_tile(forced->tile_m, forced->tile_n, pr.gated != 0)) return DGL_ERR_UNSUPPORTED;
       fill_tc_plan(pr.dtype, pr.out, pr.m, pr.gated ? 2 * pr.n : pr.n, pr.K, forced->tile_m, forced->tile_n,
                    ds->num_sms, &plan, forced->stream_k > 0 ? forced->stream_k : 0);
@@ -492,6 +494,8 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
     if (plan.path != DGL_PATH_TC) fill_tc_plan(pr.dtype, pr.out, pr.m, pr.n, pr.K, 128, 128, ds->num_sms, &plan, 0);
     if (plan.tile_m == 64 && (pr.a_mn || pr.b_mn))
       fill_tc_plan(pr.dtype, pr.out, pr.m, pr.n, pr.K, 128, plan.tile_n, ds->num_sms, &plan, 0);
+    if (plan.tile_n == 224 && pr.b_mn)
+      fill_tc_plan(pr.dtype, pr.out, pr.m, pr.n, pr.K, 256, 256, ds->num_sms, &plan, 0);
   } else {
     PlanKey key{dev, pr.dtype, pr.out, pr.m, pr.n, pr.K};
     std::lock_guard<std::mutex> lock(g_mu);
