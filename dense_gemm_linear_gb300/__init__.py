@@ -43,7 +43,9 @@ MN_MAJOR = 1
 EXPORTED = ["dgl_gemm_bf16", "dgl_gemm_fp8", "dgl_gemm_planned", "dgl_plan", "dgl_tile_metrics",
             "dgl_device_status", "dgl_status_string", "dgl_version", "dgl_gemm_noalloc", "dgl_linear",
             "dgl_plan_linear", "dgl_gemm_bf16_ex", "dgl_gemm_mxfp4", "dgl_shutdown", "dgl_gemm_w4a8",
-            "dgl_gemm_batch"]
+            "dgl_gemm_batch", "dgl_head_workspace", "dgl_linear_xent", "dgl_linear_distill"]
+
+DISTILL_MAX_K = 128
 
 
 class PlanInfo(ctypes.Structure):
@@ -63,6 +65,16 @@ class GemmDesc(ctypes.Structure):
                 ("B", ctypes.c_void_p), ("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p),
                 ("C", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("m_valid", ctypes.c_int64), ("n_valid", ctypes.c_int64)]
+
+
+class HeadDesc(ctypes.Structure):
+    """Arguments of the head losses (the C struct dgl_head_desc)."""
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("loss", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("ws", ctypes.c_void_p),
+                ("ws_bytes", ctypes.c_int64), ("logit_scale", ctypes.c_float), ("dw_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
 
 
 class DglError(RuntimeError):
@@ -107,6 +119,12 @@ def load_library(path: str | None = None):
     lib.dgl_gemm_mxfp4.restype = i32
     lib.dgl_gemm_batch.argtypes = [ctypes.POINTER(GemmDesc), i32, vp]
     lib.dgl_gemm_batch.restype = i32
+    lib.dgl_head_workspace.argtypes = [ctypes.POINTER(HeadDesc), i32, ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    lib.dgl_head_workspace.restype = i32
+    lib.dgl_linear_xent.argtypes = [ctypes.POINTER(HeadDesc), vp, i64, vp]
+    lib.dgl_linear_xent.restype = i32
+    lib.dgl_linear_distill.argtypes = [ctypes.POINTER(HeadDesc), vp, vp, vp, i32, ctypes.c_float, vp]
+    lib.dgl_linear_distill.restype = i32
     lib.dgl_plan.argtypes = [i32, i64, i64, i64, i32, i32, ctypes.POINTER(PlanInfo)]
     lib.dgl_plan.restype = i32
     lib.dgl_tile_metrics.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(PlanInfo)]
@@ -192,6 +210,24 @@ def dgl_gemm_bf16_ex(a_major, b_major, A, lda, B, ldb, C, ldc, m, n, K, out_dtyp
     """bf16 GEMM with K-major or MN-major operands and explicit pitches (see include/dgl.h)."""
     return load_library().dgl_gemm_bf16_ex(a_major, b_major, A, lda, B, ldb, C, ldc, m, n, K, out_dtype,
                                            ctypes.byref(plan) if plan is not None else None, stream)
+
+
+def dgl_head_workspace(head: HeadDesc, k=0) -> tuple[int, int]:
+    """(smallest accepted, largest useful) workspace bytes of a head loss."""
+    low, best = ctypes.c_int64(), ctypes.c_int64()
+    _check(load_library().dgl_head_workspace(ctypes.byref(head), k, ctypes.byref(low), ctypes.byref(best)),
+           "dgl_head_workspace")
+    return low.value, best.value
+
+
+def dgl_linear_xent(head: HeadDesc, target, ignore_index=-100, stream=0) -> int:
+    """Softmax cross entropy of a linear head (see include/dgl.h)."""
+    return load_library().dgl_linear_xent(ctypes.byref(head), target, ignore_index, stream)
+
+
+def dgl_linear_distill(head: HeadDesc, indices, logits, teacher_lse, k, temperature=1.0, stream=0) -> int:
+    """Distillation of a linear head from a teacher's top logits (see include/dgl.h)."""
+    return load_library().dgl_linear_distill(ctypes.byref(head), indices, logits, teacher_lse, k, temperature, stream)
 
 
 def dgl_plan(dtype, m, n, K, out_dtype=OUT_BF16, num_sms=0) -> PlanInfo:
@@ -392,3 +428,125 @@ def linear(A, B, bias=None, out=None, *, act=ACT_NONE, gated=False, sa=None, sb=
     _check(st, "dgl_linear")
     return C
 
+
+
+# ---------------------------------------------------------------- losses of a linear head
+def _rows(t, name, dtype, shape):
+    """Checks a CUDA matrix of `shape` whose rows are contiguous; returns its row pitch in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(t, name, dtype, shape):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+
+
+def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, k, call, where):
+    import torch
+    if not isinstance(X, torch.Tensor) or X.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise TypeError("X and W must be 2-D CUDA tensors")
+    T, d = X.shape
+    V = W.shape[0]
+    h = HeadDesc()
+    h.T, h.V, h.d = T, V, d
+    h.ldx = _rows(X, "X", torch.bfloat16, (T, d))
+    h.ldw = _rows(W, "W", torch.bfloat16, (V, d))
+    h.X, h.W = X.data_ptr(), W.data_ptr()
+    h.logit_scale = logit_scale
+    s = stream if stream is not None else torch.cuda.current_stream()
+    # buffers made here belong to the stream that uses them, so the allocator
+    # hands them out again only after its work
+    with torch.cuda.stream(s):
+        loss = torch.empty(T, dtype=torch.float32, device=X.device)
+        lse = torch.empty(T, dtype=torch.float32, device=X.device)
+        h.loss, h.lse = loss.data_ptr(), lse.data_ptr()
+        dX = None
+        if grad is not None:
+            _vector(grad, "grad", torch.float32, (T,))
+            if not (need_dx or need_dw):
+                raise ValueError("a call with grad computes dX, dW or both")
+            h.grad = grad.data_ptr()
+            if need_dx:
+                dX = torch.empty((T, d), dtype=torch.bfloat16, device=X.device)
+                h.dX, h.lddx = dX.data_ptr(), d
+            if need_dw:
+                if dW is None:
+                    if accumulate:
+                        raise ValueError("accumulate adds to the fp32 dW that is passed in")
+                    dW = torch.empty((V, d), dtype=torch.float32 if dw_dtype == OUT_F32 else torch.bfloat16,
+                                     device=X.device)
+                elif dW.dtype not in (torch.float32, torch.bfloat16):
+                    raise TypeError(f"dW must be fp32 or bf16, got {dW.dtype}")
+                h.lddw = _rows(dW, "dW", dW.dtype, (V, d))
+                h.dw_dtype = OUT_F32 if dW.dtype == torch.float32 else OUT_BF16
+                h.dW, h.accumulate = dW.data_ptr(), int(bool(accumulate))
+            elif dW is not None or accumulate:
+                raise ValueError("dW is given but not asked for")
+        elif dW is not None or accumulate:
+            raise ValueError("dW needs grad, the losses' upstream gradient")
+        if workspace is None:
+            workspace = torch.empty(max(1, dgl_head_workspace(h, k)[1]), dtype=torch.uint8, device=X.device)
+        elif not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        h.ws, h.ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _check(call(h, s.cuda_stream), where)
+    if grad is None:
+        return loss, lse
+    return loss, lse, dX, dW if need_dw else None
+
+
+def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_scale=1.0, need_dx=True, need_dw=True,
+                         dW=None, dw_dtype=OUT_BF16, accumulate=False, workspace=None, stream=None):
+    """Softmax cross entropy of the head z = logit_scale X . W^T, without keeping the logits.
+
+    X [T, d], W [V, d] bf16 (rows may be strided), target int64 [T].  Returns
+    (loss, lse), fp32 [T] each.  With grad, fp32 [T], the gradient of the
+    final scalar by each loss (1 / tokens for a mean), returns (loss, lse, dX,
+    dW): dX bf16, dW bf16 or fp32 (dw_dtype, or the type of the dW passed in;
+    accumulate adds to an fp32 dW).  workspace: a CUDA buffer of at least
+    dgl_head_workspace bytes, made when None.
+    """
+    import torch
+    _vector(target, "target", torch.int64, (X.shape[0],))
+    return _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, 0,
+                 lambda h, s: dgl_linear_xent(h, target.data_ptr(), ignore_index, s), "dgl_linear_xent")
+
+
+def linear_distill(X, W, indices, logits, grad=None, *, temperature=1.0, teacher_lse=None, logit_scale=1.0,
+                   need_dx=True, need_dw=True, dW=None, dw_dtype=OUT_BF16, accumulate=False, workspace=None,
+                   stream=None):
+    """Distillation of the head z = logit_scale X . W^T from a teacher's top logits.
+
+    indices int64 [T, k] (negative: absent) and logits fp32 [T, k] are the
+    teacher's; loss_t is the Kullback-Leibler divergence of the student's
+    softmax(z / temperature) from the teacher's distribution over the entries
+    (with teacher_lse, fp32 [T], from its share of the whole vocabulary's).
+    Otherwise as linear_cross_entropy.
+    """
+    import torch
+    T = X.shape[0]
+    k = indices.shape[1] if indices.dim() == 2 else 0
+    if not 1 <= k <= DISTILL_MAX_K:
+        raise ValueError(f"indices must be [T, k] with 1 <= k <= {DISTILL_MAX_K}")
+    _vector(indices, "indices", torch.int64, (T, k))
+    _vector(logits, "logits", torch.float32, (T, k))
+    if teacher_lse is not None:
+        _vector(teacher_lse, "teacher_lse", torch.float32, (T,))
+    return _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, k,
+                 lambda h, s: dgl_linear_distill(h, indices.data_ptr(), logits.data_ptr(),
+                                                 teacher_lse.data_ptr() if teacher_lse is not None else None, k,
+                                                 temperature, s), "dgl_linear_distill")

@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "dgl.h"
+#include "host.h"
 #include "launch.h"
 #include "plan.h"
 
@@ -23,16 +24,6 @@ namespace dgl {
 __device__ int g_status_word;
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-
-struct DeviceState {
-  bool ready = false;
-  int num_sms = 0;
-  int cc_major = 0, cc_minor = 0;
-  int smem_optin = 0;
-  int* status = nullptr;  // device address of g_status_word on this device
-};
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -170,6 +161,7 @@ struct StaticScratch {
 StaticScratch g_noalloc[kMaxDevices];
 std::mutex g_noalloc_mu;  // set-up of g_noalloc
 
+}  // namespace
 
 dgl_status get_device(int* dev_out, DeviceState** st_out) {
   int dev = 0;
@@ -201,6 +193,8 @@ dgl_status get_device(int* dev_out, DeviceState** st_out) {
   *st_out = &st;
   return DGL_OK;
 }
+
+namespace {
 
 // 2-D tensor map over a row-major [rows, inner] matrix with a 128-byte-wide
 // box of box_rows rows and the 128-byte swizzle.  Reads outside
@@ -383,31 +377,6 @@ constexpr int kDecodeRingBytes = 196608;
 // fields (bits 7-9 / 10-12; E4M3 is 0).
 constexpr uint32_t kIdescE2M1 = 5;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Problem {
-  int dtype, out;
-  const void *A, *B;
-  const float *sa, *sb;
-  void* C;
-  int64_t M, N, K, m, n;
-  // linear-layer epilogue (dgl_linear): bias per column, activation, gated up projection
-  const float* bias = nullptr;
-  int act = 0;
-  int gated = 0;
-  // operand layouts (dgl_gemm_bf16_ex): MN-major A is [K][m], B is [K][n];
-  // lda / ldb are row pitches in elements (0: the packed pitch)
-  int a_mn = 0;
-  int b_mn = 0;
-  int64_t lda = 0;
-  int64_t ldb = 0;
-  // W4A8 (dgl_gemm_w4a8): dtype E4M3 for A, B holds packed E2M1 codes (K / 2
-  // bytes a row)
-  int w4 = 0;
-  // programmatic dependent launch mode of the kernel (PDL_*; dgl_gemm_batch)
-  int pdl_mode = PDL_SERIAL;
-};
-
 dgl_status validate(Problem& pr) {
   if (pr.dtype != DGL_DTYPE_BF16 && pr.dtype != DGL_DTYPE_E4M3) return DGL_ERR_ARG;
   if (pr.out != DGL_OUT_BF16 && pr.out != DGL_OUT_F32) return DGL_ERR_ARG;
@@ -425,7 +394,7 @@ dgl_status validate(Problem& pr) {
   if (pr.K == 0) return DGL_OK;  // empty sum: zero fill, operands unused
   if (!pr.A || !pr.B) return DGL_ERR_ARG;
   const int64_t esize = pr.dtype == DGL_DTYPE_E4M3 ? 1 : 2;
-  if ((pr.K * esize) % 16 != 0) return DGL_ERR_ALIGN;
+  if (!(pr.k_any && pr.a_mn && pr.b_mn) && (pr.K * esize) % 16 != 0) return DGL_ERR_ALIGN;
   if (!aligned(pr.A, 16) || !aligned(pr.B, 16)) return DGL_ERR_ALIGN;
   // packed 4-bit B: whole 128-element boxes along K, a 32-byte-aligned base
   // (the tensor-map rules of the 16U4_ALIGN16B type)
@@ -448,7 +417,7 @@ dgl_status validate(Problem& pr) {
   return DGL_OK;
 }
 
-dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, StaticScratch* fixed = nullptr) {
+dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, StaticScratch* fixed) {
   dgl_status st = validate(pr);
   if (st != DGL_OK) return st;
   if (pr.m == 0 || pr.n == 0) return DGL_OK;
@@ -577,7 +546,7 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
   const bool map_ok =
       (pr.a_mn ? cached_operand_map_mn(&ta, pr.A, pr.m, pr.K, pr.lda)
                : cached_operand_map(&ta, pr.A, e4m3, pr.K, pr.m, plan.tile_m == 64 ? 64 : 128, pr.lda)) &&
-      (pr.b_mn ? cached_operand_map_mn(&tb, pr.B, b_rows, pr.K, pr.ldb)
+      (pr.b_mn ? cached_operand_map_mn(&tb, pr.B, b_rows, pr.b_k ? pr.b_k : pr.K, pr.ldb)
                : cached_b_map(&tb, pr.B, e4m3, pr.w4, pr.K, b_rows, plan.tile_n / cg, pr.ldb));
   if (!map_ok) return DGL_ERR_CUDA;
   // B with half-height boxes, for the half tiles of a split tail (else unused)
@@ -587,6 +556,8 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
     return DGL_ERR_CUDA;
   const bool f32 = pr.out == DGL_OUT_F32;
   const bool c_tma = aligned(pr.C, 16) && (pr.N * (f32 ? 4 : 2)) % 16 == 0;
+  // adding to C is done by the TMA stores: fp32 rows of whole 16-byte units
+  if (pr.c_add && (!f32 || !c_tma || pr.n % 4 != 0)) return DGL_ERR_UNSUPPORTED;
   std::memset(&tc, 0, sizeof(tc));
   if (c_tma && !cached_output_map(&tc, pr.C, f32, pr.n, pr.m, pr.N, plan.tile_m == 64 ? 16 : 32)) return DGL_ERR_CUDA;
   TcParams p;
@@ -605,6 +576,7 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
   p.num_kb = static_cast<int>((pr.K * esize + 127) / 128);
   p.group_m = 16;
   p.c_tma = c_tma ? 1 : 0;
+  p.c_add = pr.c_add;
   p.status = ds->status;
   p.bias = pr.bias;
   p.act = pr.act;
@@ -619,7 +591,7 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
   // A split schedule needs the stream's workspace.  A stream being captured
   // into a CUDA graph cannot have one allocated, so a captured call on a
   // stream without one runs the data-parallel schedule instead.
-  bool split = plan.stream_k != 0;
+  bool split = plan.stream_k != 0 && !pr.no_split;
   if (split && !fixed) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return DGL_ERR_CUDA;
@@ -680,6 +652,14 @@ dgl_status run(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, Sta
              : launch_tc_bf16(pr.out, plan.tile_m, plan.tile_n, row_staging, ta, tb, tbh, tc, p, grid, stream);
   return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
 }
+
+}  // namespace
+
+dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stream) {
+  return run_impl(pr, forced, stream, nullptr);
+}
+
+namespace {
 
 // Block-scaled FP4 (MXFP4): A and B as byte tensors of K / 2 bytes per row
 // (TMA moves the packed E2M1 codes untouched), E8M0 scales read by the
@@ -1009,7 +989,7 @@ dgl_status dgl_gemm_noalloc(int32_t dtype, const void* A, const void* B, const f
   plan.stream_k = plan.path == DGL_PATH_TC ? 1 : 0;
   plan.grid = 0;
   plan.tile_k = 0;
-  return run(pr, &plan, static_cast<cudaStream_t>(stream), sc);
+  return run_impl(pr, &plan, static_cast<cudaStream_t>(stream), sc);
 }
 
 dgl_status dgl_shutdown(void) {

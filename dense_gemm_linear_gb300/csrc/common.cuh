@@ -39,6 +39,7 @@ struct TcParams {
   int tiles_m, tiles_n, num_tiles, num_kb;
   int group_m;          // tile raster: group_m row-tiles share each column sweep
   int c_tma;            // 1: C is written by TMA tensor stores (16-byte aligned pitch and base)
+  int c_add;            // 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
   int* status;          // device status word
   // Schedule.  `workers` CTAs (or CTA pairs) run at once.  Tiles below
   // dp_tiles run whole, worker w taking w, w + workers, ...  The remaining

@@ -340,6 +340,107 @@ dgl_status dgl_linear(int32_t dtype, const void* A, const void* B, const float* 
                       int32_t out_dtype, int32_t act, int32_t gated, const dgl_plan_info* plan, void* stream);
 
 /*
+ * The losses of a language-model head.  The head is the last linear layer,
+ * W [V, d] over a vocabulary of V tokens (the lm_head shape 1024 x 50257 x 512
+ * of the ragged-shape set); its logits feed a loss and are needed nowhere
+ * else.  These calls compute the loss, and when asked its gradient, without
+ * keeping the T x V logits: with hidden states x_t (rows of X) and s the
+ * logit scale,
+ *     z_tv = s x_t . w_v,   lse_t = log sum_v exp(z_tv),   p_tv = exp(z_tv - lse_t)
+ *   dgl_linear_xent     loss_t = lse_t - z_{t, target_t}
+ *                       dz_tv  = grad_t (p_tv - [v == target_t])
+ *   dgl_linear_distill  loss_t = sum_k q_tk (log q_tk - z_{t, i_tk} + lse_t)
+ *                       dz_tv  = grad_t (Q_t p_tv - sum_{k: i_tk == v} q_tk),  Q_t = sum_k q_tk
+ *   both                dX = s dz W,   dW = s dz^T X
+ * grad_t is dL / dloss_t, known before the call (1 / tokens for a mean).
+ *
+ * Fields.  T, V, d: tokens, vocabulary, width (d > 0 a multiple of 8, V > 0).
+ *   X: bf16, T rows of d, row pitch ldx elements; W: bf16, V rows of d, pitch
+ *   ldw (pitches 0 = d, else at least d and a multiple of 8; bases 16-byte
+ *   aligned).
+ *   logit_scale: s (finite).
+ *   loss: fp32 [T].  lse: fp32 [T], or NULL.
+ *   grad: fp32 [T], or NULL for the forward pass alone (dX and dW then NULL).
+ *   dX: bf16, T rows, pitch lddx, or NULL; dW: V rows, pitch lddw, of
+ *   dw_dtype (DGL_OUT_BF16 or DGL_OUT_F32), or NULL (with grad at least one of
+ *   the two; bases 16-byte aligned, pitches as X's).
+ *   accumulate: 1 adds to the fp32 dW instead of replacing it (micro-batches).
+ *   ws, ws_bytes: device scratch, 256-byte aligned, at least the minimum that
+ *   dgl_head_workspace reports.  Tokens are taken in chunks that fit it, so
+ *   its size bounds the memory of a call whatever T is; the largest useful
+ *   size is the one reported as best.  Its contents mean nothing between
+ *   calls.
+ *
+ * Accuracy.  Products and sums are fp32, statistics and losses fp32.  The
+ * gradient's dz is rounded once to bf16 (relative 2^-9 an entry, entries of a
+ * target included: they are formed as a sum of the others, not as p - 1), as
+ * the operand of the two products; dX and a bf16 dW are rounded once more.
+ *
+ * Rows without a target.  dgl_linear_xent: target_t == ignore_index gives loss
+ * 0 and no gradient, whatever x_t holds (NaN and infinities included: the row
+ * does not reach dW, and its dX row is zero).  Any other target outside
+ * [0, V) gives a NaN loss and no gradient.  dgl_linear_distill: an entry with
+ * a negative index is absent, its logit is not looked at; a row with no
+ * entries, or none above -infinity, has loss 0 and no gradient; an index >= V
+ * makes the row's loss NaN, without gradient.  lse is reported for every row.
+ */
+typedef struct dgl_head_desc {
+  int64_t T, V, d;
+  const void* X;
+  int64_t ldx;
+  const void* W;
+  int64_t ldw;
+  float* loss;
+  float* lse;
+  const float* grad;
+  void* dX;
+  int64_t lddx;
+  void* dW;
+  int64_t lddw;
+  void* ws;
+  int64_t ws_bytes;
+  float logit_scale;
+  int32_t dw_dtype;
+  int32_t accumulate;
+} dgl_head_desc;
+
+/* Entries a row of teacher logits may have. */
+#define DGL_DISTILL_MAX_K 128
+
+/*
+ * Scratch sizes of a call: *min_bytes, below which it is refused, and
+ * *best_bytes, above which more changes nothing.  Reads T, V, d, dw_dtype,
+ * and whether grad, dX and dW are NULL.  k: entries a row of the teacher's
+ * (0 for dgl_linear_xent).  Pure host logic.
+ */
+dgl_status dgl_head_workspace(const dgl_head_desc* head, int32_t k, int64_t* min_bytes, int64_t* best_bytes);
+
+/*
+ * Softmax cross entropy of a linear head.  target: int64 [T], a row of W each,
+ * or ignore_index.  Enqueues work on `stream` only, allocates nothing, and may
+ * be captured into a CUDA graph.  T == 0 writes a zero dW (unless accumulate)
+ * and nothing else.  Errors: DGL_ERR_ARG (null pointers, negative extents,
+ * V or d of 0, a scale that is not finite, accumulate without an fp32 dW, a
+ * workspace below the minimum), DGL_ERR_ALIGN, DGL_ERR_SHAPE (extents past
+ * 2^31 - 1), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.
+ */
+dgl_status dgl_linear_xent(const dgl_head_desc* head, const int64_t* target, int64_t ignore_index, void* stream);
+
+/*
+ * Distillation of a linear head from a teacher's top logits.  indices: int64
+ * [T][k], rows of W or negative for an absent entry; logits: fp32 [T][k], the
+ * teacher's logits of those entries; 1 <= k <= DGL_DISTILL_MAX_K.  Both
+ * distributions are taken at `temperature` (> 0): the student's logits are
+ * z / temperature, and lse is theirs.  teacher_lse NULL: q_t is the softmax of
+ * the row's entries, which then sum to one.  teacher_lse fp32 [T]: the
+ * teacher's log-normaliser over its whole vocabulary at that temperature, and
+ * q_tk = exp(logit / temperature - teacher_lse_t), which sum to the kept mass
+ * Q_t.  An index given twice counts twice.  Errors as dgl_linear_xent.
+ */
+dgl_status dgl_linear_distill(const dgl_head_desc* head, const int64_t* indices, const float* logits,
+                              const float* teacher_lse, int32_t k, float temperature, void* stream);
+
+/*
  * The plan the library would use for a problem of m x n x K (valid extents)
  * on a device with num_sms SMs (num_sms <= 0: query the current device).
  * Pure host logic when num_sms > 0: needs no GPU.
