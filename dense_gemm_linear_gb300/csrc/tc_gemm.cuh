@@ -829,12 +829,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (tma_ok) {
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0 && row0 < p.m && col0 < p.n) {
-              if (Cfg::OUT_F32 && p.c_add)
-                tma_reduce_add_2d(&tmC, stg_u, col0, row0);
-              else
-                tma_store_2d(&tmC, stg_u, col0, row0);
-              bulk_commit();
+            if (lane == 0) {
+              if (row0 < p.m && col0 < p.n) {
+                if (Cfg::OUT_F32 && p.c_add)
+                  tma_reduce_add_2d(&tmC, stg_u, col0, row0);
+                else
+                  tma_store_2d(&tmC, stg_u, col0, row0);
+              }
+              bulk_commit();  // an empty group too: the waits above count groups
             }
           } else {
             __syncwarp();
