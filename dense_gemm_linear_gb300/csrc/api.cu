@@ -151,12 +151,8 @@ static __device__ __align__(256) uint8_t g_noalloc_scratch[DGL_NOALLOC_SCRATCH_B
 // The array as this device sees it.  Host code cannot use the array's name as
 // an address (it stands for a host-side shadow), so set-up asks the runtime
 // for the device address once per device, with that device current.
-struct StaticScratch {
+struct StaticScratch : SplitScratch {
   bool ready = false;
-  float* ws = nullptr;
-  size_t ws_bytes = 0;
-  int* flags = nullptr;
-  int nflags = 0;
 };
 StaticScratch g_noalloc[kMaxDevices];
 std::mutex g_noalloc_mu;  // set-up of g_noalloc
@@ -417,7 +413,7 @@ dgl_status validate(Problem& pr) {
   return DGL_OK;
 }
 
-dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, StaticScratch* fixed) {
+dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream, const SplitScratch* fixed) {
   dgl_status st = validate(pr);
   if (st != DGL_OK) return st;
   if (pr.m == 0 || pr.n == 0) return DGL_OK;
@@ -560,7 +556,7 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   if (pr.c_add && (!f32 || !c_tma || pr.n % 4 != 0)) return DGL_ERR_UNSUPPORTED;
   std::memset(&tc, 0, sizeof(tc));
   if (c_tma && !cached_output_map(&tc, pr.C, f32, pr.n, pr.m, pr.N, plan.tile_m == 64 ? 16 : 32)) return DGL_ERR_CUDA;
-  TcParams p;
+  TcParams p = {};
   p.C = pr.C;
   p.ldc = pr.N;
   p.m = static_cast<int>(pr.m);
@@ -655,8 +651,16 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
 
 }  // namespace
 
-dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stream) {
-  return run_impl(pr, forced, stream, nullptr);
+dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stream, const SplitScratch* scratch) {
+  return run_impl(pr, forced, stream, scratch);
+}
+
+bool bf16_operand_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows, int64_t pitch) {
+  return cached_operand_map(map, base, false, inner, rows, box_rows, pitch);
+}
+
+bool bf16_output_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t ldc) {
+  return cached_output_map(map, base, false, cols, rows, ldc);
 }
 
 namespace {

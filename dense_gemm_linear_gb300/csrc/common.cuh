@@ -29,6 +29,33 @@ enum : int {
 // the one before it and writes C after it.
 enum : int { PDL_SERIAL = 0, PDL_BATCH_HEAD = 1, PDL_BATCH_NEXT = 2 };
 
+// Epilogue of a linear head's logits (tile kernel variants with HEAD set).
+// The tile's accumulators are logits up to the factor `scale`; in units of
+// log 2 they are y = acc c, c = scale log2(e).  A warp holds 32 rows by one
+// column group (half a tile's columns); per row and group it leaves in part
+// the largest y, Y, and the sum of 2^(y - Y + kHeadShift), and with `store`
+// writes 2^(y - Y + kHeadShift) in fp16 as the tile's output.
+struct HeadEpi {
+  float c;      // scale log2(e); its sign is applied to the accumulators first
+  int store;
+  float2* part;  // [rows][part_ld] (Y, sum) per column group
+  int part_ld;
+  // Accumulators to pick out of the tile, [rows][k] into pick: one target per
+  // row (start null; others than 0 .. n - 1 are not picked), or the row's k
+  // sorted columns, of which group g holds number start[row][g] up to
+  // start[row][g + 1].
+  const int64_t* target;
+  const int* column;
+  const uint8_t* start;
+  int start_ld;
+  int k;
+  float* pick;
+};
+
+// fp16 holds the exponentials of a group with its 11 bits from the largest,
+// 2^15, down to 2^-14, 2^-29 of the largest; what is below 2^-40 of it is zero.
+constexpr float kHeadShift = 15.0f;
+
 // Persistent tcgen05 tile kernel: problem and schedule.
 struct TcParams {
   void* C;              // output, row pitch ldc elements
@@ -91,6 +118,7 @@ struct TcParams {
   // Programmatic dependent launch (PDL_*): where the kernel waits for the
   // previous kernel on the stream and when it lets the next one launch
   int pdl_mode;
+  HeadEpi head;  // HEAD variants only
 };
 
 // Decode (m <= 16) kernel parameters.  A and B are read through tensor maps.

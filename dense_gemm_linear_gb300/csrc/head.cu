@@ -1,26 +1,41 @@
 // Losses of a linear head (dgl_linear_xent, dgl_linear_distill): validation,
 // workspace, the per-row kernels and the calls into the tile kernel.
 //
-// Tokens are taken in chunks.  A chunk's logits z = s X W^T are computed by
-// the tile kernel, one block per row then reduces the row to its loss and
-// writes dz, and two more products of the tile kernel give dX and dW.
+// Tokens are taken in chunks.  In units of log 2, with y = s log2(e) x . w:
+//   prepare  (distill; one warp per row) the teacher's weights q, sorted by column
+//   logits   (tile kernel, HEAD) y in fp32, never stored: per row and group of
+//            columns its largest Y and the sum of 2^(y - Y), the y of the
+//            targets, and for a gradient e = 2^(y - Y) in fp16
+//   finish   (one block per row) S = sum e, lse, loss, and for the gradient
+//            dz = grad s (Q e / S - q) in bf16 in the place of e
+//   dX = dz W, dW = dz^T x  (tile kernel)
+// T x V values take 2 bytes of workspace for the chunk's tokens, are written
+// twice and read three times; the three products are 6 T V d operations.
+// e needs the 11 bits of fp16 because it is rounded again, as dz, once S is
+// known (in bf16 its rounding would add to dz's); a group's own maximum keeps
+// it in fp16's range whatever the logits are.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
 #include "dgl.h"
 #include "host.h"
 #include "launch.h"
+#include "plan.h"
+#include "ptx.cuh"
 
 namespace dgl {
 
 namespace {
 
 constexpr int kMaxK = DGL_DISTILL_MAX_K;
-constexpr int kRowThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // What a row asks of the softmax: xent (k == 0) one target, distill k entries.
 struct HeadTargets {
@@ -30,6 +45,18 @@ struct HeadTargets {
   const float* teacher_lse;  // distill: [T] or null
   float inv_temp;            // distill
   int k;                     // 0: xent
+};
+
+// A chunk's rows: what `prepare` (distill only) and the logits' epilogue leave.
+struct HeadRows {
+  int* column;       // [rows][k] kept entries sorted by column, then INT_MAX
+  float* q;          // [rows][k] their weights
+  float4* sums;      // [rows] Q, sum q log q, state (1: has a loss, 0: none, -1: index out of range), 0
+  uint8_t* start;    // [rows][start_ld] entries before each column group
+  int start_ld, group_cols;
+  float* pick;       // [rows][max(k, 1)] accumulators of the entries
+  float2* part;      // [rows][groups] (largest y, sum of the exponentials)
+  int groups;
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -43,152 +70,239 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One row's entries: index (or -1), weight q and q log q, prepared by warp 0
-// into shared memory.  state: 1 a row with a loss, 0 no entries, -1 an index
-// out of range.
-struct RowEntries {
-  int index[kMaxK];
-  float q[kMaxK];
-  float qlogq, Q;
-  int state;
-};
+constexpr int kPrepareWarps = 4;
 
-__device__ __forceinline__ void load_entries(RowEntries& r, const HeadTargets& tg, int64_t t, int64_t V, int lane) {
-  if (tg.k == 0) {
-    if (lane == 0) {
-      const int64_t y = tg.index[t];
-      const bool in = y >= 0 && y < V;
-      r.state = y == tg.ignore_index ? 0 : in ? 1 : -1;
-      r.index[0] = r.state == 1 ? static_cast<int>(y) : -1;
-      r.q[0] = r.state == 1 ? 1.0f : 0.0f;
-      r.Q = r.q[0];
-      r.qlogq = 0.0f;
-    }
-    return;
-  }
-  // the teacher's distribution, its maximum and sum in fp32
+// Distill, one warp per row: the teacher's distribution over the row's entries
+// in fp32 (maximum first), the entries sorted by column, and the number of them
+// before each column group.
+__global__ void __launch_bounds__(32 * kPrepareWarps)
+    head_prepare_kernel(HeadTargets tg, HeadRows rows, int n, int V) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int PER = kMaxK / 32;
+  __shared__ int s_col[kPrepareWarps][kMaxK];
+  __shared__ int s_sorted[kPrepareWarps][kMaxK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * kPrepareWarps + warp;
+  if (row >= n) return;
+  const int k = tg.k;
+  int col[PER];
+  float l[PER];
   float high = -INFINITY;
-  int bad = 0;
-  for (int j = lane; j < tg.k; j += 32) {
-    const int64_t i = tg.index[t * tg.k + j];
-    bad |= i >= V;
-    const bool kept = i >= 0 && i < V;
-    const float l = kept ? tg.logits[t * tg.k + j] * tg.inv_temp : -INFINITY;
-    r.index[j] = kept ? static_cast<int>(i) : -1;
-    r.q[j] = l;
-    // a NaN logit of a kept entry has to reach the loss: fmaxf drops it, the
-    // sum below does not
-    high = fmaxf(high, l);
+  bool bad = false, some = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = lane + 32 * i;
+    col[i] = INT_MAX;
+    l[i] = -INFINITY;
+    if (j < k) {
+      const int64_t c64 = tg.index[static_cast<int64_t>(row) * k + j];
+      bad |= c64 >= V;
+      if (c64 >= 0 && c64 < V) {
+        const float v = tg.logits[static_cast<int64_t>(row) * k + j] * tg.inv_temp;
+        if (!(v == -INFINITY)) {  // minus infinity: no probability; NaN stays, and reaches the loss
+          col[i] = static_cast<int>(c64);
+          l[i] = v;
+          high = fmaxf(high, v);
+          some = true;
+        }
+      }
+    }
   }
-  high = warp_max(high);
   bad = __any_sync(0xffffffffu, bad);
-  const float base = tg.teacher_lse ? tg.teacher_lse[t] : high;
-  float sum = 0.0f;
-  bool some = false;
-  for (int j = lane; j < tg.k; j += 32) {
-    const float l = r.q[j];
-    const bool here = r.index[j] >= 0 && !(l == -INFINITY);
-    some |= here;
-    sum += here ? expf(l - base) : 0.0f;
-  }
-  sum = warp_sum(sum);
   some = __any_sync(0xffffffffu, some);
+  high = warp_max(high);
+  const float base = tg.teacher_lse ? tg.teacher_lse[row] : high;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += col[i] != INT_MAX ? expf(l[i] - base) : 0.0f;
+  sum = warp_sum(sum);
   const float log_total = tg.teacher_lse ? base : base + logf(sum);
   float Q = 0.0f, qlogq = 0.0f;
-  for (int j = lane; j < tg.k; j += 32) {
-    const float l = r.q[j];
-    const bool here = r.index[j] >= 0 && !(l == -INFINITY);
-    const float lq = l - log_total;
-    const float q = here ? expf(lq) : 0.0f;
-    r.q[j] = q;
-    Q += q;
-    qlogq += q != 0.0f ? q * lq : 0.0f;
+  float q[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float lq = l[i] - log_total;
+    q[i] = col[i] != INT_MAX ? expf(lq) : 0.0f;
+    Q += q[i];
+    qlogq += q[i] != 0.0f ? q[i] * lq : 0.0f;
   }
   Q = warp_sum(Q);
   qlogq = warp_sum(qlogq);
-  if (lane == 0) {
-    r.state = bad ? -1 : some ? 1 : 0;
-    r.Q = Q;
-    r.qlogq = qlogq;
+  const int state = bad ? -1 : some ? 1 : 0;
+  if (lane == 0) rows.sums[row] = make_float4(Q, qlogq, static_cast<float>(state), 0.0f);
+  // sort by (column, position): an entry's place is the number before it
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (state != 1) col[i] = INT_MAX;
+    s_col[warp][lane + 32 * i] = col[i];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = lane + 32 * i;
+    if (j < k) {
+      int place = 0;
+      for (int o = 0; o < k; ++o) {
+        const int other = s_col[warp][o];
+        place += other < col[i] || (other == col[i] && o < j);
+      }
+      s_sorted[warp][place] = col[i];
+      rows.column[static_cast<int64_t>(row) * k + place] = col[i];
+      rows.q[static_cast<int64_t>(row) * k + place] = q[i];
+    }
+  }
+  __syncwarp();
+  for (int g = lane; g < rows.start_ld; g += 32) {
+    // entries with a column below the group's first one (the last group ends past V)
+    const int64_t below = static_cast<int64_t>(g) * rows.group_cols;
+    int lo = 0, hi = k;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (s_sorted[warp][mid] < below && s_sorted[warp][mid] != INT_MAX)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    rows.start[static_cast<int64_t>(row) * rows.start_ld + g] = static_cast<uint8_t>(lo);
   }
 }
 
-// One block per row of a chunk: z (fp32, scaled here by `scale`) -> loss, lse
-// and, with dz, the row of dz in bf16, zero from V to V8, and the row of X for
-// dW = dz^T X, zero where the row has no gradient (0 x NaN would reach dW).
-__global__ void __launch_bounds__(kRowThreads)
-    head_row_kernel(const float* __restrict__ z, int64_t ldz, __nv_bfloat16* __restrict__ dz, int64_t lddz, int64_t t0,
-                    int64_t V, float scale, HeadTargets tg, const float* __restrict__ grad, float* __restrict__ loss,
-                    float* __restrict__ lse_out, const __nv_bfloat16* __restrict__ x, int64_t ldx,
-                    __nv_bfloat16* __restrict__ xs, int64_t d) {
-  __shared__ RowEntries ent;
-  __shared__ float red[2][kRowThreads / 32];
-  const int64_t t = t0 + blockIdx.x;
-  const float* row = z + static_cast<int64_t>(blockIdx.x) * ldz;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) load_entries(ent, tg, t, V, lane);
+constexpr int kFinishThreads = 256;
+
+// One block per row: statistics of the row's column groups -> loss and lse;
+// with e (gradient), e -> dz in place (zero up to V8), and x for dW = dz^T x,
+// zero where the row has no gradient (0 x NaN would reach dW).
+__global__ void __launch_bounds__(kFinishThreads)
+    head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
+                       float* __restrict__ loss, float* __restrict__ lse_out, uint16_t* __restrict__ e, int64_t lde,
+                       const __nv_bfloat16* __restrict__ x, int64_t ldx, __nv_bfloat16* __restrict__ xs, int d,
+                       int* __restrict__ flags, int nflags) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int WARPS = kFinishThreads / 32;
+  __shared__ float red[2][WARPS];
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (row == 0)
+    for (int i = threadIdx.x; i < nflags; i += kFinishThreads) flags[i] = 0;
+  const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
   float m = -INFINITY, s = 0.0f;
-  for (int64_t v = threadIdx.x; v < V; v += kRowThreads) {
-    const float x = row[v] * scale;
-    if (x > m) {
-      s = s * expf(m - x) + 1.0f;
-      m = x;
-    } else {
-      s += x == m ? 1.0f : expf(x - m);  // equal infinities count as one each
-    }
+  for (int g = threadIdx.x; g < rows.groups; g += kFinishThreads) {
+    const float2 v = part[g];
+    const float top = fmaxf(m, v.x);
+    // a group without a maximum sums to zero, or to NaN
+    s = top == -INFINITY ? s + v.y : s * exp2f(m - top) + v.y * exp2f(v.x - top);
+    m = top;
   }
   const float wm = warp_max(m);
-  s = warp_sum(m == wm ? s : s * expf(m - wm));
+  s = warp_sum(wm == -INFINITY ? s : s * exp2f(m - wm));
   if (lane == 0) {
     red[0][warp] = wm;
     red[1][warp] = s;
   }
   __syncthreads();
-  float bm = red[0][0], bs = 0.0f;
-  for (int w = 1; w < kRowThreads / 32; ++w) bm = fmaxf(bm, red[0][w]);
-  for (int w = 0; w < kRowThreads / 32; ++w) bs += red[0][w] == bm ? red[1][w] : red[1][w] * expf(red[0][w] - bm);
-  const float lse = bm + logf(bs);
-  const int nk = tg.k == 0 ? 1 : tg.k;
-  if (threadIdx.x == 0) {
-    if (lse_out) lse_out[t] = lse;
-    float l = 0.0f;
-    if (ent.state == 1) {
-      l = ent.qlogq;
-      for (int j = 0; j < nk; ++j)
-        if (ent.q[j] != 0.0f) l += ent.q[j] * (lse - row[ent.index[j]] * scale);
-    }
-    loss[t] = ent.state < 0 ? NAN : l;
+  float base = red[0][0], S = 0.0f;
+#pragma unroll
+  for (int i = 1; i < WARPS; ++i) base = fmaxf(base, red[0][i]);
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) S += red[0][i] == -INFINITY ? red[1][i] : red[1][i] * exp2f(red[0][i] - base);
+  S *= exp2f(-kHeadShift);  // relative to 2^base
+  const float log_S = log2f(S);
+
+  // the row's targets
+  int state;
+  float Q = 1.0f, l = 0.0f;
+  const int k = tg.k == 0 ? 1 : tg.k;
+  const float* pick = rows.pick + static_cast<int64_t>(row) * k;
+  const int* column = tg.k == 0 ? nullptr : rows.column + static_cast<int64_t>(row) * k;
+  const float* q = tg.k == 0 ? nullptr : rows.q + static_cast<int64_t>(row) * k;
+  int64_t y0 = 0;
+  if (tg.k == 0) {
+    y0 = tg.index[row];
+    state = y0 == tg.ignore_index ? 0 : y0 >= 0 && y0 < V ? 1 : -1;
+  } else {
+    const float4 sums = rows.sums[row];
+    Q = sums.x;
+    l = sums.y;
+    state = static_cast<int>(sums.z);
   }
-  if (!dz) return;
-  __nv_bfloat16* out = dz + static_cast<int64_t>(blockIdx.x) * lddz;
-  const bool live = ent.state == 1;
-  const float g = live ? grad[t] * scale : 0.0f;
-  const int64_t V8 = (V + 7) / 8 * 8;
-  for (int64_t v = threadIdx.x; v < V8; v += kRowThreads)
-    out[v] = __float2bfloat16(live && v < V ? g * ent.Q * expf(row[v] * scale - lse) : 0.0f);
-  for (int64_t c = threadIdx.x; c < d / 8; c += kRowThreads)
-    reinterpret_cast<uint4*>(xs + blockIdx.x * d)[c] =
-        live ? reinterpret_cast<const uint4*>(x + blockIdx.x * ldx)[c] : make_uint4(0u, 0u, 0u, 0u);
-  if (!live) return;
-  // the entries' own values, one thread each; a repeated index is written by
-  // its first occurrence, with the sum of its weights
+  if (warp == 0) {
+    // sum_k q (lse - z_k) as base - y_k + log2 S: what a likely target's y has
+    // in common with the maximum cancels before anything is rounded
+    float t = 0.0f;
+    if (state == 1)
+      for (int j = lane; j < k; j += 32) {
+        if (tg.k != 0 && column[j] == INT_MAX) continue;
+        const float w = tg.k == 0 ? 1.0f : q[j];
+        if (w != 0.0f) t += w * ((base - pick[j] * c) + log_S);
+      }
+    t = warp_sum(t);
+    if (lane == 0) {
+      if (lse_out) lse_out[row] = (base + log_S) * kLn2;
+      loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : fmaf(t, kLn2, l);
+    }
+  }
+  if (!e) return;
+
+  const bool has = state == 1;
+  const float f = has ? grad[row] * scale : 0.0f;
+  const float fS = f * (Q / S);
+  uint16_t* er = e + row * lde;
+  const int V8 = (V + 7) / 8;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < V8; i += kFinishThreads) {
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (has) {
+      const uint4 v = reinterpret_cast<const uint4*>(er)[i];
+      const float a = fS * exp2f((part[8 * i / rows.group_cols].x - base) - kHeadShift);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      uint32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(p2.x * a, p2.y * a);
+        r[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      o = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    reinterpret_cast<uint4*>(er)[i] = o;
+  }
+  const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+  uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
+  for (int i = threadIdx.x; i < d / 8; i += kFinishThreads) xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
+  if (!has) return;
   __syncthreads();
-  for (int j = threadIdx.x; j < nk; j += kRowThreads) {
-    const int i = ent.index[j];
-    if (i < 0) continue;
-    bool first = true;
-    float q = 0.0f;
-    for (int l = 0; l < nk; ++l) {
-      if (ent.index[l] != i) continue;
-      if (l < j) first = false;
-      q += ent.q[l];
+  for (int j = threadIdx.x; j < k; j += kFinishThreads) {
+    int64_t v = y0;
+    float w = 1.0f;
+    if (tg.k != 0) {
+      // entries of one column are neighbours: the first carries their weights
+      v = column[j];
+      if (v == INT_MAX || (j > 0 && column[j - 1] == v)) continue;
+      w = 0.0f;
+      for (int o = j; o < k && column[o] == v; ++o) w += q[o];
     }
-    if (!first) continue;
-    const float p = expf(row[i] * scale - lse);
-    // xent: p - 1 as minus the sum of the others would need them; expm1 of
-    // the log-probability is as exact
-    out[i] = __float2bfloat16(g * (tg.k == 0 ? expm1f(row[i] * scale - lse) : ent.Q * p - q));
+    const float ev = exp2f(pick[j] * c - base);
+    // xent: minus the sum of the others, which is what p - 1 leaves of a sure target
+    const float dz = tg.k == 0 ? f * ((ev - S) / S) : f * (Q * (ev / S) - w);
+    er[v] = __bfloat16_as_ushort(__float2bfloat16(dz));
   }
+}
+
+// Launch of a kernel that starts with griddep_wait.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t stream,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
 __global__ void head_to_bf16_kernel(const float* __restrict__ src, int64_t lds, __nv_bfloat16* __restrict__ dst,
@@ -207,47 +321,68 @@ __global__ void head_to_bf16_kernel(const float* __restrict__ src, int64_t lds, 
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Chunk and workspace.  A chunk of c tokens needs c rows of fp32 logits and,
-// with a gradient, c rows of bf16 dz; more than one chunk accumulating a bf16
-// dW needs its fp32 sums.
+// Chunk and workspace.  Rows of a chunk hold e (gradient), the prepared rows
+// and the column groups' statistics; the gradient also needs x, the partial tiles of dX's split schedule and, when several chunks add up to a
+// bf16 dW, its fp32 sums.
 struct HeadLayout {
-  int64_t chunk = 0;    // tokens at a time
-  int64_t ldz = 0;      // row pitch of the logits and of dz, elements
-  int64_t z_off = 0, dz_off = 0, xs_off = 0, dw_off = 0, bytes = 0;
+  int64_t chunk = 0;  // tokens at a time (0: does not fit)
+  int64_t lde = 0;    // row pitch of e, elements
+  int64_t e = 0, xs = 0, pick = 0, part = 0, column = 0, q = 0, sums = 0, start = 0;
+  int64_t split = 0, flags = 0, dw = 0;
+  int64_t bytes = 0;
 };
 
-constexpr int64_t kChunkRows = 128;                // a chunk is a multiple of this
-constexpr int64_t kChunkBytes = int64_t(1) << 30;  // dz of the largest chunk
+constexpr int64_t kChunkRows = 128;  // a chunk is a multiple of this
+// The largest chunk: rows that fill every SM many times over, and with a
+// gradient e of at most 1 GiB.  Each further chunk of a gradient reads and
+// writes the fp32 sums of dW once more.
+constexpr int64_t kChunkBytes = int64_t(1) << 30;
+constexpr int64_t kChunkRowsMost = 32768;
+constexpr int kSplitSlots = 160;  // partial tiles of 128 x 256: one per CTA
 
-HeadLayout layout_for(const dgl_head_desc& h, int64_t chunk) {
+int64_t head_groups(int64_t V, int tile_n) { return 2 * ((V + tile_n - 1) / tile_n); }
+
+HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   HeadLayout l;
-  l.ldz = round_up(h.V, 64);
+  l.lde = round_up(h.V, 64);
   l.chunk = chunk;
   const bool grad = h.grad != nullptr;
-  const int64_t rows = std::min(round_up(chunk, kChunkRows), round_up(std::max<int64_t>(h.T, 1), kChunkRows));
+  const int64_t rows = std::min(chunk, round_up(std::max<int64_t>(h.T, 1), kChunkRows));
+  const int64_t groups = head_groups(h.V, 128);  // of the narrowest tile
   int64_t at = 0;
-  l.z_off = at;
-  at = round_up(at + rows * l.ldz * 4, 256);
-  l.dz_off = at;
-  if (grad) at = round_up(at + rows * l.ldz * 2, 256);
-  l.xs_off = at;
-  if (grad) at = round_up(at + rows * h.d * 2, 256);
-  l.dw_off = at;
-  if (grad && h.dW && h.dw_dtype == DGL_OUT_BF16 && chunk < h.T) at = round_up(at + h.V * h.d * 4, 256);
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at = round_up(at + bytes, 256);
+    return here;
+  };
+  if (grad) {
+    l.e = take(rows * l.lde * 2);
+    l.xs = take(rows * h.d * 2);
+    l.split = take(int64_t(kSplitSlots) * 128 * 256 * 4);
+    l.flags = take(kSplitSlots * 4);
+  }
+  l.part = take(rows * groups * 8);
+  l.pick = take(rows * std::max(k, 1) * 4);
+  if (k > 0) {
+    l.column = take(rows * k * 4);
+    l.q = take(rows * k * 4);
+    l.sums = take(rows * 16);
+    l.start = take(rows * (groups + 1));
+  }
+  if (grad && h.dW && h.dw_dtype == DGL_OUT_BF16 && chunk < h.T) l.dw = take(h.V * h.d * 4);
   l.bytes = at;
   return l;
 }
 
-// The largest chunk whose layout fits `bytes` (0 if none does).
-HeadLayout choose_layout(const dgl_head_desc& h, int64_t bytes) {
-  const int64_t ldz = round_up(h.V, 64);
-  const int64_t most = std::max<int64_t>(kChunkRows, kChunkBytes / (ldz * 2) / kChunkRows * kChunkRows);
-  HeadLayout best;
+// The largest chunk whose layout fits `bytes` (chunk 0 if none does).
+HeadLayout choose_layout(const dgl_head_desc& h, int k, int64_t bytes) {
+  const int64_t fit = kChunkBytes / (round_up(h.V, 64) * 2) / kChunkRows * kChunkRows;
+  const int64_t most = h.grad ? std::max(kChunkRows, std::min(fit, kChunkRowsMost)) : kChunkRowsMost;
   for (int64_t c = std::min(most, round_up(std::max<int64_t>(h.T, 1), kChunkRows)); c >= kChunkRows; c -= kChunkRows) {
-    const HeadLayout l = layout_for(h, c);
+    const HeadLayout l = layout_for(h, k, c);
     if (l.bytes <= bytes) return l;
   }
-  return best;
+  return HeadLayout{};
 }
 
 dgl_status check_extents(const dgl_head_desc* h, int32_t k) {
@@ -268,7 +403,26 @@ dgl_status check_matrix(const void* p, int64_t& ld, int64_t d) {
   return DGL_OK;
 }
 
-dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& tg, float scale, cudaStream_t stream) {
+// The tile of the logits' product: CTA pairs from 129 rows on.
+void logits_tile(int64_t rows, int& tile_m, int& tile_n) {
+  tile_m = rows > 128 ? 256 : 128;
+  tile_n = rows > 128 ? 256 : 128;
+}
+
+// dX's tile and schedule: few tiles with a long sum (V) are split along it.
+void choose_dx_plan(int64_t m, int64_t n, int64_t K, int num_sms, dgl_plan_info* out) {
+  bool have = false;
+  for (int tile_m : {128, 256})
+    for (int tile_n : {128, 256}) {
+      dgl_plan_info cand;
+      fill_tc_plan(DGL_DTYPE_BF16, DGL_OUT_BF16, m, n, K, tile_m, tile_n, num_sms, &cand, -1);
+      if (!have || cand.est_us <= out->est_us) *out = cand;
+      have = true;
+    }
+}
+
+dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float scale, cudaStream_t stream) {
+  HeadTargets tg = targets;
   dgl_status st = check_extents(hp, tg.k);
   if (st != DGL_OK) return st;
   dgl_head_desc h = *hp;
@@ -283,7 +437,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& tg, float scale,
   if (!aligned(h.loss, 4) || !aligned(h.lse, 4) || !aligned(h.grad, 4) || !aligned(tg.index, 8) ||
       !aligned(tg.logits, 4) || !aligned(tg.teacher_lse, 4))
     return DGL_ERR_ALIGN;
-  const HeadLayout lay = choose_layout(h, h.ws_bytes);
+  const HeadLayout lay = choose_layout(h, tg.k, h.ws_bytes);
   if (h.T > 0) {
     if (lay.chunk == 0 || !h.ws) return DGL_ERR_ARG;
     if (!aligned(h.ws, 256)) return DGL_ERR_ALIGN;
@@ -291,6 +445,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& tg, float scale,
   int dev = 0;
   DeviceState* ds = nullptr;
   if ((st = get_device(&dev, &ds)) != DGL_OK) return st;
+  if (ds->smem_optin < 232448) return DGL_ERR_UNSUPPORTED;  // every tile variant is sized for 227 KB
   if (h.T == 0) {
     if (!h.dW || h.accumulate) return DGL_OK;
     return launch_zero_fill(h.dw_dtype, h.dW, h.lddw, static_cast<int>(h.V), static_cast<int>(h.d), stream) ==
@@ -299,42 +454,104 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& tg, float scale,
                : DGL_ERR_CUDA;
   }
 
+  const bool grad = h.grad != nullptr;
   uint8_t* ws = static_cast<uint8_t*>(h.ws);
-  float* z = reinterpret_cast<float*>(ws + lay.z_off);
-  __nv_bfloat16* dz = h.grad ? reinterpret_cast<__nv_bfloat16*>(ws + lay.dz_off) : nullptr;
-  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(ws + lay.xs_off);
+  uint16_t* e = grad ? reinterpret_cast<uint16_t*>(ws + lay.e) : nullptr;
+  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(ws + lay.xs);
+  SplitScratch scratch;
+  scratch.ws = reinterpret_cast<float*>(ws + lay.split);
+  scratch.ws_bytes = size_t(kSplitSlots) * 128 * 256 * 4;
+  scratch.flags = reinterpret_cast<int*>(ws + lay.flags);
+  scratch.nflags = kSplitSlots;
+  const int V = static_cast<int>(h.V), d = static_cast<int>(h.d);
   const int64_t V8 = round_up(h.V, 8);
-  const bool chunked = lay.chunk < h.T;
+  const float c = scale * kLog2e;
   // a bf16 dW of several chunks is summed in fp32 and rounded once at the end
-  const bool dw_sums = h.dW && chunked && h.dw_dtype == DGL_OUT_BF16;
+  const bool dw_sums = h.dW && lay.chunk < h.T && h.dw_dtype == DGL_OUT_BF16;
   for (int64_t t0 = 0; t0 < h.T; t0 += lay.chunk) {
-    const int64_t n = std::min(lay.chunk, h.T - t0);
+    const int n = static_cast<int>(std::min(lay.chunk, h.T - t0));
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(h.X) + t0 * h.ldx;
-    Problem pz{DGL_DTYPE_BF16, DGL_OUT_F32, x, h.W, nullptr, nullptr, z, n, lay.ldz, h.d, n, h.V};
-    pz.no_split = 1;
-    pz.lda = h.ldx;
-    pz.ldb = h.ldw;
-    if ((st = run(pz, nullptr, stream)) != DGL_OK) return st;
-    head_row_kernel<<<static_cast<unsigned>(n), kRowThreads, 0, stream>>>(z, lay.ldz, dz, lay.ldz, t0, h.V, scale, tg,
-                                                                         h.grad, h.loss, h.lse, x, h.ldx, xs, h.d);
-    if (cudaGetLastError() != cudaSuccess) return DGL_ERR_CUDA;
+    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(h.W);
+    int tile_m, tile_n;
+    logits_tile(n, tile_m, tile_n);
+    tg.index = targets.index + t0 * std::max(tg.k, 1);
+    if (tg.k > 0) tg.logits = targets.logits + t0 * tg.k;
+    if (tg.teacher_lse) tg.teacher_lse = targets.teacher_lse + t0;
+    HeadRows rows = {};
+    rows.pick = reinterpret_cast<float*>(ws + lay.pick);
+    rows.part = reinterpret_cast<float2*>(ws + lay.part);
+    rows.groups = static_cast<int>(head_groups(h.V, tile_n));
+    rows.group_cols = tile_n / 2;
+    if (tg.k > 0) {
+      rows.column = reinterpret_cast<int*>(ws + lay.column);
+      rows.q = reinterpret_cast<float*>(ws + lay.q);
+      rows.sums = reinterpret_cast<float4*>(ws + lay.sums);
+      rows.start = ws + lay.start;
+      rows.start_ld = rows.groups + 1;
+    }
+
+    if (tg.k > 0 && launch_dependent(head_prepare_kernel, static_cast<unsigned>((n + kPrepareWarps - 1) / kPrepareWarps),
+                                     32 * kPrepareWarps, stream, tg, rows, n, V) != cudaSuccess)
+      return DGL_ERR_CUDA;
+
+    // ---- logits
+    const int cg = tile_m == 256 ? 2 : 1;
+    CUtensorMap ta, tb, tc = {};
+    if (!bf16_operand_map(&ta, x, h.d, n, 128, h.ldx) || !bf16_operand_map(&tb, w, h.d, h.V, tile_n / cg, h.ldw) ||
+        (grad && !bf16_output_map(&tc, e, V8, n, lay.lde)))
+      return DGL_ERR_CUDA;
+    TcParams p = {};
+    p.m = n;
+    p.n = V;
+    p.K = d;
+    p.tiles_m = (n + tile_m - 1) / tile_m;
+    p.tiles_n = static_cast<int>((h.V + tile_n - 1) / tile_n);
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    if (tiles > INT32_MAX) return DGL_ERR_SHAPE;
+    p.num_tiles = static_cast<int>(tiles);
+    p.num_kb = (d + 63) / 64;
+    p.group_m = 16;
+    p.c_tma = grad ? 1 : 0;
+    p.status = ds->status;
+    p.workers = std::min(p.num_tiles, ds->num_sms / cg);
+    p.dp_tiles = p.num_tiles;
+    p.sk_workers = p.workers;
+    p.pdl_mode = PDL_SERIAL;
+    p.head.c = c;
+    p.head.store = grad ? 1 : 0;
+    p.head.part = rows.part;
+    p.head.part_ld = rows.groups;
+    p.head.target = tg.k > 0 ? nullptr : tg.index;
+    p.head.column = rows.column;
+    p.head.start = rows.start;
+    p.head.start_ld = rows.start_ld;
+    p.head.k = std::max(tg.k, 1);
+    p.head.pick = rows.pick;
+    if (launch_tc_head(tile_m, tile_n, ta, tb, tc, p, p.workers * cg, stream) != cudaSuccess) return DGL_ERR_CUDA;
+
+    if (launch_dependent(head_finish_kernel, static_cast<unsigned>(n), kFinishThreads, stream, tg, rows, V, scale, c,
+                         grad ? h.grad + t0 : nullptr, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
+                         xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
+      return DGL_ERR_CUDA;
+
     if (h.dX) {
-      Problem px{DGL_DTYPE_BF16, DGL_OUT_BF16, dz, h.W, nullptr, nullptr,
+      Problem px{DGL_DTYPE_BF16, DGL_OUT_BF16, e, w, nullptr, nullptr,
                  static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx, n, h.lddx, V8, n, h.d};
-      px.no_split = 1;
       px.b_mn = 1;
-      px.lda = lay.ldz;
+      px.lda = lay.lde;
       px.ldb = h.ldw;
       px.b_k = h.V;
-      if ((st = run(px, nullptr, stream)) != DGL_OK) return st;
+      dgl_plan_info plan;
+      choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
+      if ((st = run(px, &plan, stream, &scratch)) != DGL_OK) return st;
     }
     if (h.dW) {
       const bool f32 = dw_sums || h.dw_dtype == DGL_OUT_F32;
-      Problem pw{DGL_DTYPE_BF16, f32 ? DGL_OUT_F32 : DGL_OUT_BF16, dz, xs, nullptr, nullptr,
-                 dw_sums ? static_cast<void*>(ws + lay.dw_off) : h.dW, h.V, dw_sums ? h.d : h.lddw, n, h.V, h.d};
+      Problem pw{DGL_DTYPE_BF16, f32 ? DGL_OUT_F32 : DGL_OUT_BF16, e, xs, nullptr, nullptr,
+                 dw_sums ? static_cast<void*>(ws + lay.dw) : h.dW, h.V, dw_sums ? h.d : h.lddw, n, h.V, h.d};
       pw.no_split = 1;
       pw.a_mn = pw.b_mn = 1;
-      pw.lda = lay.ldz;
+      pw.lda = lay.lde;
       pw.ldb = h.d;
       pw.k_any = 1;
       pw.c_add = (t0 > 0 || h.accumulate) ? 1 : 0;
@@ -342,7 +559,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& tg, float scale,
     }
   }
   if (dw_sums) {
-    head_to_bf16_kernel<<<ds->num_sms * 8, 256, 0, stream>>>(reinterpret_cast<const float*>(ws + lay.dw_off), h.d,
+    head_to_bf16_kernel<<<ds->num_sms * 8, 256, 0, stream>>>(reinterpret_cast<const float*>(ws + lay.dw), h.d,
                                                              static_cast<__nv_bfloat16*>(h.dW), h.lddw, h.V, h.d);
     if (cudaGetLastError() != cudaSuccess) return DGL_ERR_CUDA;
   }
@@ -360,8 +577,9 @@ dgl_status dgl_head_workspace(const dgl_head_desc* head, int32_t k, int64_t* min
   const dgl_status st = check_extents(head, k);
   if (st != DGL_OK) return st;
   if (!min_bytes || !best_bytes) return DGL_ERR_ARG;
-  *min_bytes = layout_for(*head, kChunkRows).bytes;
-  *best_bytes = choose_layout(*head, INT64_MAX).bytes;
+  // (one chunk of all tokens needs no sums of dW, so it may be the smaller)
+  *best_bytes = choose_layout(*head, k, INT64_MAX).bytes;
+  *min_bytes = std::min(layout_for(*head, k, kChunkRows).bytes, *best_bytes);
   return DGL_OK;
 }
 

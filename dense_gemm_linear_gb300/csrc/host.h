@@ -61,7 +61,23 @@ struct Problem {
   int c_add = 0;
 };
 
-// Validates, plans and enqueues one bf16 / E4M3 / W4A8 GEMM.
-dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stream);
+// Partial tiles and flags of a split schedule: flags zero before a launch, and
+// zero again after it.
+struct SplitScratch {
+  float* ws = nullptr;
+  size_t ws_bytes = 0;
+  int* flags = nullptr;
+  int nflags = 0;
+};
+
+// Validates, plans and enqueues one bf16 / E4M3 / W4A8 GEMM.  scratch: where
+// a split schedule keeps its partial tiles (null: the stream's own workspace).
+dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stream,
+               const SplitScratch* scratch = nullptr);
+
+// Tensor maps of a K-major bf16 operand (128-byte boxes of box_rows rows) and
+// of a bf16 output (32 x 32 boxes), from the cache.
+bool bf16_operand_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows, int64_t pitch);
+bool bf16_output_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t ldc);
 
 }  // namespace dgl

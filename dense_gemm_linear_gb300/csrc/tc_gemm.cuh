@@ -42,6 +42,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -60,12 +61,15 @@ constexpr int tc_ring_stages(int stage_bytes, int staging_bytes) {
 }
 
 template <int BN_, bool FP8_, bool OUT_F32_, bool ROWSTG_, int CG_ = 1, bool EPI_ = false, bool MX_ = false,
-          int BM_ = 128>
+          int BM_ = 128, bool HEAD_ = false>
 struct TcConfig {
   static constexpr int CG = CG_;                        // CTAs per MMA: 1, or 2 for a CTA pair (M = 256)
   // EPI: the linear-layer epilogue (bias, activation, and on CTA pairs the
   // gated up projection) is compiled in; plain GEMM variants leave it out.
   static constexpr bool EPI = EPI_;
+  // HEAD: the epilogue of a linear head's logits (HeadEpi) takes the place of
+  // the others'.
+  static constexpr bool HEAD = HEAD_;
   // Rows of C per CTA: 128, or 64 for the small rungs of the ladder (one CTA,
   // an M = 64 MMA).  An M = 64 accumulator puts row 16 q + r (r < 16) in
   // tensor-memory lane 32 q + r, so each epilogue warp of lane quarter q holds
@@ -140,6 +144,8 @@ struct TcConfig {
   static_assert(BN == 64 || BN == 128 || BN == 256 || (BN == 224 && CG == 2 && !EPI && !MX),
                 "tile widths of the ladder (224: plain GEMM on CTA pairs)");
   static_assert(BM == 128 || (BM == 64 && CG == 1 && !EPI && !MX), "64-row tiles: one CTA, plain GEMM");
+  static_assert(!HEAD || (!FP8_ && !EPI && !MX && !ROWSTG_ && !OUT_F32_ && BM_ == 128 && BN_ % 128 == 0),
+                "head variants: bf16 operands, TMA-stored 16-bit output");
   static_assert(STAGES >= 3, "ring too shallow");
   static_assert((ROW_PITCH / 16) % 2 == 1, "row pitch: odd multiple of 16 bytes");
   static_assert(TMEM_COLS == 128 || TMEM_COLS == 256 || TMEM_COLS == 512, "TMEM allocation: power of two");
@@ -297,6 +303,153 @@ __device__ __forceinline__ void next_acc(uint32_t& acc, uint32_t& acc_phase) {
   } else {
     acc_phase ^= 1;
   }
+}
+
+// Stores a warp's 32 x 32 chunk of 16-bit values (w[i]: this lane's row,
+// columns 2 i and 2 i + 1) as one TMA box at (col0, row0), through staging tile
+// `buf` of two: the store that last used the tile has finished reading it once
+// at most one later store is pending.
+template <class Cfg>
+__device__ __forceinline__ void store_chunk_16(const CUtensorMap* map, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
+                                               const uint32_t (&w)[16], int lane, int col0, int row0, bool any) {
+  const uint32_t a = stg_addr + buf * Cfg::STG_BYTES;
+  if (lane == 0) bulk_wait_read1();
+  __syncwarp();
+#pragma unroll
+  for (int c16 = 0; c16 < 4; ++c16)
+    sts_v4(a + stg_offset<64>(lane, c16), w[4 * c16], w[4 * c16 + 1], w[4 * c16 + 2], w[4 * c16 + 3]);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+    if (any) tma_store_2d(map, stg + buf * Cfg::STG_BYTES, col0, row0);
+    bulk_commit();  // an empty group too: the wait above counts them
+  }
+  buf ^= 1u;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One warp's share (32 rows x BN / 2 columns) of a tile of head logits: see
+// HeadEpi.  Two passes over the accumulators in tensor memory: the group's
+// largest value first, so that the second knows what its exponentials are
+// relative to before it stores any.  hand_back() releases the accumulator.
+template <class Cfg, class HandBack>
+__device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorMap* tmC, uint32_t t_row, int row0, int nb,
+                                              int half, int lane, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
+                                              HandBack hand_back) {
+  constexpr int GW = Cfg::BN / 2;       // columns of the group
+  constexpr int NC = GW / 32;           // its 32-column chunks, taken two at a time
+  const HeadEpi& h = p.head;
+  const int row = row0 + lane;
+  const bool in = row < p.m;
+  const int group = 2 * nb + half;
+  const int col0 = group * GW;
+  const float c = fabsf(h.c);
+  const bool flip = h.c < 0.0f;
+  const uint32_t t0 = t_row + half * GW;
+  // accumulators to pick: this row's first entry and how many it has here
+  int at = -1, first = 0, last = 0;
+  if (h.start) {
+    if (in) {
+      const uint8_t* st = h.start + static_cast<int64_t>(row) * h.start_ld + group;
+      first = st[0];
+      last = st[1];
+      if (first < last) at = h.column[static_cast<int64_t>(row) * h.k + first] - col0;
+    }
+  } else if (h.target && in) {
+    const int64_t y = h.target[row];
+    if (y >= col0 && y < min(col0 + GW, p.n)) {
+      at = static_cast<int>(y) - col0;
+      last = 1;
+    }
+  }
+  // Picked accumulators: the warp reads one column of all its rows at a time,
+  // the row that wants it keeps its own.
+  for (uint32_t want = __ballot_sync(0xffffffffu, first < last); want != 0;
+       want = __ballot_sync(0xffffffffu, first < last)) {
+    const int src = __ffs(want) - 1;
+    const uint32_t v = tmem_ld_32x32b_x1(t0 + __shfl_sync(0xffffffffu, at, src));
+    if (lane == src) {
+      h.pick[static_cast<int64_t>(row) * h.k + first] = __uint_as_float(v);
+      ++first;
+      if (first < last) at = h.column[static_cast<int64_t>(row) * h.k + first] - col0;
+    }
+  }
+
+  auto load = [&](uint32_t(&r)[2][32], int u) {
+    tmem_ld_32x32b_x32(t0 + u * 32, r[0]);
+    tmem_ld_32x32b_x32(t0 + u * 32 + 32, r[1]);
+    tmem_ld_wait();
+    reg_fence(r[0]);
+    reg_fence(r[1]);
+    if (flip) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[i][j] ^= 0x80000000u;
+    }
+  };
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int u = 0; u < NC; u += 2) {
+    uint32_t r[2][32];
+    load(r, u);
+    if (col0 + (u + 2) * 32 > p.n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col0 + (u + i) * 32 + j >= p.n) r[i][j] = 0xFF800000u;  // no such column: minus infinity
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m = fmaxf(m, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[1][j])));
+  }
+  const float top = m == -INFINITY ? m : m * c;
+  const float less = top == -INFINITY ? 0.0f : kHeadShift - top;
+
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int u = 0; u < NC; u += 2) {
+    uint32_t r[2][32];
+    load(r, u);
+    if (u + 2 >= NC) hand_back();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[i][j] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i][j]), c, less)));
+    if (col0 + (u + 2) * 32 > p.n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (col0 + (u + i) * 32 + j >= p.n) r[i][j] = 0u;
+    }
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      s0 += __uint_as_float(r[0][j]);
+      s1 += __uint_as_float(r[1][j]);
+    }
+    sum += s0 + s1;
+    if (h.store) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const __half2 h2 = __floats2half2_rn(__uint_as_float(r[i][2 * t]), __uint_as_float(r[i][2 * t + 1]));
+          w[t] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        const int col = col0 + (u + i) * 32;
+        store_chunk_16<Cfg>(tmC, stg, stg_addr, buf, w, lane, col, row0, row0 < p.m && col < p.n);
+      }
+    }
+  }
+  if (in) h.part[static_cast<int64_t>(row) * h.part_ld + group] = make_float2(top, sum);
 }
 
 template <class Cfg>
@@ -603,7 +756,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int nc = EVEN ? CPW : (half ? Cfg::CHUNKS - Cfg::CB0 : Cfg::CB0);
     uint8_t* stg = Cfg::ROWSTG ? sStg + q * 32 * Cfg::ROW_PITCH : sStg + e * 4096;
     const uint32_t stg_addr = smem_u32(stg);
-    uint32_t acc = 0, acc_phase = 0, fx_phase = 0;
+    uint32_t acc = 0, acc_phase = 0, fx_phase = 0, head_buf = 0;
     SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
     Segment sg;
     while (it.next(sg)) {
@@ -873,7 +1026,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       };
 
-      bool gated_done = false;
+      if constexpr (Cfg::HEAD) {
+        head_epilogue<Cfg>(p, &tmC, t_row, row0, nb, half, lane, stg, stg_addr, head_buf, hand_back);
+        next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
+        continue;
+      }
+      bool gated_done = Cfg::HEAD;
       if constexpr (BN == 256) {
         if (sg.half) {
           // ---- a half tile of the split tail: BN / 2 columns in TMEM
