@@ -555,7 +555,10 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   // adding to C is done by the TMA stores: fp32 rows of whole 16-byte units
   if (pr.c_add && (!f32 || !c_tma || pr.n % 4 != 0)) return DGL_ERR_UNSUPPORTED;
   std::memset(&tc, 0, sizeof(tc));
-  if (c_tma && !cached_output_map(&tc, pr.C, f32, pr.n, pr.m, pr.N, plan.tile_m == 64 ? 16 : 32)) return DGL_ERR_CUDA;
+  if (pr.k_splits > 1 && (!f32 || !c_tma || pr.c_add || linear || plan.tile_m == 64)) return DGL_ERR_UNSUPPORTED;
+  const int64_t slab_rows = (pr.m + plan.tile_m - 1) / plan.tile_m * plan.tile_m;
+  const int64_t c_rows = pr.k_splits > 1 ? pr.k_splits * slab_rows : pr.m;
+  if (c_tma && !cached_output_map(&tc, pr.C, f32, pr.n, c_rows, pr.N, plan.tile_m == 64 ? 16 : 32)) return DGL_ERR_CUDA;
   TcParams p = {};
   p.C = pr.C;
   p.ldc = pr.N;
@@ -609,7 +612,15 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   p.half_tiles = 0;
   p.ws = nullptr;
   p.flags = nullptr;
-  if (plan.split_tail && !split && !pr.gated && plan.tile_n == 256 && p.num_tiles > p.workers) {
+  if (pr.k_splits > 1) {
+    p.dp_tiles = p.num_tiles * pr.k_splits;
+    p.k_splits = pr.k_splits;
+    p.slab_rows = static_cast<int>(slab_rows);
+    p.workers = p.dp_tiles < ds->num_sms / cg ? p.dp_tiles : ds->num_sms / cg;
+    p.sk_workers = p.workers;
+    grid = p.workers * cg;
+    split = false;
+  } else if (plan.split_tail && !split && !pr.gated && plan.tile_n == 256 && p.num_tiles > p.workers) {
     // the last, partial wave as half tiles, one per worker
     const int tail = p.num_tiles % p.workers;
     if (tail > 0 && 2 * tail <= p.workers) {

@@ -66,6 +66,11 @@ struct TcParams {
   int tiles_m, tiles_n, num_tiles, num_kb;
   int group_m;          // tile raster: group_m row-tiles share each column sweep
   int c_tma;            // 1: C is written by TMA tensor stores (16-byte aligned pitch and base)
+  // k_splits > 1: each tile's k-stages in k_splits ranges, every range a segment
+  // of its own whose fp32 sums go to a C of its own, slab_rows rows further
+  // on; the caller adds them.  No stream-K or half tiles then.
+  int k_splits;
+  int slab_rows;
   int c_add;            // 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
   int* status;          // device status word
   // Schedule.  `workers` CTAs (or CTA pairs) run at once.  Tiles below
@@ -188,6 +193,7 @@ __device__ __forceinline__ float apply_act(int act, float x) {
 struct Segment {
   int tile, kb0, kb1;
   int half;  // 0: the whole tile; 1 / 2: its left / right half (BN / 2 columns)
+  int split; // k_splits > 1: which of the tile's ranges of k-stages
 };
 
 __host__ __device__ inline int64_t sk_range_start(int64_t units, int workers, int w) {
@@ -202,18 +208,19 @@ __host__ __device__ inline int sk_worker_of(int64_t units, int workers, int64_t 
   return w;
 }
 
-// Walks worker w's segments in order: its data-parallel tiles, then (split
+// Walks worker w's segments in order: its data-parallel tiles (with k_splits,
+// one range of a tile's k-stages at a time), then (split
 // tail) at most one half tile of the last wave, or (stream-K) its range of
 // the last wave's k-stages: the units are cut into sk_workers equal ranges
 // (0: one per worker), and workers from sk_workers on get none.  Every role
 // of a CTA walks the same sequence.
 struct SegmentIter {
-  int w, workers, nk, dp_tiles, next_dp, half_tiles, next_half;
+  int w, workers, nk, dp_tiles, next_dp, half_tiles, next_half, splits;
   int64_t u, u_end;
   __host__ __device__ SegmentIter(int worker, int num_workers, int num_kb, int dp, int64_t units, int halves = 0,
-                                  int sk_workers = 0)
+                                  int sk_workers = 0, int k_splits = 0)
       : w(worker), workers(num_workers), nk(num_kb), dp_tiles(dp), next_dp(worker), half_tiles(halves),
-        next_half(worker), u(0), u_end(0) {
+        next_half(worker), splits(k_splits), u(0), u_end(0) {
     const int skw = sk_workers > 0 ? sk_workers : num_workers;
     if (units > 0 && worker < skw) {
       u = sk_range_start(units, skw, worker);
@@ -222,10 +229,19 @@ struct SegmentIter {
   }
   __host__ __device__ bool next(Segment& s) {
     s.half = 0;
+    s.split = 0;
     if (next_dp < dp_tiles) {
       s.tile = next_dp;
       s.kb0 = 0;
       s.kb1 = nk;
+      if (splits > 1) {
+        // dp_tiles counts every tile once per split; a split's tiles are neighbours
+        const int tiles = dp_tiles / splits;
+        s.split = next_dp / tiles;
+        s.tile = next_dp - s.split * tiles;
+        s.kb0 = static_cast<int>(static_cast<int64_t>(nk) * s.split / splits);
+        s.kb1 = static_cast<int>(static_cast<int64_t>(nk) * (s.split + 1) / splits);
+      }
       next_dp += workers;
       return true;
     }

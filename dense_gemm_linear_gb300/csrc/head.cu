@@ -289,6 +289,29 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
 }
 
+// dX from the fp32 sums of its ranges of the vocabulary, in order; a thread
+// adds four columns of a row.
+__global__ void __launch_bounds__(256)
+    head_join_kernel(const float* __restrict__ part, int64_t slab, int splits, __nv_bfloat16* __restrict__ out,
+                     int64_t ldo, int rows, int cols) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
+  if (i >= static_cast<int64_t>(rows) * (cols / 4)) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(part + k * slab + 4 * i);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
+  const int64_t r = i / (cols / 4), c = i % (cols / 4) * 4;
+  *reinterpret_cast<uint2*>(out + r * ldo + c) = *reinterpret_cast<const uint2*>(o);
+}
+
 // Launch of a kernel that starts with griddep_wait.
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t stream,
@@ -409,16 +432,45 @@ void logits_tile(int64_t rows, int& tile_m, int& tile_n) {
   tile_n = rows > 128 ? 256 : 128;
 }
 
-// dX's tile and schedule: few tiles with a long sum (V) are split along it.
-void choose_dx_plan(int64_t m, int64_t n, int64_t K, int num_sms, dgl_plan_info* out) {
-  bool have = false;
+// dX's tile and schedule.  The sum runs over the vocabulary, so few tiles with
+// a very long sum are the ordinary case.  Either the tail's k-stages are
+// shared by all workers (stream-K), or, with at most one tile per worker, each
+// tile's sum is cut into as many ranges as there are workers for and a further
+// kernel adds their fp32 sums: the ranges are added by all SMs at once, where
+// stream-K's tile owner adds them one after another (131 x 1024 over 11007:
+// 63 us with stream-K).  Returns the number of ranges.
+constexpr double kJoinUs = 3.0;           // the adding kernel's launch and latency
+constexpr double kJoinBytesPerUs = 4.0e6;  // its reads, and the ranges' writes, mostly in L2
+
+int choose_dx_plan(int64_t m, int64_t n, int64_t K, int num_sms, dgl_plan_info* out) {
+  double best = 0.0;
+  int best_splits = 0;
+  const int nk = static_cast<int>((K + 63) / 64);
   for (int tile_m : {128, 256})
     for (int tile_n : {128, 256}) {
       dgl_plan_info cand;
       fill_tc_plan(DGL_DTYPE_BF16, DGL_OUT_BF16, m, n, K, tile_m, tile_n, num_sms, &cand, -1);
-      if (!have || cand.est_us <= out->est_us) *out = cand;
-      have = true;
+      if (best_splits == 0 || cand.est_us <= best) {
+        *out = cand;
+        best = cand.est_us;
+        best_splits = 1;
+      }
+      const int units = num_sms / (tile_m == 256 ? 2 : 1);
+      const int64_t tiles = ((m + tile_m - 1) / tile_m) * ((n + tile_n - 1) / tile_n);
+      const int splits = static_cast<int>(std::min<int64_t>(units / std::max<int64_t>(tiles, 1), nk / 4));
+      if (splits < 2) continue;
+      double stage_us, tile_us;
+      if (!tc_tile_cost(tile_m, tile_n, &stage_us, &tile_us)) continue;
+      const double est = 5.0 + (nk + splits - 1) / splits * stage_us + tile_us + kJoinUs +
+                         8.0 * splits * static_cast<double>(m) * n / kJoinBytesPerUs;
+      if (est < best) {
+        fill_tc_plan(DGL_DTYPE_BF16, DGL_OUT_F32, m, n, K, tile_m, tile_n, num_sms, out, 0);
+        out->split_tail = 0;
+        best = est;
+        best_splits = splits;
+      }
     }
+  return best_splits;
 }
 
 dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float scale, cudaStream_t stream) {
@@ -535,15 +587,24 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       return DGL_ERR_CUDA;
 
     if (h.dX) {
-      Problem px{DGL_DTYPE_BF16, DGL_OUT_BF16, e, w, nullptr, nullptr,
-                 static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx, n, h.lddx, V8, n, h.d};
+      __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx;
+      dgl_plan_info plan;
+      const int splits = choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
+      Problem px{DGL_DTYPE_BF16, splits > 1 ? DGL_OUT_F32 : DGL_OUT_BF16, e, w, nullptr, nullptr,
+                 splits > 1 ? static_cast<void*>(scratch.ws) : dx, n, splits > 1 ? h.d : h.lddx, V8, n, h.d};
       px.b_mn = 1;
       px.lda = lay.lde;
       px.ldb = h.ldw;
       px.b_k = h.V;
-      dgl_plan_info plan;
-      choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
+      px.k_splits = splits;
       if ((st = run(px, &plan, stream, &scratch)) != DGL_OK) return st;
+      if (splits > 1) {
+        const int64_t slab = round_up(n, plan.tile_m) * h.d;
+        const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
+        if (launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream, scratch.ws, slab,
+                             splits, dx, h.lddx, n, d) != cudaSuccess)
+          return DGL_ERR_CUDA;
+      }
     }
     if (h.dW) {
       const bool f32 = dw_sums || h.dw_dtype == DGL_OUT_F32;

@@ -98,6 +98,14 @@ static const Rung* find_rung(int tile_m, int tile_n) {
   return nullptr;
 }
 
+bool tc_tile_cost(int tile_m, int tile_n, double* stage_us, double* tile_us) {
+  const Rung* r = find_rung(tile_m, tile_n);
+  if (!r) return false;
+  *stage_us = r->stage_us;
+  *tile_us = r->tile_us;
+  return true;
+}
+
 constexpr double kFixupUs = 8.0;  // hand-over of fp32 partial tiles: write, wait, read, add (measured)
 
 // stream_k: 0 data-parallel, 1 the tail's k-stages over all workers, S >= 2

@@ -14,6 +14,8 @@ double operand_bytes(int dtype, int out_dtype, int64_t m, int64_t n, int64_t K);
 int tc_tile_k(int dtype);
 int tc_stages(int tile_m, int tile_n);
 bool tc_supported_tile(int tile_m, int tile_n);
+// The cost model's time of a tile's k-stage and of the tile besides; false for a tile off the ladder.
+bool tc_tile_cost(int tile_m, int tile_n, double* stage_us, double* tile_us);
 // stream_k: -2 the planner's default (split-K tail where it applies), -1 the
 // cost model decides on stream-K, 0 off, 1 stream-K over all workers (when
 // eligible), S >= 2 a split-K tail over S workers per tile (when it fits).

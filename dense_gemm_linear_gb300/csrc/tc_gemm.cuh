@@ -254,7 +254,8 @@ struct StageIter {
   int kb = 0, kb1 = 0, mb = 0, nb = 0;
   int tiles_m, tiles_n, group_m;
   __device__ StageIter(int worker, const TcParams& prm)
-      : it(worker, prm.workers, prm.num_kb, prm.dp_tiles, prm.sk_units, prm.half_tiles, prm.sk_workers),
+      : it(worker, prm.workers, prm.num_kb, prm.dp_tiles, prm.sk_units, prm.half_tiles, prm.sk_workers,
+           prm.k_splits),
         tiles_m(prm.tiles_m),
         tiles_n(prm.tiles_n), group_m(prm.group_m) {}
   __device__ bool next(int& mb_out, int& nb_out, int& kb_out) {
@@ -534,7 +535,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // into L2, the point where every SM's global writes land, so what the
     // loads read after the wait below is current whatever the previous kernel
     // wrote.
-    SegmentIter it0(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
+    SegmentIter it0(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
+                   p.k_splits);
     Segment s0;
     if (it0.next(s0) && !s0.half) {
       int mb, nb;
@@ -578,7 +580,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const uint64_t pol = l2_policy_evict_last();
       uint32_t stage = 0, phase = 0;
       int64_t issued = 0;
-      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
+      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
+                   p.k_splits);
       Segment sg;
       while (!fail && it.next(sg)) {
         int mb, nb;
@@ -656,7 +659,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const uint32_t b_kstep = (p.b_mn ? MN_K_STEP_BYTES : Cfg::MMA_K_BYTES) >> 4;
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued_any = false;
-      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
+      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
+                   p.k_splits);
       Segment sg;
       while (!fail && it.next(sg)) {
         const bool ok = mbar_wait(&tempty[acc], acc_phase ^ 1);
@@ -757,7 +761,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* stg = Cfg::ROWSTG ? sStg + q * 32 * Cfg::ROW_PITCH : sStg + e * 4096;
     const uint32_t stg_addr = smem_u32(stg);
     uint32_t acc = 0, acc_phase = 0, fx_phase = 0, head_buf = 0;
-    SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
+    SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
+                   p.k_splits);
     Segment sg;
     while (it.next(sg)) {
       int mb, nb;
@@ -790,7 +795,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // ((c * 4 + q) * 8 + t) * 32 + lane holds columns 32c + 4t .. 32c + 4t + 3
       // of slab row 32q + lane, so each warp's 32 x 32 chunk is 4 KB of
       // contiguous memory, written and read with bulk copies.
-      if (Cfg::STREAM_K && sg.kb0 > 0) {
+      if (Cfg::STREAM_K && sg.kb0 > 0 && p.k_splits <= 1) {
         uint8_t* slot = reinterpret_cast<uint8_t*>(p.ws) + (static_cast<int64_t>(cluster_id) * CG + rank) * Cfg::SLOT_BYTES;
         const uint32_t fx = Cfg::ROWSTG ? stg_addr + half * Cfg::FX_WARP_BYTES : stg_addr;
         int piece = 0;
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
-      if (Cfg::STREAM_K && sg.kb1 < p.num_kb) {
+      if (Cfg::STREAM_K && sg.kb1 < p.num_kb && p.k_splits <= 1) {
         // Finisher: the tile's other k-stages belong to workers cluster_id + 1
         // .. w_last (an empty range holds none).  This is the worker's last
         // segment, so every MMA has finished and the operand ring is free:
@@ -987,7 +992,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (Cfg::OUT_F32 && p.c_add)
                   tma_reduce_add_2d(&tmC, stg_u, col0, row0);
                 else
-                  tma_store_2d(&tmC, stg_u, col0, row0);
+                  tma_store_2d(&tmC, stg_u, col0, row0 + sg.split * p.slab_rows);
               }
               bulk_commit();  // an empty group too: the waits above count groups
             }
