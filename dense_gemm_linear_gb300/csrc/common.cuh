@@ -33,11 +33,10 @@ enum : int { PDL_SERIAL = 0, PDL_BATCH_HEAD = 1, PDL_BATCH_NEXT = 2 };
 // The tile's accumulators are logits up to the factor `scale`; in units of
 // log 2 they are y = acc c, c = scale log2(e).  A warp holds 32 rows by one
 // column group (half a tile's columns); per row and group it leaves in part
-// the largest y, Y, and the sum of 2^(y - Y + kHeadShift), and with `store`
+// the largest y, Y, and the sum of 2^(y - Y + kHeadShift), and with HEAD = 2
 // writes 2^(y - Y + kHeadShift) in fp16 as the tile's output.
 struct HeadEpi {
   float c;      // scale log2(e); its sign is applied to the accumulators first
-  int store;
   float2* part;  // [rows][part_ld] (Y, sum) per column group
   int part_ld;
   // Accumulators to pick out of the tile, [rows][k] into pick: one target per

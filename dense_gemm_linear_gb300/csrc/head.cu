@@ -53,7 +53,7 @@ struct HeadRows {
   float* q;          // [rows][k] their weights
   float4* sums;      // [rows] Q, sum q log q, state (1: has a loss, 0: none, -1: index out of range), 0
   uint8_t* start;    // [rows][start_ld] entries before each column group
-  int start_ld, group_cols;
+  int start_ld, group_shift;  // a group is 2^group_shift columns
   float* pick;       // [rows][max(k, 1)] accumulators of the entries
   float2* part;      // [rows][groups] (largest y, sum of the exponentials)
   int groups;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   __syncwarp();
   for (int g = lane; g < rows.start_ld; g += 32) {
     // entries with a column below the group's first one (the last group ends past V)
-    const int64_t below = static_cast<int64_t>(g) * rows.group_cols;
+    const int64_t below = static_cast<int64_t>(g) << rows.group_shift;
     int lo = 0, hi = k;
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
@@ -248,24 +248,39 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float f = has ? grad[row] * scale : 0.0f;
   const float fS = f * (Q / S);
   uint16_t* er = e + row * lde;
+  uint4* e8 = reinterpret_cast<uint4*>(er);
   const int V8 = (V + 7) / 8;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < V8; i += kFinishThreads) {
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (has) {
-      const uint4 v = reinterpret_cast<const uint4*>(er)[i];
-      const float a = fS * exp2f((part[8 * i / rows.group_cols].x - base) - kHeadShift);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      uint32_t r[4];
+  if (!has) {
+    for (int i = threadIdx.x; i < V8; i += kFinishThreads) e8[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    // four loads in flight a thread
+    constexpr int U = 4;
+    for (int i0 = threadIdx.x; i0 < V8; i0 += U * kFinishThreads) {
+      uint4 v[U];
+      float top[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-        const __nv_bfloat162 b2 = __floats2bfloat162_rn(p2.x * a, p2.y * a);
-        r[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kFinishThreads;
+        if (i < V8) {
+          v[u] = e8[i];
+          top[u] = part[8 * i >> rows.group_shift].x;
+        }
       }
-      o = make_uint4(r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kFinishThreads;
+        if (i >= V8) break;
+        const float a = fS * exp2f((top[u] - base) - kHeadShift);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(p2.x * a, p2.y * a);
+          w[j] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        e8[i] = v[u];
+      }
     }
-    reinterpret_cast<uint4*>(er)[i] = o;
   }
   const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
   uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
@@ -363,7 +378,15 @@ constexpr int64_t kChunkBytes = int64_t(1) << 30;
 constexpr int64_t kChunkRowsMost = 32768;
 constexpr int kSplitSlots = 160;  // partial tiles of 128 x 256: one per CTA
 
+// Column groups of a row: halves of the logits' tiles.
 int64_t head_groups(int64_t V, int tile_n) { return 2 * ((V + tile_n - 1) / tile_n); }
+
+// The tile of the logits' product: CTA pairs from 129 rows on.
+void logits_tile(int64_t rows, int& tile_m, int& tile_n) {
+  tile_m = rows > 128 ? 256 : 128;
+  tile_n = rows > 128 ? 256 : 128;
+}
+
 
 HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   HeadLayout l;
@@ -371,7 +394,11 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   l.chunk = chunk;
   const bool grad = h.grad != nullptr;
   const int64_t rows = std::min(chunk, round_up(std::max<int64_t>(h.T, 1), kChunkRows));
-  const int64_t groups = head_groups(h.V, 128);  // of the narrowest tile
+  // statistics of the whole chunk, or of a last one on the narrower tiles
+  int tile_m, tile_n;
+  logits_tile(rows, tile_m, tile_n);
+  const int64_t groups = head_groups(h.V, tile_n);
+  const int64_t narrow = std::min(rows, kChunkRows) * (head_groups(h.V, 128) + 1);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -384,13 +411,13 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
     l.split = take(int64_t(kSplitSlots) * 128 * 256 * 4);
     l.flags = take(kSplitSlots * 4);
   }
-  l.part = take(rows * groups * 8);
+  l.part = take(std::max(rows * groups, narrow) * 8);
   l.pick = take(rows * std::max(k, 1) * 4);
   if (k > 0) {
     l.column = take(rows * k * 4);
     l.q = take(rows * k * 4);
     l.sums = take(rows * 16);
-    l.start = take(rows * (groups + 1));
+    l.start = take(std::max(rows * (groups + 1), narrow));
   }
   if (grad && h.dW && h.dw_dtype == DGL_OUT_BF16 && chunk < h.T) l.dw = take(h.V * h.d * 4);
   l.bytes = at;
@@ -426,19 +453,14 @@ dgl_status check_matrix(const void* p, int64_t& ld, int64_t d) {
   return DGL_OK;
 }
 
-// The tile of the logits' product: CTA pairs from 129 rows on.
-void logits_tile(int64_t rows, int& tile_m, int& tile_n) {
-  tile_m = rows > 128 ? 256 : 128;
-  tile_n = rows > 128 ? 256 : 128;
-}
-
 // dX's tile and schedule.  The sum runs over the vocabulary, so few tiles with
-// a very long sum are the ordinary case.  Either the tail's k-stages are
-// shared by all workers (stream-K), or, with at most one tile per worker, each
-// tile's sum is cut into as many ranges as there are workers for and a further
-// kernel adds their fp32 sums: the ranges are added by all SMs at once, where
-// stream-K's tile owner adds them one after another (131 x 1024 over 11007:
-// 63 us with stream-K).  Returns the number of ranges.
+// a very long sum are the ordinary case.  With at most half as many tiles as
+// workers, each tile's sum is cut into as many ranges as there are workers for
+// and a further kernel adds their fp32 sums, all SMs at once; stream-K's tile
+// owner would add them one after another (131 x 1024 over 11007: 63 us with
+// stream-K, 18.6 us with ranges).  With more tiles, the tail's k-stages are
+// shared by all workers where the cost model says so (stream-K): few ranges a
+// tile.  Returns the number of ranges.
 constexpr double kJoinUs = 3.0;           // the adding kernel's launch and latency
 constexpr double kJoinBytesPerUs = 4.0e6;  // its reads, and the ranges' writes, mostly in L2
 
@@ -448,15 +470,15 @@ int choose_dx_plan(int64_t m, int64_t n, int64_t K, int num_sms, dgl_plan_info* 
   const int nk = static_cast<int>((K + 63) / 64);
   for (int tile_m : {128, 256})
     for (int tile_n : {128, 256}) {
+      const int units = num_sms / (tile_m == 256 ? 2 : 1);
+      const int64_t tiles = ((m + tile_m - 1) / tile_m) * ((n + tile_n - 1) / tile_n);
       dgl_plan_info cand;
-      fill_tc_plan(DGL_DTYPE_BF16, DGL_OUT_BF16, m, n, K, tile_m, tile_n, num_sms, &cand, -1);
+      fill_tc_plan(DGL_DTYPE_BF16, DGL_OUT_BF16, m, n, K, tile_m, tile_n, num_sms, &cand, 2 * tiles > units ? -1 : 0);
       if (best_splits == 0 || cand.est_us <= best) {
         *out = cand;
         best = cand.est_us;
         best_splits = 1;
       }
-      const int units = num_sms / (tile_m == 256 ? 2 : 1);
-      const int64_t tiles = ((m + tile_m - 1) / tile_m) * ((n + tile_n - 1) / tile_n);
       const int splits = static_cast<int>(std::min<int64_t>(units / std::max<int64_t>(tiles, 1), nk / 4));
       if (splits < 2) continue;
       double stage_us, tile_us;
@@ -533,7 +555,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     rows.pick = reinterpret_cast<float*>(ws + lay.pick);
     rows.part = reinterpret_cast<float2*>(ws + lay.part);
     rows.groups = static_cast<int>(head_groups(h.V, tile_n));
-    rows.group_cols = tile_n / 2;
+    rows.group_shift = tile_n == 256 ? 7 : 6;
     if (tg.k > 0) {
       rows.column = reinterpret_cast<int*>(ws + lay.column);
       rows.q = reinterpret_cast<float*>(ws + lay.q);
@@ -570,7 +592,6 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.sk_workers = p.workers;
     p.pdl_mode = PDL_SERIAL;
     p.head.c = c;
-    p.head.store = grad ? 1 : 0;
     p.head.part = rows.part;
     p.head.part_ld = rows.groups;
     p.head.target = tg.k > 0 ? nullptr : tg.index;
@@ -579,7 +600,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.head.start_ld = rows.start_ld;
     p.head.k = std::max(tg.k, 1);
     p.head.pick = rows.pick;
-    if (launch_tc_head(tile_m, tile_n, ta, tb, tc, p, p.workers * cg, stream) != cudaSuccess) return DGL_ERR_CUDA;
+    if (launch_tc_head(grad, tile_m, tile_n, ta, tb, tc, p, p.workers * cg, stream) != cudaSuccess) return DGL_ERR_CUDA;
 
     if (launch_dependent(head_finish_kernel, static_cast<unsigned>(n), kFinishThreads, stream, tg, rows, V, scale, c,
                          grad ? h.grad + t0 : nullptr, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,

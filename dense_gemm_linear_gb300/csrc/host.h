@@ -79,7 +79,7 @@ dgl_status run(const Problem& pr, const dgl_plan_info* forced, cudaStream_t stre
                const SplitScratch* scratch = nullptr);
 
 // Tensor maps of a K-major bf16 operand (128-byte boxes of box_rows rows) and
-// of a bf16 output (32 x 32 boxes), from the cache.
+// of a 16-bit output (32 x 32 boxes), from the cache.
 bool bf16_operand_map(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int box_rows, int64_t pitch);
 bool bf16_output_map(CUtensorMap* map, void* base, int64_t cols, int64_t rows, int64_t ldc);
 

@@ -57,10 +57,10 @@ cudaError_t launch_tc_e4m3_m64(int out, int tile_n, bool row_staging, const CUte
 // p.sfb: the E8M0 scales.
 cudaError_t launch_tc_mxfp4(int out, bool row_staging, const CUtensorMap& ta, const CUtensorMap& tb,
                             const CUtensorMap& tc, const TcParams& p, int grid, cudaStream_t stream);
-// Logits of a linear head (p.head; 16-bit output through tc where p.head.store):
-// tiles 256 x 256, 128 x 256 and 128 x 128.
-cudaError_t launch_tc_head(int tile_m, int tile_n, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
-                           const TcParams& p, int grid, cudaStream_t stream);
+// Logits of a linear head (p.head; store: 16-bit output through tc): tiles 256 x 256,
+// 128 x 256 and 128 x 128.
+cudaError_t launch_tc_head(bool store, int tile_m, int tile_n, const CUtensorMap& ta, const CUtensorMap& tb,
+                           const CUtensorMap& tc, const TcParams& p, int grid, cudaStream_t stream);
 // Decode kernel: ta = A map (16-row box), tb_lo / tb_hi = B maps whose box
 // heights are the two part sizes floor(n/parts) and ceil(n/parts).
 cudaError_t launch_decode(int dtype, int out, const CUtensorMap& ta, const CUtensorMap& tb_lo,

@@ -61,15 +61,15 @@ constexpr int tc_ring_stages(int stage_bytes, int staging_bytes) {
 }
 
 template <int BN_, bool FP8_, bool OUT_F32_, bool ROWSTG_, int CG_ = 1, bool EPI_ = false, bool MX_ = false,
-          int BM_ = 128, bool HEAD_ = false>
+          int BM_ = 128, int HEAD_ = 0>
 struct TcConfig {
   static constexpr int CG = CG_;                        // CTAs per MMA: 1, or 2 for a CTA pair (M = 256)
   // EPI: the linear-layer epilogue (bias, activation, and on CTA pairs the
   // gated up projection) is compiled in; plain GEMM variants leave it out.
   static constexpr bool EPI = EPI_;
   // HEAD: the epilogue of a linear head's logits (HeadEpi) takes the place of
-  // the others'.
-  static constexpr bool HEAD = HEAD_;
+  // the others': 1 statistics only, 2 the exponentials are stored too.
+  static constexpr int HEAD = HEAD_;
   // Rows of C per CTA: 128, or 64 for the small rungs of the ladder (one CTA,
   // an M = 64 MMA).  An M = 64 accumulator puts row 16 q + r (r < 16) in
   // tensor-memory lane 32 q + r, so each epilogue warp of lane quarter q holds
@@ -114,7 +114,7 @@ struct TcConfig {
   // whole-row staging: BN bf16 + 16 bytes of shift room; the pitch is an odd
   // multiple of 16 bytes so rows spread over the banks
   static constexpr int ROW_PITCH = BN * 2 + 16;
-  static constexpr int STG_TOTAL = ROWSTG ? 4 * 32 * ROW_PITCH : EPI_WARPS * 4096;
+  static constexpr int STG_TOTAL = ROWSTG ? 4 * 32 * ROW_PITCH : HEAD == 1 ? 0 : EPI_WARPS * 4096;
   // MX: per stage, 512-byte scale atoms for each 128 rows and each 4 k-blocks:
   // 2 of A's, 2 per 128 rows of B
   static constexpr int SCALE_ATOMS = MX ? 2 + 2 * (BN / 128) : 0;
@@ -144,7 +144,7 @@ struct TcConfig {
   static_assert(BN == 64 || BN == 128 || BN == 256 || (BN == 224 && CG == 2 && !EPI && !MX),
                 "tile widths of the ladder (224: plain GEMM on CTA pairs)");
   static_assert(BM == 128 || (BM == 64 && CG == 1 && !EPI && !MX), "64-row tiles: one CTA, plain GEMM");
-  static_assert(!HEAD || (!FP8_ && !EPI && !MX && !ROWSTG_ && !OUT_F32_ && BM_ == 128 && BN_ % 128 == 0),
+  static_assert(HEAD == 0 || (!FP8_ && !EPI && !MX && !ROWSTG_ && !OUT_F32_ && BM_ == 128 && BN_ % 128 == 0),
                 "head variants: bf16 operands, TMA-stored 16-bit output");
   static_assert(STAGES >= 3, "ring too shallow");
   static_assert((ROW_PITCH / 16) % 2 == 1, "row pitch: odd multiple of 16 bytes");
@@ -334,50 +334,85 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// One warp's share (32 rows x BN / 2 columns) of a tile of head logits: see
-// HeadEpi.  Two passes over the accumulators in tensor memory: the group's
-// largest value first, so that the second knows what its exponentials are
-// relative to before it stores any.  hand_back() releases the accumulator.
+// Two fp32 operations in one instruction: the epilogue shares its schedulers
+// with the warp that issues the MMAs.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The accumulators that a row wants picked out of one column group: entries
+// first .. last - 1 of its sorted columns, the first at column `at` of the
+// group (or its one target).  Read before the tile's products are waited for.
+struct HeadPicks {
+  int first = 0, last = 0, at = 0;
+};
+
+__device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int group, int cols) {
+  const HeadEpi& h = p.head;
+  HeadPicks k;
+  if (row >= p.m) return k;
+  const int col0 = group * cols;
+  if (h.start) {
+    const uint8_t* st = h.start + static_cast<int64_t>(row) * h.start_ld + group;
+    k.first = st[0];
+    k.last = st[1];
+    if (k.first < k.last) k.at = h.column[static_cast<int64_t>(row) * h.k + k.first] - col0;
+  } else if (h.target) {
+    const int64_t y = h.target[row];
+    if (y >= col0 && y < min(col0 + cols, p.n)) {
+      k.at = static_cast<int>(y) - col0;
+      k.last = 1;
+    }
+  }
+  return k;
+}
+
+// One warp's share (32 rows x BN / 2 columns, one group) of a tile of head
+// logits: see HeadEpi.  Two passes over the accumulators in tensor memory: the
+// group's largest value first, so that every exponential is relative to it.
+// hand_back() releases the accumulator.
+//
+// Four warps per lane quarter with a quarter of the columns each, read once
+// and kept in registers, measured slower (xent gradient 1024 x 50257 x 512: 58
+// against 54 us; distill forward 2047 x 50257 x 1024: 166 against 153 us in
+// all): more warps compete with the one that issues the MMAs.
 template <class Cfg, class HandBack>
-__device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorMap* tmC, uint32_t t_row, int row0, int nb,
-                                              int half, int lane, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
+__device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorMap* tmC, uint32_t t0, int row0, int group,
+                                              HeadPicks want, int lane, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
                                               HandBack hand_back) {
   constexpr int GW = Cfg::BN / 2;       // columns of the group
   constexpr int NC = GW / 32;           // its 32-column chunks, taken two at a time
   const HeadEpi& h = p.head;
   const int row = row0 + lane;
-  const bool in = row < p.m;
-  const int group = 2 * nb + half;
   const int col0 = group * GW;
   const float c = fabsf(h.c);
   const bool flip = h.c < 0.0f;
-  const uint32_t t0 = t_row + half * GW;
-  // accumulators to pick: this row's first entry and how many it has here
-  int at = -1, first = 0, last = 0;
-  if (h.start) {
-    if (in) {
-      const uint8_t* st = h.start + static_cast<int64_t>(row) * h.start_ld + group;
-      first = st[0];
-      last = st[1];
-      if (first < last) at = h.column[static_cast<int64_t>(row) * h.k + first] - col0;
-    }
-  } else if (h.target && in) {
-    const int64_t y = h.target[row];
-    if (y >= col0 && y < min(col0 + GW, p.n)) {
-      at = static_cast<int>(y) - col0;
-      last = 1;
-    }
-  }
-  // Picked accumulators: the warp reads one column of all its rows at a time,
-  // the row that wants it keeps its own.
-  for (uint32_t want = __ballot_sync(0xffffffffu, first < last); want != 0;
-       want = __ballot_sync(0xffffffffu, first < last)) {
-    const int src = __ffs(want) - 1;
-    const uint32_t v = tmem_ld_32x32b_x1(t0 + __shfl_sync(0xffffffffu, at, src));
+
+  // The warp reads one column of all its rows at a time, the row that wants
+  // it keeps its own.
+  for (uint32_t who = __ballot_sync(0xffffffffu, want.first < want.last); who != 0;
+       who = __ballot_sync(0xffffffffu, want.first < want.last)) {
+    const int src = __ffs(who) - 1;
+    const uint32_t v = tmem_ld_32x32b_x1(t0 + __shfl_sync(0xffffffffu, want.at, src));
     if (lane == src) {
-      h.pick[static_cast<int64_t>(row) * h.k + first] = __uint_as_float(v);
-      ++first;
-      if (first < last) at = h.column[static_cast<int64_t>(row) * h.k + first] - col0;
+      h.pick[static_cast<int64_t>(row) * h.k + want.first] = __uint_as_float(v);
+      ++want.first;
+      if (want.first < want.last) want.at = h.column[static_cast<int64_t>(row) * h.k + want.first] - col0;
     }
   }
 
@@ -394,7 +429,7 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
         for (int j = 0; j < 32; ++j) r[i][j] ^= 0x80000000u;
     }
   };
-  float m = -INFINITY;
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
   for (int u = 0; u < NC; u += 2) {
     uint32_t r[2][32];
@@ -407,12 +442,16 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
           if (col0 + (u + i) * 32 + j >= p.n) r[i][j] = 0xFF800000u;  // no such column: minus infinity
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) m = fmaxf(m, fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[1][j])));
+    for (int j = 0; j < 32; ++j)
+      m4[j & 3] = fmaxf(m4[j & 3], fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[1][j])));
   }
+  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
   const float top = m == -INFINITY ? m : m * c;
   const float less = top == -INFINITY ? 0.0f : kHeadShift - top;
+  const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c));
+  const uint64_t less2 = pack2(__float_as_uint(less), __float_as_uint(less));
 
-  float sum = 0.0f;
+  uint64_t s2[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
   for (int u = 0; u < NC; u += 2) {
     uint32_t r[2][32];
@@ -421,7 +460,12 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 32; ++j) r[i][j] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i][j]), c, less)));
+      for (int j = 0; j < 32; j += 2) {
+        float lo, hi;
+        unpack2(fma2(pack2(r[i][j], r[i][j + 1]), c2, less2), lo, hi);
+        r[i][j] = __float_as_uint(ex2(lo));
+        r[i][j + 1] = __float_as_uint(ex2(hi));
+      }
     if (col0 + (u + 2) * 32 > p.n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -429,14 +473,12 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
         for (int j = 0; j < 32; ++j)
           if (col0 + (u + i) * 32 + j >= p.n) r[i][j] = 0u;
     }
-    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      s0 += __uint_as_float(r[0][j]);
-      s1 += __uint_as_float(r[1][j]);
-    }
-    sum += s0 + s1;
-    if (h.store) {
+    for (int j = 0; j < 32; j += 2)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        s2[(j + i) & 3] = add2(s2[(j + i) & 3], pack2(r[i][j], r[i][j + 1]));
+    if constexpr (Cfg::HEAD == 2) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t w[16];
@@ -450,7 +492,11 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
       }
     }
   }
-  if (in) h.part[static_cast<int64_t>(row) * h.part_ld + group] = make_float2(top, sum);
+  if (row < p.m) {
+    float lo, hi;
+    unpack2(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), lo, hi);
+    h.part[static_cast<int64_t>(row) * h.part_ld + group] = make_float2(top, lo + hi);
+  }
 }
 
 template <class Cfg>
@@ -767,6 +813,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     while (it.next(sg)) {
       int mb, nb;
       tile_coords(sg.tile, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+      HeadPicks want;
+      if constexpr (Cfg::HEAD != 0)
+        want = head_picks(p, mb * Cfg::TILE_M + static_cast<int>(rank) * BM + q * 32 + lane, 2 * nb + half, BN / 2);
       // all lanes decide together: tcgen05.ld below is warp-collective
       bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase));
       if constexpr (Cfg::ROWSTG) {
@@ -1031,12 +1080,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       };
 
-      if constexpr (Cfg::HEAD) {
-        head_epilogue<Cfg>(p, &tmC, t_row, row0, nb, half, lane, stg, stg_addr, head_buf, hand_back);
+      if constexpr (Cfg::HEAD != 0) {
+        head_epilogue<Cfg>(p, &tmC, t_row + half * (BN / 2), row0, 2 * nb + half, want, lane, stg, stg_addr, head_buf,
+                           hand_back);
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
-      bool gated_done = Cfg::HEAD;
+      bool gated_done = Cfg::HEAD != 0;
       if constexpr (BN == 256) {
         if (sg.half) {
           // ---- a half tile of the split tail: BN / 2 columns in TMEM

@@ -10,7 +10,7 @@
 
 namespace dgl {
 
-template <int BN, bool FP8, bool OUT_F32, bool ROWSTG, int CG, bool EPI, bool MX = false, int BM = 128, bool HEAD = false>
+template <int BN, bool FP8, bool OUT_F32, bool ROWSTG, int CG, bool EPI, bool MX = false, int BM = 128, int HEAD = 0>
 cudaError_t tc_launch_one(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tbh, const CUtensorMap& tc,
                           const TcParams& p, int grid, cudaStream_t stream) {
   using Cfg = TcConfig<BN, FP8, OUT_F32, ROWSTG, CG, EPI, MX, BM, HEAD>;
