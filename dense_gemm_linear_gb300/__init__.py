@@ -10,6 +10,7 @@ missing, loading raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import metrics  # noqa: F401  (pure-Python metric helpers)
@@ -438,11 +439,12 @@ def _rows(t, name, dtype, shape):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return pitch if shape[0] > 1 else shape[1]
 
 
 def _vector(t, name, dtype, shape):
@@ -451,8 +453,14 @@ def _vector(t, name, dtype, shape):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
+
+
+@functools.lru_cache(maxsize=256)
+def _head_workspace_bytes(T, V, d, grad, dX, dW, dw_dtype, k):
+    h = HeadDesc(T=T, V=V, d=d, grad=grad, dX=dX, dW=dW, dw_dtype=dw_dtype)
+    return max(1, dgl_head_workspace(h, k)[1])
 
 
 def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, k, call, where):
@@ -461,52 +469,61 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
         raise TypeError("X and W must be 2-D CUDA tensors")
     T, d = X.shape
     V = W.shape[0]
-    h = HeadDesc()
-    h.T, h.V, h.d = T, V, d
-    h.ldx = _rows(X, "X", torch.bfloat16, (T, d))
-    h.ldw = _rows(W, "W", torch.bfloat16, (V, d))
-    h.X, h.W = X.data_ptr(), W.data_ptr()
-    h.logit_scale = logit_scale
-    s = stream if stream is not None else torch.cuda.current_stream()
-    # buffers made here belong to the stream that uses them, so the allocator
-    # hands them out again only after its work
-    with torch.cuda.stream(s):
-        loss = torch.empty(T, dtype=torch.float32, device=X.device)
-        lse = torch.empty(T, dtype=torch.float32, device=X.device)
-        h.loss, h.lse = loss.data_ptr(), lse.data_ptr()
-        dX = None
-        if grad is not None:
-            _vector(grad, "grad", torch.float32, (T,))
-            if not (need_dx or need_dw):
-                raise ValueError("a call with grad computes dX, dW or both")
-            h.grad = grad.data_ptr()
-            if need_dx:
-                dX = torch.empty((T, d), dtype=torch.bfloat16, device=X.device)
-                h.dX, h.lddx = dX.data_ptr(), d
-            if need_dw:
-                if dW is None:
-                    if accumulate:
-                        raise ValueError("accumulate adds to the fp32 dW that is passed in")
-                    dW = torch.empty((V, d), dtype=torch.float32 if dw_dtype == OUT_F32 else torch.bfloat16,
-                                     device=X.device)
-                elif dW.dtype not in (torch.float32, torch.bfloat16):
+    ldx = _rows(X, "X", torch.bfloat16, (T, d))
+    ldw = _rows(W, "W", torch.bfloat16, (V, d))
+    if stream is not None:
+        # buffers made here belong to the stream that uses them, so the
+        # allocator hands them out again only after its work
+        with torch.cuda.stream(stream):
+            return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate,
+                            workspace, stream.cuda_stream, k, call, where)
+    return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace,
+                    torch.cuda.current_stream().cuda_stream, k, call, where)
+
+
+def _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, s, k,
+             call, where):
+    import torch
+    device = X.device
+    loss = torch.empty(T, dtype=torch.float32, device=device)
+    lse = torch.empty(T, dtype=torch.float32, device=device)
+    dX = None
+    p_grad = p_dx = p_dw = lddw = 0
+    dw_type = OUT_BF16
+    if grad is not None:
+        _vector(grad, "grad", torch.float32, (T,))
+        if not (need_dx or need_dw):
+            raise ValueError("a call with grad computes dX, dW or both")
+        p_grad = grad.data_ptr()
+        if need_dx:
+            dX = torch.empty((T, d), dtype=torch.bfloat16, device=device)
+            p_dx = dX.data_ptr()
+        if need_dw:
+            if dW is None:
+                if accumulate:
+                    raise ValueError("accumulate adds to the fp32 dW that is passed in")
+                dW = torch.empty((V, d), dtype=torch.float32 if dw_dtype == OUT_F32 else torch.bfloat16, device=device)
+                lddw = d
+            else:
+                if dW.dtype not in (torch.float32, torch.bfloat16):
                     raise TypeError(f"dW must be fp32 or bf16, got {dW.dtype}")
-                h.lddw = _rows(dW, "dW", dW.dtype, (V, d))
-                h.dw_dtype = OUT_F32 if dW.dtype == torch.float32 else OUT_BF16
-                h.dW, h.accumulate = dW.data_ptr(), int(bool(accumulate))
-            elif dW is not None or accumulate:
-                raise ValueError("dW is given but not asked for")
-        elif dW is not None or accumulate:
-            raise ValueError("dW needs grad, the losses' upstream gradient")
-        if workspace is None:
-            workspace = torch.empty(max(1, dgl_head_workspace(h, k)[1]), dtype=torch.uint8, device=X.device)
-        elif not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        h.ws, h.ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _check(call(h, s.cuda_stream), where)
+                lddw = _rows(dW, "dW", dW.dtype, (V, d))
+            dw_type = OUT_F32 if dW.dtype == torch.float32 else OUT_BF16
+            p_dw = dW.data_ptr()
+    if not need_dw or grad is None:
+        if dW is not None or accumulate:
+            raise ValueError("dW needs grad, the losses' upstream gradient, and need_dw")
+    if workspace is None:
+        workspace = torch.empty(_head_workspace_bytes(T, V, d, bool(p_grad), bool(p_dx), bool(p_dw), dw_type, k),
+                                dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    h = HeadDesc(T, V, d, X.data_ptr(), ldx, W.data_ptr(), ldw, loss.data_ptr(), lse.data_ptr(), p_grad, p_dx, d, p_dw,
+                 lddw, workspace.data_ptr(), workspace.nbytes, logit_scale, dw_type, int(bool(accumulate)))
+    _check(call(h, s), where)
     if grad is None:
         return loss, lse
-    return loss, lse, dX, dW if need_dw else None
+    return loss, lse, dX, dW
 
 
 def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_scale=1.0, need_dx=True, need_dw=True,

@@ -539,9 +539,12 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   const int cg = plan.cta_group == 2 ? 2 : 1;
   // a gated layer's B holds the gate rows, then the up rows
   const int64_t b_rows = pr.gated ? 2 * pr.n : pr.n;
+  // whole 8-row swizzle atoms
+  const bool tight = pr.tight_a && !pr.a_mn && plan.tile_m == 128 && pr.m <= 120;
+  const int a_box = tight ? static_cast<int>((pr.m + 7) / 8 * 8) : plan.tile_m == 64 ? 64 : 128;
   const bool map_ok =
       (pr.a_mn ? cached_operand_map_mn(&ta, pr.A, pr.m, pr.K, pr.lda)
-               : cached_operand_map(&ta, pr.A, e4m3, pr.K, pr.m, plan.tile_m == 64 ? 64 : 128, pr.lda)) &&
+               : cached_operand_map(&ta, pr.A, e4m3, pr.K, pr.m, a_box, pr.lda)) &&
       (pr.b_mn ? cached_operand_map_mn(&tb, pr.B, b_rows, pr.b_k ? pr.b_k : pr.K, pr.ldb)
                : cached_b_map(&tb, pr.B, e4m3, pr.w4, pr.K, b_rows, plan.tile_n / cg, pr.ldb));
   if (!map_ok) return DGL_ERR_CUDA;
@@ -576,6 +579,7 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   p.group_m = 16;
   p.c_tma = c_tma ? 1 : 0;
   p.c_add = pr.c_add;
+  p.a_box_rows = tight ? a_box : 0;
   p.status = ds->status;
   p.bias = pr.bias;
   p.act = pr.act;

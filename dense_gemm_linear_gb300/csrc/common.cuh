@@ -70,6 +70,11 @@ struct TcParams {
   // on; the caller adds them.  No stream-K or half tiles then.
   int k_splits;
   int slab_rows;
+  // Rows of A's K-major box when they are fewer than the tile's (0: all): rows
+  // past the box hold whatever the ring held, and only feed rows of C past m.
+  // A box that reached past m would spend the copy engine's time on its zeros.
+  int a_box_rows;
+  int b_once;           // 1: B's rows are read by one row of tiles only: their lines leave L2 first
   int c_add;            // 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
   int* status;          // device status word
   // Schedule.  `workers` CTAs (or CTA pairs) run at once.  Tiles below

@@ -381,12 +381,31 @@ constexpr int kSplitSlots = 160;  // partial tiles of 128 x 256: one per CTA
 // Column groups of a row: halves of the logits' tiles.
 int64_t head_groups(int64_t V, int tile_n) { return 2 * ((V + tile_n - 1) / tile_n); }
 
-// The tile of the logits' product: CTA pairs from 129 rows on.
-void logits_tile(int64_t rows, int& tile_m, int& tile_n) {
-  tile_m = rows > 128 ? 256 : 128;
-  tile_n = rows > 128 ? 256 : 128;
-}
+// The tile of the logits' product.  Up to 128 rows W's reads set the time and
+// narrow tiles spread it evenly; above, the cost model's cheaper of 128 x 256
+// tiles and 256 x 256 CTA pairs (333 rows: 3 row tiles against 2 of twice the
+// height).
+constexpr int64_t kNarrowRows = 128;
 
+int logits_tile_n(int64_t rows) { return rows > kNarrowRows ? 256 : 128; }
+
+int logits_tile_m(int64_t rows, int64_t V, int64_t d, int num_sms) {
+  if (rows <= kNarrowRows) return 128;
+  double best = 0.0;
+  int best_m = 0;
+  for (int tile_m : {128, 256}) {
+    double stage_us, tile_us;
+    if (!tc_tile_cost(tile_m, 256, &stage_us, &tile_us)) continue;
+    const int64_t units = num_sms / (tile_m == 256 ? 2 : 1);
+    const int64_t tiles = ((rows + tile_m - 1) / tile_m) * ((V + 255) / 256);
+    const double est = static_cast<double>((tiles + units - 1) / units) * ((d + 63) / 64 * stage_us + tile_us);
+    if (best_m == 0 || est <= best) {
+      best = est;
+      best_m = tile_m;
+    }
+  }
+  return best_m;
+}
 
 HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   HeadLayout l;
@@ -395,9 +414,7 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   const bool grad = h.grad != nullptr;
   const int64_t rows = std::min(chunk, round_up(std::max<int64_t>(h.T, 1), kChunkRows));
   // statistics of the whole chunk, or of a last one on the narrower tiles
-  int tile_m, tile_n;
-  logits_tile(rows, tile_m, tile_n);
-  const int64_t groups = head_groups(h.V, tile_n);
+  const int64_t groups = head_groups(h.V, logits_tile_n(rows));
   const int64_t narrow = std::min(rows, kChunkRows) * (head_groups(h.V, 128) + 1);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -546,8 +563,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     const int n = static_cast<int>(std::min(lay.chunk, h.T - t0));
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(h.X) + t0 * h.ldx;
     const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(h.W);
-    int tile_m, tile_n;
-    logits_tile(n, tile_m, tile_n);
+    const int tile_m = logits_tile_m(n, h.V, h.d, ds->num_sms), tile_n = logits_tile_n(n);
     tg.index = targets.index + t0 * std::max(tg.k, 1);
     if (tg.k > 0) tg.logits = targets.logits + t0 * tg.k;
     if (tg.teacher_lse) tg.teacher_lse = targets.teacher_lse + t0;
@@ -571,7 +587,8 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     // ---- logits
     const int cg = tile_m == 256 ? 2 : 1;
     CUtensorMap ta, tb, tc = {};
-    if (!bf16_operand_map(&ta, x, h.d, n, 128, h.ldx) || !bf16_operand_map(&tb, w, h.d, h.V, tile_n / cg, h.ldw) ||
+    const int a_box = static_cast<int>(std::min<int64_t>(round_up(n, 8), 128));
+    if (!bf16_operand_map(&ta, x, h.d, n, a_box, h.ldx) || !bf16_operand_map(&tb, w, h.d, h.V, tile_n / cg, h.ldw) ||
         (grad && !bf16_output_map(&tc, e, V8, n, lay.lde)))
       return DGL_ERR_CUDA;
     TcParams p = {};
@@ -586,6 +603,8 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.num_kb = (d + 63) / 64;
     p.group_m = 16;
     p.c_tma = grad ? 1 : 0;
+    p.a_box_rows = a_box < 128 ? a_box : 0;
+    p.b_once = p.tiles_m == 1 ? 1 : 0;
     p.status = ds->status;
     p.workers = std::min(p.num_tiles, ds->num_sms / cg);
     p.dp_tiles = p.num_tiles;
@@ -618,6 +637,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       px.ldb = h.ldw;
       px.b_k = h.V;
       px.k_splits = splits;
+      px.tight_a = 1;
       if ((st = run(px, &plan, stream, &scratch)) != DGL_OK) return st;
       if (splits > 1) {
         const int64_t slab = round_up(n, plan.tile_m) * h.d;

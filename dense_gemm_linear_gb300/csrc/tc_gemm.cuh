@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
+      const uint64_t pol_b = Cfg::HEAD != 0 && p.b_once ? l2_policy_evict_first() : pol;
       uint32_t stage = 0, phase = 0;
       int64_t issued = 0;
       SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
@@ -644,7 +645,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // a stage's transaction bytes: what the copies read from global
         // memory (packed 4-bit B lands in twice its size of shared memory)
         const uint32_t stage_bytes =
-            Cfg::A_STAGE_BYTES + ((sg.half ? Cfg::B_STAGE_BYTES / 2 : Cfg::B_STAGE_BYTES) >> p.b_tx_shift);
+            (p.a_box_rows ? static_cast<uint32_t>(p.a_box_rows) * Cfg::ROW_BYTES : Cfg::A_STAGE_BYTES) + ((sg.half ? Cfg::B_STAGE_BYTES / 2 : Cfg::B_STAGE_BYTES) >> p.b_tx_shift);
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
           const bool ok = mbar_wait(&empty[stage], phase ^ 1);
           if (!ok) {
@@ -660,12 +661,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], stage_bytes * CG);
             load_operand_pair(sA + stage * Cfg::A_STAGE_BYTES, &tmA, fb, kb * Cfg::BK, a_row, BM, p.a_mn, pol);
             load_operand_pair(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, fb, kb * Cfg::BK, b_row, b_rows,
-                              p.b_mn, pol);
+                              p.b_mn, pol_b);
           } else {
             mbar_arrive_expect_tx(&full[stage], stage_bytes);
             load_operand(sA + stage * Cfg::A_STAGE_BYTES, &tmA, &full[stage], kb * Cfg::BK, a_row, BM, p.a_mn, pol);
             load_operand(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, &full[stage], kb * Cfg::BK, b_row, b_rows,
-                         p.b_mn, pol);
+                         p.b_mn, pol_b);
           }
           ++issued;
           if (++stage == STAGES) {
