@@ -478,7 +478,7 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
             return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate,
                             workspace, stream.cuda_stream, k, call, where)
     return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace,
-                    torch.cuda.current_stream().cuda_stream, k, call, where)
+                    torch._C._cuda_getCurrentRawStream(X.device.index), k, call, where)
 
 
 def _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, s, k,

@@ -77,8 +77,10 @@ constexpr int kPrepareWarps = 4;
 // before each column group.
 __global__ void __launch_bounds__(32 * kPrepareWarps)
     head_prepare_kernel(HeadTargets tg, HeadRows rows, int n, int V) {
-  griddep_launch_dependents();
+  // everything before is done once the logits' kernel may start: it loads its
+  // operands beside this one and waits for it in its epilogue (PDL_BATCH_NEXT)
   griddep_wait();
+  griddep_launch_dependents();
   constexpr int PER = kMaxK / 32;
   __shared__ int s_col[kPrepareWarps][kMaxK];
   __shared__ int s_sorted[kPrepareWarps][kMaxK];
@@ -170,9 +172,11 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
 
 constexpr int kFinishThreads = 256;
 
-// One block per row: statistics of the row's column groups -> loss and lse;
-// with e (gradient), e -> dz in place (zero up to V8), and x for dW = dz^T x,
-// zero where the row has no gradient (0 x NaN would reach dW).
+// One block per row, and with few rows several, each for a slice of the
+// vocabulary (gridDim.y; all of them reduce the row's statistics): statistics
+// of the row's column groups -> loss and lse; with e (gradient), e -> dz in
+// place (zero up to a multiple of 8 columns), and x for dW = dz^T x, zero where
+// the row has no gradient (0 x NaN would reach dW).
 __global__ void __launch_bounds__(kFinishThreads)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
                        float* __restrict__ loss, float* __restrict__ lse_out, uint16_t* __restrict__ e, int64_t lde,
@@ -183,7 +187,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   constexpr int WARPS = kFinishThreads / 32;
   __shared__ float red[2][WARPS];
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (row == 0)
+  const bool lead = blockIdx.y == 0;
+  if (row == 0 && lead)
     for (int i = threadIdx.x; i < nflags; i += kFinishThreads) flags[i] = 0;
   const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
   float m = -INFINITY, s = 0.0f;
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     l = sums.y;
     state = static_cast<int>(sums.z);
   }
-  if (warp == 0) {
+  if (warp == 0 && lead) {
     // sum_k q (lse - z_k) as base - y_k + log2 S: what a likely target's y has
     // in common with the maximum cancels before anything is rounded
     float t = 0.0f;
@@ -249,19 +254,22 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float fS = f * (Q / S);
   uint16_t* er = e + row * lde;
   uint4* e8 = reinterpret_cast<uint4*>(er);
-  const int V8 = (V + 7) / 8;
+  // this block's slice, in units of eight columns
+  const int units = (V + 7) / 8;
+  const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.y / gridDim.y);
+  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.y + 1) / gridDim.y);
   if (!has) {
-    for (int i = threadIdx.x; i < V8; i += kFinishThreads) e8[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = u0 + threadIdx.x; i < u1; i += kFinishThreads) e8[i] = make_uint4(0u, 0u, 0u, 0u);
   } else {
     // four loads in flight a thread
     constexpr int U = 4;
-    for (int i0 = threadIdx.x; i0 < V8; i0 += U * kFinishThreads) {
+    for (int i0 = u0 + threadIdx.x; i0 < u1; i0 += U * kFinishThreads) {
       uint4 v[U];
       float top[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kFinishThreads;
-        if (i < V8) {
+        if (i < u1) {
           v[u] = e8[i];
           top[u] = part[8 * i >> rows.group_shift].x;
         }
@@ -269,7 +277,7 @@ __global__ void __launch_bounds__(kFinishThreads)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kFinishThreads;
-        if (i >= V8) break;
+        if (i >= u1) break;
         const float a = fS * exp2f((top[u] - base) - kHeadShift);
         uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
 #pragma unroll
@@ -284,7 +292,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
   uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
-  for (int i = threadIdx.x; i < d / 8; i += kFinishThreads) xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x + blockIdx.y * kFinishThreads; i < d / 8; i += kFinishThreads * gridDim.y) xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
   if (!has) return;
   __syncthreads();
   for (int j = threadIdx.x; j < k; j += kFinishThreads) {
@@ -297,6 +305,7 @@ __global__ void __launch_bounds__(kFinishThreads)
       w = 0.0f;
       for (int o = j; o < k && column[o] == v; ++o) w += q[o];
     }
+    if (v < static_cast<int64_t>(u0) * 8 || v >= static_cast<int64_t>(u1) * 8) continue;  // another block's
     const float ev = exp2f(pick[j] * c - base);
     // xent: minus the sum of the others, which is what p - 1 leaves of a sure target
     const float dz = tg.k == 0 ? f * ((ev - S) / S) : f * (Q * (ev / S) - w);
@@ -329,10 +338,10 @@ __global__ void __launch_bounds__(256)
 
 // Launch of a kernel that starts with griddep_wait.
 template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t stream,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t stream,
                              Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -609,7 +618,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.workers = std::min(p.num_tiles, ds->num_sms / cg);
     p.dp_tiles = p.num_tiles;
     p.sk_workers = p.workers;
-    p.pdl_mode = PDL_SERIAL;
+    p.pdl_mode = tg.k > 0 ? PDL_BATCH_NEXT : PDL_SERIAL;
     p.head.c = c;
     p.head.part = rows.part;
     p.head.part_ld = rows.groups;
@@ -621,15 +630,20 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.head.pick = rows.pick;
     if (launch_tc_head(grad, tile_m, tile_n, ta, tb, tc, p, p.workers * cg, stream) != cudaSuccess) return DGL_ERR_CUDA;
 
-    if (launch_dependent(head_finish_kernel, static_cast<unsigned>(n), kFinishThreads, stream, tg, rows, V, scale, c,
+    // few rows: enough blocks for every SM to hold several, of at least 2048 columns
+    const int64_t slices = grad ? std::min<int64_t>(int64_t(8) * ds->num_sms / n, h.V / 2048) : 1;
+    const dim3 finish(static_cast<unsigned>(n), static_cast<unsigned>(std::max<int64_t>(1, slices)));
+    if (launch_dependent(head_finish_kernel, finish, kFinishThreads, stream, tg, rows, V, scale, c,
                          grad ? h.grad + t0 : nullptr, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
                          xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
       return DGL_ERR_CUDA;
 
+    __nv_bfloat16* dx = h.dX ? static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx : nullptr;
+    int splits = 1;    // of dX's sum
+    int64_t slab = 0;  // elements of one
     if (h.dX) {
-      __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx;
       dgl_plan_info plan;
-      const int splits = choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
+      splits = choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
       Problem px{DGL_DTYPE_BF16, splits > 1 ? DGL_OUT_F32 : DGL_OUT_BF16, e, w, nullptr, nullptr,
                  splits > 1 ? static_cast<void*>(scratch.ws) : dx, n, splits > 1 ? h.d : h.lddx, V8, n, h.d};
       px.b_mn = 1;
@@ -638,14 +652,10 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       px.b_k = h.V;
       px.k_splits = splits;
       px.tight_a = 1;
+      // dW needs nothing of dX: it loads its operands while dX's last tiles run
+      if (h.dW) px.pdl_mode = PDL_BATCH_HEAD;
       if ((st = run(px, &plan, stream, &scratch)) != DGL_OK) return st;
-      if (splits > 1) {
-        const int64_t slab = round_up(n, plan.tile_m) * h.d;
-        const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
-        if (launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream, scratch.ws, slab,
-                             splits, dx, h.lddx, n, d) != cudaSuccess)
-          return DGL_ERR_CUDA;
-      }
+      slab = round_up(n, plan.tile_m) * h.d;
     }
     if (h.dW) {
       const bool f32 = dw_sums || h.dw_dtype == DGL_OUT_F32;
@@ -657,7 +667,14 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       pw.ldb = h.d;
       pw.k_any = 1;
       pw.c_add = (t0 > 0 || h.accumulate) ? 1 : 0;
+      if (h.dX) pw.pdl_mode = PDL_BATCH_NEXT;
       if ((st = run(pw, nullptr, stream)) != DGL_OK) return st;
+    }
+    if (splits > 1) {
+      const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
+      if (launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream, scratch.ws, slab,
+                           splits, dx, h.lddx, n, d) != cudaSuccess)
+        return DGL_ERR_CUDA;
     }
   }
   if (dw_sums) {
