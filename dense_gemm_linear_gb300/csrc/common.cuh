@@ -65,16 +65,18 @@ struct TcParams {
   int tiles_m, tiles_n, num_tiles, num_kb;
   int group_m;          // tile raster: group_m row-tiles share each column sweep
   int c_tma;            // 1: C is written by TMA tensor stores (16-byte aligned pitch and base)
-  // k_splits > 1: each tile's k-stages in k_splits ranges, every range a segment
-  // of its own whose fp32 sums go to a C of its own, slab_rows rows further
-  // on; the caller adds them.  No stream-K or half tiles then.
+  // k_splits > 1: each tile's k-stages dealt to k_splits segments (segment s
+  // takes s, s + k_splits, ...: segments in step read neighbouring pieces of the
+  // same rows), whose fp32 sums go each to a C of its own, slab_rows rows
+  // further on; the caller adds them.  No stream-K or half tiles then.
   int k_splits;
   int slab_rows;
   // Rows of A's K-major box when they are fewer than the tile's (0: all): rows
   // past the box hold whatever the ring held, and only feed rows of C past m.
   // A box that reached past m would spend the copy engine's time on its zeros.
   int a_box_rows;
-  int b_once;           // 1: B's rows are read by one row of tiles only: their lines leave L2 first
+  int b_once;           // HEAD, 1: B's lines leave L2 first
+  int c_keep;           // HEAD, 1: C's lines stay in L2 longest
   int c_add;            // 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
   int* status;          // device status word
   // Schedule.  `workers` CTAs (or CTA pairs) run at once.  Tiles below
@@ -197,7 +199,7 @@ __device__ __forceinline__ float apply_act(int act, float x) {
 struct Segment {
   int tile, kb0, kb1;
   int half;  // 0: the whole tile; 1 / 2: its left / right half (BN / 2 columns)
-  int split; // k_splits > 1: which of the tile's ranges of k-stages
+  int split; // k_splits > 1: which of the tile's segments; kb0 .. kb1 then count its own k-stages
 };
 
 __host__ __device__ inline int64_t sk_range_start(int64_t units, int workers, int w) {
@@ -213,7 +215,7 @@ __host__ __device__ inline int sk_worker_of(int64_t units, int workers, int64_t 
 }
 
 // Walks worker w's segments in order: its data-parallel tiles (with k_splits,
-// one range of a tile's k-stages at a time), then (split
+// a part of a tile's k-stages at a time), then (split
 // tail) at most one half tile of the last wave, or (stream-K) its range of
 // the last wave's k-stages: the units are cut into sk_workers equal ranges
 // (0: one per worker), and workers from sk_workers on get none.  Every role
@@ -243,8 +245,7 @@ struct SegmentIter {
         const int tiles = dp_tiles / splits;
         s.split = next_dp / tiles;
         s.tile = next_dp - s.split * tiles;
-        s.kb0 = static_cast<int>(static_cast<int64_t>(nk) * s.split / splits);
-        s.kb1 = static_cast<int>(static_cast<int64_t>(nk) * (s.split + 1) / splits);
+        s.kb1 = (nk - s.split + splits - 1) / splits;
       }
       next_dp += workers;
       return true;

@@ -312,7 +312,8 @@ __device__ __forceinline__ void next_acc(uint32_t& acc, uint32_t& acc_phase) {
 // at most one later store is pending.
 template <class Cfg>
 __device__ __forceinline__ void store_chunk_16(const CUtensorMap* map, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
-                                               const uint32_t (&w)[16], int lane, int col0, int row0, bool any) {
+                                               const uint32_t (&w)[16], int lane, int col0, int row0, bool any,
+                                               uint64_t policy) {
   const uint32_t a = stg_addr + buf * Cfg::STG_BYTES;
   if (lane == 0) bulk_wait_read1();
   __syncwarp();
@@ -322,7 +323,7 @@ __device__ __forceinline__ void store_chunk_16(const CUtensorMap* map, uint8_t* 
   fence_proxy_async_shared();
   __syncwarp();
   if (lane == 0) {
-    if (any) tma_store_2d(map, stg + buf * Cfg::STG_BYTES, col0, row0);
+    if (any) tma_store_2d(map, stg + buf * Cfg::STG_BYTES, col0, row0, policy);
     bulk_commit();  // an empty group too: the wait above counts them
   }
   buf ^= 1u;
@@ -488,7 +489,8 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
           w[t] = *reinterpret_cast<const uint32_t*>(&h2);
         }
         const int col = col0 + (u + i) * 32;
-        store_chunk_16<Cfg>(tmC, stg, stg_addr, buf, w, lane, col, row0, row0 < p.m && col < p.n);
+        store_chunk_16<Cfg>(tmC, stg, stg_addr, buf, w, lane, col, row0, row0 < p.m && col < p.n,
+                            p.c_keep ? l2_policy_evict_last() : l2_policy_evict_normal());
       }
     }
   }
@@ -652,6 +654,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             fail = STATUS_TIMEOUT_PRODUCER;
             break;
           }
+          const int k0 = (p.k_splits > 1 ? sg.split + kb * p.k_splits : kb) * Cfg::BK;
           if constexpr (CG == 2) {
             // Both CTAs' loads complete on the leader's barrier; the leader
             // alone announces the pair's bytes.  A peer's bytes may land
@@ -659,13 +662,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // for a moment and the phase still waits for the leader's arrival.
             const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], stage_bytes * CG);
-            load_operand_pair(sA + stage * Cfg::A_STAGE_BYTES, &tmA, fb, kb * Cfg::BK, a_row, BM, p.a_mn, pol);
-            load_operand_pair(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, fb, kb * Cfg::BK, b_row, b_rows,
+            load_operand_pair(sA + stage * Cfg::A_STAGE_BYTES, &tmA, fb, k0, a_row, BM, p.a_mn, pol);
+            load_operand_pair(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, fb, k0, b_row, b_rows,
                               p.b_mn, pol_b);
           } else {
             mbar_arrive_expect_tx(&full[stage], stage_bytes);
-            load_operand(sA + stage * Cfg::A_STAGE_BYTES, &tmA, &full[stage], kb * Cfg::BK, a_row, BM, p.a_mn, pol);
-            load_operand(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, &full[stage], kb * Cfg::BK, b_row, b_rows,
+            load_operand(sA + stage * Cfg::A_STAGE_BYTES, &tmA, &full[stage], k0, a_row, BM, p.a_mn, pol);
+            load_operand(sB + stage * Cfg::B_STAGE_BYTES, p.b_mn ? &tmB : tmb, &full[stage], k0, b_row, b_rows,
                          p.b_mn, pol_b);
           }
           ++issued;
@@ -845,7 +848,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // ((c * 4 + q) * 8 + t) * 32 + lane holds columns 32c + 4t .. 32c + 4t + 3
       // of slab row 32q + lane, so each warp's 32 x 32 chunk is 4 KB of
       // contiguous memory, written and read with bulk copies.
-      if (Cfg::STREAM_K && sg.kb0 > 0 && p.k_splits <= 1) {
+      if (Cfg::STREAM_K && sg.kb0 > 0) {
         uint8_t* slot = reinterpret_cast<uint8_t*>(p.ws) + (static_cast<int64_t>(cluster_id) * CG + rank) * Cfg::SLOT_BYTES;
         const uint32_t fx = Cfg::ROWSTG ? stg_addr + half * Cfg::FX_WARP_BYTES : stg_addr;
         int piece = 0;
