@@ -140,32 +140,32 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     s_col[warp][lane + 32 * i] = col[i];
   }
   __syncwarp();
+  int place[PER] = {};
+#pragma unroll 4
+  for (int o = 0; o < k; ++o) {
+    const int other = s_col[warp][o];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) place[i] += other < col[i] || (other == col[i] && o < lane + 32 * i);
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int j = lane + 32 * i;
-    if (j < k) {
-      int place = 0;
-      for (int o = 0; o < k; ++o) {
-        const int other = s_col[warp][o];
-        place += other < col[i] || (other == col[i] && o < j);
-      }
-      s_sorted[warp][place] = col[i];
-      rows.column[static_cast<int64_t>(row) * k + place] = col[i];
-      rows.q[static_cast<int64_t>(row) * k + place] = q[i];
+    if (lane + 32 * i < k) {
+      s_sorted[warp][place[i]] = col[i];
+      rows.column[static_cast<int64_t>(row) * k + place[i]] = col[i];
+      rows.q[static_cast<int64_t>(row) * k + place[i]] = q[i];
     }
   }
   __syncwarp();
+  const int kept = __reduce_add_sync(0xffffffffu, (col[0] != INT_MAX) + (col[1] != INT_MAX) + (col[2] != INT_MAX) +
+                                                      (col[3] != INT_MAX));
+#pragma unroll 4
   for (int g = lane; g < rows.start_ld; g += 32) {
     // entries with a column below the group's first one (the last group ends past V)
     const int64_t below = static_cast<int64_t>(g) << rows.group_shift;
-    int lo = 0, hi = k;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (s_sorted[warp][mid] < below && s_sorted[warp][mid] != INT_MAX)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
+    int lo = 0;
+#pragma unroll
+    for (int step = kMaxK; step > 0; step >>= 1)
+      if (lo + step <= kept && s_sorted[warp][lo + step - 1] < below) lo += step;
     rows.start[static_cast<int64_t>(row) * rows.start_ld + g] = static_cast<uint8_t>(lo);
   }
 }
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kFinishThreads)
 __global__ void __launch_bounds__(256)
     head_join_kernel(const float* __restrict__ part, int64_t slab, int splits, __nv_bfloat16* __restrict__ out,
                      int64_t ldo, int rows, int cols) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();  // dW loads its operands beside this (PDL_BATCH_NEXT)
   const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
   if (i >= static_cast<int64_t>(rows) * (cols / 4)) return;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -644,12 +644,10 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
                          xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
       return DGL_ERR_CUDA;
 
-    __nv_bfloat16* dx = h.dX ? static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx : nullptr;
-    int splits = 1;    // of dX's sum
-    int64_t slab = 0;  // elements of one
     if (h.dX) {
+      __nv_bfloat16* dx = static_cast<__nv_bfloat16*>(h.dX) + t0 * h.lddx;
       dgl_plan_info plan;
-      splits = choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
+      const int splits = choose_dx_plan(n, h.d, V8, ds->num_sms, &plan);
       Problem px{DGL_DTYPE_BF16, splits > 1 ? DGL_OUT_F32 : DGL_OUT_BF16, e, w, nullptr, nullptr,
                  splits > 1 ? static_cast<void*>(scratch.ws) : dx, n, splits > 1 ? h.d : h.lddx, V8, n, h.d};
       px.b_mn = 1;
@@ -658,10 +656,15 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       px.b_k = h.V;
       px.k_splits = splits;
       px.tight_a = 1;
-      // dW needs nothing of dX: it loads its operands while dX's last tiles run
-      if (h.dW) px.pdl_mode = PDL_BATCH_HEAD;
+      // dW needs nothing of dX: it loads its operands while dX's last tiles, or
+      // the kernel that adds its ranges, run
+      if (h.dW && splits == 1) px.pdl_mode = PDL_BATCH_HEAD;
       if ((st = run(px, &plan, stream, &scratch)) != DGL_OK) return st;
-      slab = round_up(n, plan.tile_m) * h.d;
+      const int64_t slab = round_up(n, plan.tile_m) * h.d;  // elements of a range's sums
+      const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
+      if (splits > 1 && launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream,
+                                         scratch.ws, slab, splits, dx, h.lddx, n, d) != cudaSuccess)
+        return DGL_ERR_CUDA;
     }
     if (h.dW) {
       const bool f32 = dw_sums || h.dw_dtype == DGL_OUT_F32;
@@ -675,12 +678,6 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       pw.c_add = (t0 > 0 || h.accumulate) ? 1 : 0;
       if (h.dX) pw.pdl_mode = PDL_BATCH_NEXT;
       if ((st = run(pw, nullptr, stream)) != DGL_OK) return st;
-    }
-    if (splits > 1) {
-      const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
-      if (launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream, scratch.ws, slab,
-                           splits, dx, h.lddx, n, d) != cudaSuccess)
-        return DGL_ERR_CUDA;
     }
   }
   if (dw_sums) {
