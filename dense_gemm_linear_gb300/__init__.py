@@ -10,7 +10,6 @@ missing, loading raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 from . import metrics  # noqa: F401  (pure-Python metric helpers)
@@ -431,139 +430,12 @@ def linear(A, B, bias=None, out=None, *, act=ACT_NONE, gated=False, sa=None, sb=
 
 
 
-# ---------------------------------------------------------------- losses of a linear head
-def _rows(t, name, dtype, shape):
-    """Checks a CUDA matrix of `shape` whose rows are contiguous; returns its row pitch in elements."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    pitch, step = t.stride()
-    if step != 1 and shape[1] > 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return pitch if shape[0] > 1 else shape[1]
 
-
-def _vector(t, name, dtype, shape):
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}")
-
-
-@functools.lru_cache(maxsize=256)
-def _head_workspace_bytes(T, V, d, grad, dX, dW, dw_dtype, k):
-    h = HeadDesc(T=T, V=V, d=d, grad=grad, dX=dX, dW=dW, dw_dtype=dw_dtype)
-    return max(1, dgl_head_workspace(h, k)[1])
-
-
-def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, k, call, where):
-    import torch
-    if not isinstance(X, torch.Tensor) or X.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
-        raise TypeError("X and W must be 2-D CUDA tensors")
-    T, d = X.shape
-    V = W.shape[0]
-    ldx = _rows(X, "X", torch.bfloat16, (T, d))
-    ldw = _rows(W, "W", torch.bfloat16, (V, d))
-    if stream is not None:
-        # buffers made here belong to the stream that uses them, so the
-        # allocator hands them out again only after its work
-        with torch.cuda.stream(stream):
-            return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate,
-                            workspace, stream.cuda_stream, k, call, where)
-    return _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace,
-                    torch._C._cuda_getCurrentRawStream(X.device.index), k, call, where)
-
-
-def _head_on(X, W, T, V, d, ldx, ldw, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, s, k,
-             call, where):
-    import torch
-    device = X.device
-    loss = torch.empty(T, dtype=torch.float32, device=device)
-    lse = torch.empty(T, dtype=torch.float32, device=device)
-    dX = None
-    p_grad = p_dx = p_dw = lddw = 0
-    dw_type = OUT_BF16
-    if grad is not None:
-        _vector(grad, "grad", torch.float32, (T,))
-        if not (need_dx or need_dw):
-            raise ValueError("a call with grad computes dX, dW or both")
-        p_grad = grad.data_ptr()
-        if need_dx:
-            dX = torch.empty((T, d), dtype=torch.bfloat16, device=device)
-            p_dx = dX.data_ptr()
-        if need_dw:
-            if dW is None:
-                if accumulate:
-                    raise ValueError("accumulate adds to the fp32 dW that is passed in")
-                dW = torch.empty((V, d), dtype=torch.float32 if dw_dtype == OUT_F32 else torch.bfloat16, device=device)
-                lddw = d
-            else:
-                if dW.dtype not in (torch.float32, torch.bfloat16):
-                    raise TypeError(f"dW must be fp32 or bf16, got {dW.dtype}")
-                lddw = _rows(dW, "dW", dW.dtype, (V, d))
-            dw_type = OUT_F32 if dW.dtype == torch.float32 else OUT_BF16
-            p_dw = dW.data_ptr()
-    if not need_dw or grad is None:
-        if dW is not None or accumulate:
-            raise ValueError("dW needs grad, the losses' upstream gradient, and need_dw")
-    if workspace is None:
-        workspace = torch.empty(_head_workspace_bytes(T, V, d, bool(p_grad), bool(p_dx), bool(p_dw), dw_type, k),
-                                dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    h = HeadDesc(T, V, d, X.data_ptr(), ldx, W.data_ptr(), ldw, loss.data_ptr(), lse.data_ptr(), p_grad, p_dx, d, p_dw,
-                 lddw, workspace.data_ptr(), workspace.nbytes, logit_scale, dw_type, int(bool(accumulate)))
-    _check(call(h, s), where)
-    if grad is None:
-        return loss, lse
-    return loss, lse, dX, dW
-
-
-def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_scale=1.0, need_dx=True, need_dw=True,
-                         dW=None, dw_dtype=OUT_BF16, accumulate=False, workspace=None, stream=None):
-    """Softmax cross entropy of the head z = logit_scale X . W^T, without keeping the logits.
-
-    X [T, d], W [V, d] bf16 (rows may be strided), target int64 [T].  Returns
-    (loss, lse), fp32 [T] each.  With grad, fp32 [T], the gradient of the
-    final scalar by each loss (1 / tokens for a mean), returns (loss, lse, dX,
-    dW): dX bf16, dW bf16 or fp32 (dw_dtype, or the type of the dW passed in;
-    accumulate adds to an fp32 dW).  workspace: a CUDA buffer of at least
-    dgl_head_workspace bytes, made when None.
-    """
-    import torch
-    _vector(target, "target", torch.int64, (X.shape[0],))
-    return _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, 0,
-                 lambda h, s: dgl_linear_xent(h, target.data_ptr(), ignore_index, s), "dgl_linear_xent")
-
-
-def linear_distill(X, W, indices, logits, grad=None, *, temperature=1.0, teacher_lse=None, logit_scale=1.0,
-                   need_dx=True, need_dw=True, dW=None, dw_dtype=OUT_BF16, accumulate=False, workspace=None,
-                   stream=None):
-    """Distillation of the head z = logit_scale X . W^T from a teacher's top logits.
-
-    indices int64 [T, k] (negative: absent) and logits fp32 [T, k] are the
-    teacher's; loss_t is the Kullback-Leibler divergence of the student's
-    softmax(z / temperature) from the teacher's distribution over the entries
-    (with teacher_lse, fp32 [T], from its share of the whole vocabulary's).
-    Otherwise as linear_cross_entropy.
-    """
-    import torch
-    T = X.shape[0]
-    k = indices.shape[1] if indices.dim() == 2 else 0
-    if not 1 <= k <= DISTILL_MAX_K:
-        raise ValueError(f"indices must be [T, k] with 1 <= k <= {DISTILL_MAX_K}")
-    _vector(indices, "indices", torch.int64, (T, k))
-    _vector(logits, "logits", torch.float32, (T, k))
-    if teacher_lse is not None:
-        _vector(teacher_lse, "teacher_lse", torch.float32, (T,))
-    return _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, stream, k,
-                 lambda h, s: dgl_linear_distill(h, indices.data_ptr(), logits.data_ptr(),
-                                                 teacher_lse.data_ptr() if teacher_lse is not None else None, k,
-                                                 temperature, s), "dgl_linear_distill")
+def __getattr__(name):
+    # the head losses' helpers (head.py) import torch when they are first used
+    if name in ("linear_cross_entropy", "linear_distill"):
+        from . import head
+        globals()["linear_cross_entropy"] = head.linear_cross_entropy
+        globals()["linear_distill"] = head.linear_distill
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
