@@ -585,6 +585,7 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   p.act = pr.act;
   p.gated = pr.gated;
   p.n_up = static_cast<int>(pr.n);
+  p.out_scale = pr.out_scale;
   p.a_mn = pr.a_mn;
   p.b_mn = pr.b_mn;
   p.idesc_or = pr.w4 ? kIdescE2M1 << 10 : 0u;  // E2M1 in the B format field
@@ -655,7 +656,10 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   if (ds->smem_optin < 232448) return DGL_ERR_UNSUPPORTED;  // every variant is sized for 227 KB
   const bool row_staging = !c_tma && !f32;
   cudaError_t e;
-  if (linear)
+  if (pr.out_scale) {
+    if (e4m3 || linear || !c_tma) return DGL_ERR_UNSUPPORTED;
+    e = launch_tc_scaled(pr.out, plan.tile_m, plan.tile_n, ta, tb, tbh, tc, p, grid, stream);
+  } else if (linear)
     e = e4m3 ? launch_tc_e4m3_epi(pr.out, plan.tile_m, plan.tile_n, row_staging, ta, tb, tbh, tc, p, grid, stream)
              : launch_tc_bf16_epi(pr.out, plan.tile_m, plan.tile_n, row_staging, ta, tb, tbh, tc, p, grid, stream);
   else

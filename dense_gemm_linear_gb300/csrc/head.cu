@@ -7,8 +7,12 @@
 //            columns its largest Y and the sum of 2^(y - Y), the y of the
 //            targets, and for a gradient e = 2^(y - Y) in fp16
 //   finish   (one block per row) S = sum e, lse, loss, and for the gradient
-//            dz = grad s (Q e / S - q) in bf16 in the place of e
-//   dX = dz W, dW = dz^T x  (tile kernel)
+//            dz = (grad s / m) (Q e / S - q) in bf16 in the place of e
+//   dX = m dz W, dW = m dz^T x  (tile kernel)
+// m, between 1 and 2, is the significand of one row's |grad s|: where all rows
+// have the same grad (a mean), grad s / m is a power of two, and the targets'
+// entries, near -grad s in every row that does not predict them, do not all
+// carry the rounding of that one number into dX and dW.
 // T x V values take 2 bytes of workspace for the chunk's tokens, are written
 // twice and read three times; the three products are 6 T V d operations.
 // e needs the 11 bits of fp16 because it is rounded again, as dz, once S is
@@ -170,6 +174,14 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   }
 }
 
+// m of the call: the significand of |grad s| of its first row, of the first 32,
+// with a nonzero grad; lane i holds row i's (0 past the last).  By one warp.
+__device__ __forceinline__ float common_significand(float g) {
+  const uint32_t normal = __ballot_sync(0xffffffffu, fabsf(g) >= 1.17549435e-38f && fabsf(g) < INFINITY);
+  const uint32_t bits = __shfl_sync(0xffffffffu, __float_as_uint(g), normal ? __ffs(normal) - 1 : 0);
+  return normal ? __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u) : 1.0f;
+}
+
 constexpr int kFinishThreads = 256;
 
 // One block per row, and with few rows several, each for a slice of the
@@ -179,6 +191,7 @@ constexpr int kFinishThreads = 256;
 // the row has no gradient (0 x NaN would reach dW).
 __global__ void __launch_bounds__(kFinishThreads)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
+                       const float* __restrict__ first_grad, int first_rows, float* __restrict__ out_scale,
                        float* __restrict__ loss, float* __restrict__ lse_out, uint16_t* __restrict__ e, int64_t lde,
                        const __nv_bfloat16* __restrict__ x, int64_t ldx, __nv_bfloat16* __restrict__ xs, int d,
                        int* __restrict__ flags, int nflags) {
@@ -191,6 +204,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (row == 0 && lead)
     for (int i = threadIdx.x; i < nflags; i += kFinishThreads) flags[i] = 0;
   const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
+  const float g32 = e && lane < first_rows ? first_grad[lane] * scale : 0.0f;
+  const float g_row = e ? grad[row] * scale : 0.0f;
   float m = -INFINITY, s = 0.0f;
   for (int g = threadIdx.x; g < rows.groups; g += kFinishThreads) {
     const float2 v = part[g];
@@ -250,7 +265,9 @@ __global__ void __launch_bounds__(kFinishThreads)
   if (!e) return;
 
   const bool has = state == 1;
-  const float f = has ? grad[row] * scale : 0.0f;
+  const float common = common_significand(g32);
+  if (row == 0 && lead && threadIdx.x == 0) *out_scale = common;
+  const float f = has ? __fdiv_rn(g_row, common) : 0.0f;
   const float fS = f * (Q / S);
   uint16_t* er = e + row * lde;
   uint4* e8 = reinterpret_cast<uint4*>(er);
@@ -317,7 +334,7 @@ __global__ void __launch_bounds__(kFinishThreads)
 // adds four columns of a row.
 __global__ void __launch_bounds__(256)
     head_join_kernel(const float* __restrict__ part, int64_t slab, int splits, __nv_bfloat16* __restrict__ out,
-                     int64_t ldo, int rows, int cols) {
+                     int64_t ldo, int rows, int cols, const float* __restrict__ scale) {
   griddep_wait();
   griddep_launch_dependents();  // dW loads its operands beside this (PDL_BATCH_NEXT)
   const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
@@ -331,7 +348,8 @@ __global__ void __launch_bounds__(256)
     s.z += v.z;
     s.w += v.w;
   }
-  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
+  const float m = *scale;
+  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x * m, s.y * m), __floats2bfloat162_rn(s.z * m, s.w * m)};
   const int64_t r = i / (cols / 4), c = i % (cols / 4) * 4;
   *reinterpret_cast<uint2*>(out + r * ldo + c) = *reinterpret_cast<const uint2*>(o);
 }
@@ -375,7 +393,7 @@ struct HeadLayout {
   int64_t chunk = 0;  // tokens at a time (0: does not fit)
   int64_t lde = 0;    // row pitch of e, elements
   int64_t e = 0, xs = 0, pick = 0, part = 0, column = 0, q = 0, sums = 0, start = 0;
-  int64_t split = 0, flags = 0, dw = 0;
+  int64_t split = 0, flags = 0, out_scale = 0, dw = 0;
   int64_t bytes = 0;
 };
 
@@ -437,6 +455,7 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
     l.xs = take(rows * h.d * 2);
     l.split = take(int64_t(kSplitSlots) * 128 * 256 * 4);
     l.flags = take(kSplitSlots * 4);
+    l.out_scale = take(4);
   }
   l.part = take(std::max(rows * groups, narrow) * 8);
   l.pick = take(rows * std::max(k, 1) * 4);
@@ -522,6 +541,18 @@ int choose_dx_plan(int64_t m, int64_t n, int64_t K, int num_sms, dgl_plan_info* 
   return best_splits;
 }
 
+// dW's tile: the cost model's cheapest.
+void choose_dw_plan(int64_t m, int64_t n, int64_t K, bool f32, int num_sms, dgl_plan_info* out) {
+  bool have = false;
+  for (int tile_m : {128, 256})
+    for (int tile_n : {128, 256}) {
+      dgl_plan_info cand;
+      fill_tc_plan(DGL_DTYPE_BF16, f32 ? DGL_OUT_F32 : DGL_OUT_BF16, m, n, K, tile_m, tile_n, num_sms, &cand, 0);
+      if (!have || cand.est_us <= out->est_us) *out = cand;
+      have = true;
+    }
+}
+
 dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float scale, cudaStream_t stream) {
   HeadTargets tg = targets;
   dgl_status st = check_extents(hp, tg.k);
@@ -564,6 +595,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
   scratch.ws_bytes = size_t(kSplitSlots) * 128 * 256 * 4;
   scratch.flags = reinterpret_cast<int*>(ws + lay.flags);
   scratch.nflags = kSplitSlots;
+  float* out_scale = reinterpret_cast<float*>(ws + lay.out_scale);
   const int V = static_cast<int>(h.V), d = static_cast<int>(h.d);
   const int64_t V8 = round_up(h.V, 8);
   const float c = scale * kLog2e;
@@ -640,7 +672,8 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     const int64_t slices = grad ? std::min<int64_t>(int64_t(8) * ds->num_sms / n, h.V / 2048) : 1;
     const dim3 finish(static_cast<unsigned>(n), static_cast<unsigned>(std::max<int64_t>(1, slices)));
     if (launch_dependent(head_finish_kernel, finish, kFinishThreads, stream, tg, rows, V, scale, c,
-                         grad ? h.grad + t0 : nullptr, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
+                         grad ? h.grad + t0 : nullptr, h.grad, static_cast<int>(std::min<int64_t>(h.T, 32)), out_scale,
+                         h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
                          xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
       return DGL_ERR_CUDA;
 
@@ -656,6 +689,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       px.b_k = h.V;
       px.k_splits = splits;
       px.tight_a = 1;
+      px.out_scale = splits > 1 ? nullptr : out_scale;  // else by the adding kernel
       // dW needs nothing of dX: it loads its operands while dX's last tiles, or
       // the kernel that adds its ranges, run
       if (h.dW && splits == 1) px.pdl_mode = PDL_BATCH_HEAD;
@@ -663,7 +697,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       const int64_t slab = round_up(n, plan.tile_m) * h.d;  // elements of a range's sums
       const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
       if (splits > 1 && launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream,
-                                         scratch.ws, slab, splits, dx, h.lddx, n, d) != cudaSuccess)
+                                         scratch.ws, slab, splits, dx, h.lddx, n, d, out_scale) != cudaSuccess)
         return DGL_ERR_CUDA;
     }
     if (h.dW) {
@@ -677,7 +711,10 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       pw.k_any = 1;
       pw.c_add = (t0 > 0 || h.accumulate) ? 1 : 0;
       if (h.dX) pw.pdl_mode = PDL_BATCH_NEXT;
-      if ((st = run(pw, nullptr, stream)) != DGL_OK) return st;
+      pw.out_scale = out_scale;
+      dgl_plan_info plan;
+      choose_dw_plan(h.V, h.d, n, f32, ds->num_sms, &plan);
+      if ((st = run(pw, &plan, stream)) != DGL_OK) return st;
     }
   }
   if (dw_sums) {

@@ -54,6 +54,9 @@ struct Problem {
   // 1: K need not be whole 16-byte units (both operands MN-major: K is their
   // outer extent, and rows past it read as zeros)
   int k_any = 0;
+  // bf16 operands, a TMA-stored C on 128- or 256-wide tiles: factor of every
+  // element (device scalar); else null
+  const float* out_scale = nullptr;
   // 1: A's box holds only the rows that exist when those are fewer than the tile's
   int tight_a = 0;
   // > 1: the sum over K in this many ranges, each with an fp32 C of its own:

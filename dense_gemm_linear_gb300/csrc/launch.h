@@ -61,6 +61,11 @@ cudaError_t launch_tc_mxfp4(int out, bool row_staging, const CUtensorMap& ta, co
 // 128 x 256 and 128 x 128.
 cudaError_t launch_tc_head(bool store, int tile_m, int tile_n, const CUtensorMap& ta, const CUtensorMap& tb,
                            const CUtensorMap& tc, const TcParams& p, int grid, cudaStream_t stream);
+// bf16 GEMM whose elements are scaled by p.out_scale, TMA stores only: 128- and
+// 256-row tiles, 128 or 256 wide.
+cudaError_t launch_tc_scaled(int out, int tile_m, int tile_n, const CUtensorMap& ta, const CUtensorMap& tb,
+                             const CUtensorMap& tbh, const CUtensorMap& tc, const TcParams& p, int grid,
+                             cudaStream_t stream);
 // Decode kernel: ta = A map (16-row box), tb_lo / tb_hi = B maps whose box
 // heights are the two part sizes floor(n/parts) and ceil(n/parts).
 cudaError_t launch_decode(int dtype, int out, const CUtensorMap& ta, const CUtensorMap& tb_lo,

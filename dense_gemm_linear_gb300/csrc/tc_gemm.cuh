@@ -67,9 +67,13 @@ struct TcConfig {
   // EPI: the linear-layer epilogue (bias, activation, and on CTA pairs the
   // gated up projection) is compiled in; plain GEMM variants leave it out.
   static constexpr bool EPI = EPI_;
-  // HEAD: the epilogue of a linear head's logits (HeadEpi) takes the place of
-  // the others': 1 statistics only, 2 the exponentials are stored too.
+  // HEAD: kernels of a linear head's losses.  1, 2: the logits' epilogue
+  // (HeadEpi) takes the place of the others', 1 statistics only, 2 the
+  // exponentials are stored too; 3: a plain GEMM whose elements are scaled by
+  // out_scale (1024 x 50257 x 512's dW: 46 us, 49 us with the linear layer's
+  // epilogue, whose activations it does not need).
   static constexpr int HEAD = HEAD_;
+  static constexpr bool LOGITS = HEAD_ == 1 || HEAD_ == 2;
   // Rows of C per CTA: 128, or 64 for the small rungs of the ladder (one CTA,
   // an M = 64 MMA).  An M = 64 accumulator puts row 16 q + r (r < 16) in
   // tensor-memory lane 32 q + r, so each epilogue warp of lane quarter q holds
@@ -144,8 +148,9 @@ struct TcConfig {
   static_assert(BN == 64 || BN == 128 || BN == 256 || (BN == 224 && CG == 2 && !EPI && !MX),
                 "tile widths of the ladder (224: plain GEMM on CTA pairs)");
   static_assert(BM == 128 || (BM == 64 && CG == 1 && !EPI && !MX), "64-row tiles: one CTA, plain GEMM");
-  static_assert(HEAD == 0 || (!FP8_ && !EPI && !MX && !ROWSTG_ && !OUT_F32_ && BM_ == 128 && BN_ % 128 == 0),
-                "head variants: bf16 operands, TMA-stored 16-bit output");
+  static_assert(HEAD == 0 || (!FP8_ && !EPI && !MX && !ROWSTG_ && BM_ == 128 && BN_ % 128 == 0),
+                "head variants: bf16 operands, TMA-stored output");
+  static_assert(!LOGITS || !OUT_F32_, "the logits' epilogue stores 16-bit values");
   static_assert(STAGES >= 3, "ring too shallow");
   static_assert((ROW_PITCH / 16) % 2 == 1, "row pitch: odd multiple of 16 bytes");
   static_assert(TMEM_COLS == 128 || TMEM_COLS == 256 || TMEM_COLS == 512, "TMEM allocation: power of two");
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_last();
-      const uint64_t pol_b = Cfg::HEAD != 0 && p.b_once ? l2_policy_evict_first() : pol;
+      const uint64_t pol_b = Cfg::LOGITS && p.b_once ? l2_policy_evict_first() : pol;
       uint32_t stage = 0, phase = 0;
       int64_t issued = 0;
       SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
@@ -801,6 +806,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     // C, the split schedule's workspace and its flags are written here only
     if (p.pdl_mode == PDL_BATCH_NEXT) griddep_wait();
+    const float out_scale = Cfg::HEAD == 3 ? *p.out_scale : 1.0f;
     const int e = warp - 2;                 // 0..7
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31 are reachable from this warp
     const int half = e >> 2;                // this warp takes chunks [c_first, c_first + nc)
@@ -818,7 +824,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       int mb, nb;
       tile_coords(sg.tile, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
       HeadPicks want;
-      if constexpr (Cfg::HEAD != 0)
+      if constexpr (Cfg::LOGITS)
         want = head_picks(p, mb * Cfg::TILE_M + static_cast<int>(rank) * BM + q * 32 + lane, 2 * nb + half, BN / 2);
       // all lanes decide together: tcgen05.ld below is warp-collective
       bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase));
@@ -1084,13 +1090,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       };
 
-      if constexpr (Cfg::HEAD != 0) {
+      if constexpr (Cfg::LOGITS) {
         head_epilogue<Cfg>(p, &tmC, t_row + half * (BN / 2), row0, 2 * nb + half, want, lane, stg, stg_addr, head_buf,
                            hand_back);
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
-      bool gated_done = Cfg::HEAD != 0;
+      bool gated_done = Cfg::LOGITS;
       if constexpr (BN == 256) {
         if (sg.half) {
           // ---- a half tile of the split tail: BN / 2 columns in TMEM
@@ -1111,6 +1117,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j)
                 v[j] = __float_as_uint((__uint_as_float(v[j]) * row_scale) * __shfl_sync(0xffffffffu, col_scale, j));
+            }
+            if constexpr (Cfg::HEAD == 3) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * out_scale);
             }
             if constexpr (Cfg::EPI) {
               if (p.act != 0 || p.bias != nullptr) {
@@ -1192,6 +1202,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 r[uu][j] = __float_as_uint((__uint_as_float(r[uu][j]) * row_scale) *
                                            __shfl_sync(0xffffffffu, col_scale, j));
             }
+          }
+          if constexpr (Cfg::HEAD == 3) {
+#pragma unroll
+            for (int uu = 0; uu < G; ++uu)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[uu][j] = __float_as_uint(__uint_as_float(r[uu][j]) * out_scale);
           }
           if (Cfg::EPI && epi) {
             // linear-layer epilogue: bias per column, then the activation
