@@ -41,8 +41,8 @@ struct HeadEpi {
   int part_ld;
   // Accumulators to pick out of the tile, [rows][k] into pick: one target per
   // row (start null; others than 0 .. n - 1 are not picked), or the row's k
-  // sorted columns, of which group g holds number start[row][g] up to
-  // start[row][g + 1].
+  // sorted columns, of which the tile of columns t BN .. t BN + BN - 1 holds
+  // number start[row][t] up to start[row][t + 1].
   const int64_t* target;
   const int* column;
   const uint8_t* start;

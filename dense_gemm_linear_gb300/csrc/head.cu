@@ -56,8 +56,9 @@ struct HeadRows {
   int* column;       // [rows][k] kept entries sorted by column, then INT_MAX
   float* q;          // [rows][k] their weights
   float4* sums;      // [rows] Q, sum q log q, state (1: has a loss, 0: none, -1: index out of range), 0
-  uint8_t* start;    // [rows][start_ld] entries before each column group
-  int start_ld, group_shift;  // a group is 2^group_shift columns
+  uint8_t* start;    // [rows][start_ld] entries before each tile of columns
+  int start_ld;
+  int group_shift;   // a group is 2^group_shift columns, half a tile
   float* pick;       // [rows][max(k, 1)] accumulators of the entries
   float2* part;      // [rows][groups] (largest y, sum of the exponentials)
   int groups;
@@ -78,7 +79,7 @@ constexpr int kPrepareWarps = 4;
 
 // Distill, one warp per row: the teacher's distribution over the row's entries
 // in fp32 (maximum first), the entries sorted by column, and the number of them
-// before each column group.
+// before each tile of columns.
 __global__ void __launch_bounds__(32 * kPrepareWarps)
     head_prepare_kernel(HeadTargets tg, HeadRows rows, int n, int V) {
   // everything before is done once the logits' kernel may start: it loads its
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
                                                       (col[3] != INT_MAX));
 #pragma unroll 4
   for (int g = lane; g < rows.start_ld; g += 32) {
-    // entries with a column below the group's first one (the last group ends past V)
-    const int64_t below = static_cast<int64_t>(g) << rows.group_shift;
+    // entries with a column below the tile's first one (the last tile ends past V)
+    const int64_t below = static_cast<int64_t>(g) << (rows.group_shift + 1);
     int lo = 0;
 #pragma unroll
     for (int step = kMaxK; step > 0; step >>= 1)
@@ -212,6 +213,18 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
   const float g32 = e && lane < first_rows ? first_grad[lane] * scale : 0.0f;
   const float g_row = e ? grad[row] * scale : 0.0f;
+  int state;
+  float Q = 1.0f, l = 0.0f;
+  int64_t y0 = 0;
+  if (tg.k == 0) {
+    y0 = tg.index[row];
+    state = y0 == tg.ignore_index ? 0 : y0 >= 0 && y0 < V ? 1 : -1;
+  } else {
+    const float4 sums = rows.sums[row];
+    Q = sums.x;
+    l = sums.y;
+    state = static_cast<int>(sums.z);
+  }
   float m = -INFINITY, s = 0.0f;
   for (int g = threadIdx.x; g < rows.groups; g += kFinishThreads) {
     const float2 v = part[g];
@@ -236,22 +249,10 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float log_S = log2f(S);
 
   // the row's targets
-  int state;
-  float Q = 1.0f, l = 0.0f;
   const int k = tg.k == 0 ? 1 : tg.k;
   const float* pick = rows.pick + static_cast<int64_t>(row) * k;
   const int* column = tg.k == 0 ? nullptr : rows.column + static_cast<int64_t>(row) * k;
   const float* q = tg.k == 0 ? nullptr : rows.q + static_cast<int64_t>(row) * k;
-  int64_t y0 = 0;
-  if (tg.k == 0) {
-    y0 = tg.index[row];
-    state = y0 == tg.ignore_index ? 0 : y0 >= 0 && y0 < V ? 1 : -1;
-  } else {
-    const float4 sums = rows.sums[row];
-    Q = sums.x;
-    l = sums.y;
-    state = static_cast<int>(sums.z);
-  }
   if (warp == 0 && lead) {
     // sum_k q (lse - z_k) as base - y_k + log2 S: what a likely target's y has
     // in common with the maximum cancels before anything is rounded
@@ -625,7 +626,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       rows.q = reinterpret_cast<float*>(ws + lay.q);
       rows.sums = reinterpret_cast<float4*>(ws + lay.sums);
       rows.start = ws + lay.start;
-      rows.start_ld = rows.groups + 1;
+      rows.start_ld = rows.groups / 2 + 1;
     }
 
     if (tg.k > 0 && launch_dependent(head_prepare_kernel, static_cast<unsigned>((n + kPrepareWarps - 1) / kPrepareWarps),

@@ -35,8 +35,9 @@
 //              partial 16-byte units at its two ends take 2-byte stores.
 //              The staging transpose is section 7.2's "CShuffle" idea: re-map
 //              threads so each store covers contiguous columns of a row.
-//   warps 10-13 (MXFP4 only) gather each stage's E8M0 scales into shared
-//              memory for the MMA thread to copy into tensor memory.
+//   warps 10-13 (MXFP4) gather each stage's E8M0 scales into shared memory
+//              for the MMA thread to copy into tensor memory, or (head logits)
+//              pick single accumulators out of a tile.
 // The two accumulators let the epilogue of tile t overlap the main loop of
 // tile t+1 (the MXFP4 variant has one: see TcConfig).
 #pragma once
@@ -125,7 +126,10 @@ struct TcConfig {
   static constexpr int SCALE_STAGE_BYTES = 512 * SCALE_ATOMS;
   static constexpr int STAGES = tc_ring_stages(STAGE_BYTES + SCALE_STAGE_BYTES, STG_TOTAL);
   static constexpr int SCALE_WARPS = MX ? 4 : 0;
-  static constexpr int THREADS = 64 + EPI_WARPS * 32 + SCALE_WARPS * 32;
+  // LOGITS: warps that pick the targets' accumulators out of a tile beside the
+  // epilogue, one per lane quarter
+  static constexpr int PICK_WARPS = LOGITS ? 4 : 0;
+  static constexpr int THREADS = 64 + (EPI_WARPS + SCALE_WARPS + PICK_WARPS) * 32;
   // fp32 accumulators of BN columns: two, so the epilogue of one tile
   // overlaps the main loop of the next, or one with MX 128 x 256 tiles
   static constexpr int ACC_BUFS = MX && BN == 256 ? 1 : 2;
@@ -361,31 +365,78 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// The accumulators that a row wants picked out of one column group: entries
-// first .. last - 1 of its sorted columns, the first at column `at` of the
-// group (or its one target).  Read before the tile's products are waited for.
+// The accumulators that a row wants picked out of one tile: entries first ..
+// last - 1 of its sorted columns, or its one target, at column `at` of the tile.
 struct HeadPicks {
   int first = 0, last = 0, at = 0;
 };
 
-__device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int group, int cols) {
+__device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int nb, int cols) {
   const HeadEpi& h = p.head;
   HeadPicks k;
   if (row >= p.m) return k;
-  const int col0 = group * cols;
   if (h.start) {
-    const uint8_t* st = h.start + static_cast<int64_t>(row) * h.start_ld + group;
+    const uint8_t* st = h.start + static_cast<int64_t>(row) * h.start_ld + nb;
     k.first = st[0];
     k.last = st[1];
-    if (k.first < k.last) k.at = h.column[static_cast<int64_t>(row) * h.k + k.first] - col0;
   } else if (h.target) {
-    const int64_t y = h.target[row];
-    if (y >= col0 && y < min(col0 + cols, p.n)) {
-      k.at = static_cast<int>(y) - col0;
+    const int64_t y = h.target[row], col0 = static_cast<int64_t>(nb) * cols;
+    if (y >= col0 && y < min(col0 + cols, static_cast<int64_t>(p.n))) {
+      k.at = static_cast<int>(y - col0);
       k.last = 1;
     }
   }
   return k;
+}
+
+// Picks them, by one warp for its 32 rows of the tile at tensor-memory address
+// t0 (row0: the first).  The rows' entries are taken 32 at a time, one per
+// lane, whichever rows they belong to, so that a row with many entries in one
+// tile (frequent tokens have neighbouring numbers) costs no chain of its own:
+// their columns are read at once; each column is then read out of tensor memory
+// for all 32 rows, eight in flight, and the entry's row hands its value over.
+__device__ __forceinline__ void head_pick(const HeadEpi& h, HeadPicks want, uint32_t t0, int row0, int col0, int lane) {
+  constexpr uint32_t ALL = 0xFFFFFFFFu;
+  const int count = want.last - want.first;
+  if (!__any_sync(ALL, count > 0)) return;
+  int upto = count;  // entries of this row and the ones before it
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(ALL, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const int total = __shfl_sync(ALL, upto, 31);
+#pragma unroll 1
+  for (int base = 0; base < total; base += 32) {
+    // the row of entry base + lane: the first whose entries reach past it
+    const int mine = base + lane;
+    int r = 0;
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1)
+      if (__shfl_sync(ALL, upto, r + step - 1) <= mine) r += step;
+    const int nth = mine - __shfl_sync(ALL, upto - count, r);
+    const int64_t slot = static_cast<int64_t>(row0 + r) * h.k + __shfl_sync(ALL, want.first, r) + nth;
+    int col = __shfl_sync(ALL, want.at, r);
+    if (h.start && mine < total) col = h.column[slot] - col0;
+    const int n = min(32, total - base);
+    uint32_t value = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < n) tmem_ld_32x32b_x1(t0 + __shfl_sync(ALL, col, i + j), v[j]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < n) {
+          asm volatile("" : "+r"(v[j]));  // not used before the wait
+          const uint32_t x = __shfl_sync(ALL, v[j], __shfl_sync(ALL, r, i + j));
+          if (lane == i + j) value = x;
+        }
+    }
+    if (mine < total) h.pick[slot] = __uint_as_float(value);
+  }
 }
 
 // One warp's share (32 rows x BN / 2 columns, one group) of a tile of head
@@ -399,7 +450,7 @@ __device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int 
 // all): more warps compete with the one that issues the MMAs.
 template <class Cfg, class HandBack>
 __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorMap* tmC, uint32_t t0, int row0, int group,
-                                              HeadPicks want, int lane, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
+                                              int lane, uint8_t* stg, uint32_t stg_addr, uint32_t& buf,
                                               HandBack hand_back) {
   constexpr int GW = Cfg::BN / 2;       // columns of the group
   constexpr int NC = GW / 32;           // its 32-column chunks, taken two at a time
@@ -408,19 +459,6 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
   const int col0 = group * GW;
   const float c = fabsf(h.c);
   const bool flip = h.c < 0.0f;
-
-  // The warp reads one column of all its rows at a time, the row that wants
-  // it keeps its own.
-  for (uint32_t who = __ballot_sync(0xffffffffu, want.first < want.last); who != 0;
-       who = __ballot_sync(0xffffffffu, want.first < want.last)) {
-    const int src = __ffs(who) - 1;
-    const uint32_t v = tmem_ld_32x32b_x1(t0 + __shfl_sync(0xffffffffu, want.at, src));
-    if (lane == src) {
-      h.pick[static_cast<int64_t>(row) * h.k + want.first] = __uint_as_float(v);
-      ++want.first;
-      if (want.first < want.last) want.at = h.column[static_cast<int64_t>(row) * h.k + want.first] - col0;
-    }
-  }
 
   auto load = [&](uint32_t(&r)[2][32], int u) {
     tmem_ld_32x32b_x32(t0 + u * 32, r[0]);
@@ -553,7 +591,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], Cfg::EPI_WARPS * CG);
+      mbar_init(&tempty[b], (Cfg::EPI_WARPS + Cfg::PICK_WARPS) * CG);
     }
     mbar_init(drain, 1);
     mbar_init(fixbar, 1);
@@ -823,9 +861,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     while (it.next(sg)) {
       int mb, nb;
       tile_coords(sg.tile, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
-      HeadPicks want;
-      if constexpr (Cfg::LOGITS)
-        want = head_picks(p, mb * Cfg::TILE_M + static_cast<int>(rank) * BM + q * 32 + lane, 2 * nb + half, BN / 2);
       // all lanes decide together: tcgen05.ld below is warp-collective
       bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase));
       if constexpr (Cfg::ROWSTG) {
@@ -1091,8 +1126,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       };
 
       if constexpr (Cfg::LOGITS) {
-        head_epilogue<Cfg>(p, &tmC, t_row + half * (BN / 2), row0, 2 * nb + half, want, lane, stg, stg_addr, head_buf,
-                           hand_back);
+        head_epilogue<Cfg>(p, &tmC, t_row + half * (BN / 2), row0, 2 * nb + half, lane, stg, stg_addr, head_buf, hand_back);
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
@@ -1292,6 +1326,52 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
     }
     if ((Cfg::ROWSTG ? half == 0 : (p.c_tma && lane == 0))) bulk_wait0();
+  }
+
+  if constexpr (Cfg::LOGITS) {
+    if (warp >= 2 + Cfg::EPI_WARPS) {
+      // ----------------------------------------------------------- pick warps
+      // In the epilogue's warps the picks' chain of dependent reads (which, at
+      // which column, tensor memory) would be added to every tile's time.
+      if (p.pdl_mode == PDL_BATCH_NEXT) griddep_wait();
+      const int q = warp & 3;
+      uint32_t acc = 0, acc_phase = 0;
+      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
+                     p.k_splits);
+      Segment sg;
+      HeadPicks ahead;
+      auto look = [&](int& row, int& nb) {  // the next tile's picks; row -1 after the last
+        row = -1;
+        if (!it.next(sg)) return;
+        int mb;
+        tile_coords(sg.tile, p.tiles_m, p.tiles_n, p.group_m, mb, nb);
+        row = mb * Cfg::TILE_M + static_cast<int>(rank) * BM + q * 32 + lane;
+        ahead = head_picks(p, row, nb, BN);
+      };
+      int next_row, next_nb;
+      look(next_row, next_nb);
+      while (next_row >= 0) {
+        const int row = next_row, nb = next_nb;
+        const HeadPicks want = ahead;
+        look(next_row, next_nb);  // read while this tile is waited for
+        if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase))) {
+          fail = STATUS_TIMEOUT_EPILOGUE;
+          break;
+        }
+        tc_fence_after_sync();
+        head_pick(p.head, want, tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * Cfg::ACC_STRIDE,
+                  row - lane, nb * BN, lane);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+        next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
+      }
+    }
   }
 
   if constexpr (Cfg::MX) {
