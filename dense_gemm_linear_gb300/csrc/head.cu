@@ -38,6 +38,7 @@ namespace dgl {
 namespace {
 
 constexpr int kMaxK = DGL_DISTILL_MAX_K;
+constexpr int kAbsent = INT_MAX - 1;  // the column of an absent entry; one more does not overflow
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -53,7 +54,7 @@ struct HeadTargets {
 
 // A chunk's rows: what `prepare` (distill only) and the logits' epilogue leave.
 struct HeadRows {
-  int* column;       // [rows][k] kept entries sorted by column, then INT_MAX
+  int* column;       // [rows][k] kept entries sorted by column, then kAbsent
   float* q;          // [rows][k] their weights
   float4* sums;      // [rows] Q, sum q log q, state (1: has a loss, 0: none, -1: index out of range), 0
   uint8_t* start;    // [rows][start_ld] entries before each tile of columns
@@ -80,15 +81,16 @@ constexpr int kPrepareWarps = 4;
 // Distill, one warp per row: the teacher's distribution over the row's entries
 // in fp32 (maximum first), the entries sorted by column, and the number of them
 // before each tile of columns.
+// PER: entries a lane holds (k at most 32 PER).
+template <int PER>
 __global__ void __launch_bounds__(32 * kPrepareWarps)
     head_prepare_kernel(HeadTargets tg, HeadRows rows, int n, int V) {
   // everything before is done once the logits' kernel may start: it loads its
   // operands beside this one and waits for it in its epilogue (PDL_BATCH_NEXT)
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int PER = kMaxK / 32;
-  __shared__ int s_col[kPrepareWarps][kMaxK];
-  __shared__ int s_sorted[kPrepareWarps][kMaxK];
+  __shared__ __align__(16) int s_col[kPrepareWarps][32 * PER];
+  __shared__ int s_sorted[kPrepareWarps][32 * PER];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * kPrepareWarps + warp;
   if (row >= n) return;
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int j = lane + 32 * i;
-    col[i] = INT_MAX;
+    col[i] = kAbsent;
     l[i] = -INFINITY;
     if (j < k) {
       const int64_t c64 = tg.index[static_cast<int64_t>(row) * k + j];
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   const float base = tg.teacher_lse ? tg.teacher_lse[row] : high;
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sum += col[i] != INT_MAX ? expf(l[i] - base) : 0.0f;
+  for (int i = 0; i < PER; ++i) sum += col[i] != kAbsent ? expf(l[i] - base) : 0.0f;
   sum = warp_sum(sum);
   const float log_total = tg.teacher_lse ? base : base + logf(sum);
   float Q = 0.0f, qlogq = 0.0f;
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const float lq = l[i] - log_total;
-    q[i] = col[i] != INT_MAX ? expf(lq) : 0.0f;
+    q[i] = col[i] != kAbsent ? expf(lq) : 0.0f;
     Q += q[i];
     qlogq += q[i] != 0.0f ? q[i] * lq : 0.0f;
   }
@@ -141,16 +143,20 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   // sort by (column, position): an entry's place is the number before it
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (state != 1) col[i] = INT_MAX;
+    if (state != 1) col[i] = kAbsent;
     s_col[warp][lane + 32 * i] = col[i];
   }
   __syncwarp();
+  // (entries past k are kAbsent, and come after every entry before k)
   int place[PER] = {};
-#pragma unroll 4
-  for (int o = 0; o < k; ++o) {
-    const int other = s_col[warp][o];
+#pragma unroll 2
+  for (int o = 0; o < k; o += 4) {
+    const int4 four = *reinterpret_cast<const int4*>(&s_col[warp][o]);
+    const int other[4] = {four.x, four.y, four.z, four.w};
 #pragma unroll
-    for (int i = 0; i < PER; ++i) place[i] += other < col[i] || (other == col[i] && o < lane + 32 * i);
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) place[i] += other[v] < col[i] + (o + v < lane + 32 * i);
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -161,15 +167,17 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
     }
   }
   __syncwarp();
-  const int kept = __reduce_add_sync(0xffffffffu, (col[0] != INT_MAX) + (col[1] != INT_MAX) + (col[2] != INT_MAX) +
-                                                      (col[3] != INT_MAX));
+  int kept = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) kept += col[i] != kAbsent;
+  kept = __reduce_add_sync(0xffffffffu, kept);
 #pragma unroll 4
   for (int g = lane; g < rows.start_ld; g += 32) {
     // entries with a column below the tile's first one (the last tile ends past V)
     const int64_t below = static_cast<int64_t>(g) << (rows.group_shift + 1);
     int lo = 0;
 #pragma unroll
-    for (int step = kMaxK; step > 0; step >>= 1)
+    for (int step = 32 * PER; step > 0; step >>= 1)
       if (lo + step <= kept && s_sorted[warp][lo + step - 1] < below) lo += step;
     rows.start[static_cast<int64_t>(row) * rows.start_ld + g] = static_cast<uint8_t>(lo);
   }
@@ -259,7 +267,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     float t = 0.0f;
     if (state == 1)
       for (int j = lane; j < k; j += 32) {
-        if (tg.k != 0 && column[j] == INT_MAX) continue;
+        if (tg.k != 0 && column[j] == kAbsent) continue;
         const float w = tg.k == 0 ? 1.0f : q[j];
         if (w != 0.0f) t += w * ((base - pick[j] * c) + log_S);
       }
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     if (tg.k != 0) {
       // entries of one column are neighbours: the first carries their weights
       v = column[j];
-      if (v == INT_MAX || (j > 0 && column[j - 1] == v)) continue;
+      if (v == kAbsent || (j > 0 && column[j - 1] == v)) continue;
       w = 0.0f;
       for (int o = j; o < k && column[o] == v; ++o) w += q[o];
     }
@@ -629,8 +637,11 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       rows.start_ld = rows.groups / 2 + 1;
     }
 
-    if (tg.k > 0 && launch_dependent(head_prepare_kernel, static_cast<unsigned>((n + kPrepareWarps - 1) / kPrepareWarps),
-                                     32 * kPrepareWarps, stream, tg, rows, n, V) != cudaSuccess)
+    if (tg.k > 0 && launch_dependent(tg.k <= 32   ? head_prepare_kernel<1>
+                                     : tg.k <= 64 ? head_prepare_kernel<2>
+                                                  : head_prepare_kernel<4>,
+                                     static_cast<unsigned>((n + kPrepareWarps - 1) / kPrepareWarps), 32 * kPrepareWarps,
+                                     stream, tg, rows, n, V) != cudaSuccess)
       return DGL_ERR_CUDA;
 
     // ---- logits
