@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   griddep_launch_dependents();
   griddep_wait();
   constexpr int WARPS = kFinishThreads / 32;
-  __shared__ float red[2][WARPS];
+  __shared__ float red[3][WARPS];
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool lead = blockIdx.y == 0;
   if (row == 0 && lead)
@@ -221,18 +221,35 @@ __global__ void __launch_bounds__(kFinishThreads)
   const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
   const float g32 = e && lane < first_rows ? first_grad[lane] * scale : 0.0f;
   const float g_row = e ? grad[row] * scale : 0.0f;
+  // the row's targets, entry j (of k, at most kMaxK) with thread j: its column
+  // (-1: none), weight and y
+  static_assert(kFinishThreads >= kMaxK, "an entry a thread");
+  const int k = tg.k == 0 ? 1 : tg.k;
   int state;
-  float Q = 1.0f, l = 0.0f;
-  int64_t y0 = 0;
+  float Q = 1.0f, l = 0.0f, weight = 0.0f, y = 0.0f;
+  int64_t at = -1;
+  int before = -1;  // the column of entry j - 1
   if (tg.k == 0) {
-    y0 = tg.index[row];
-    state = y0 == tg.ignore_index ? 0 : y0 >= 0 && y0 < V ? 1 : -1;
+    const int64_t target = tg.index[row];
+    state = target == tg.ignore_index ? 0 : target >= 0 && target < V ? 1 : -1;
+    if (state == 1 && threadIdx.x == 0) {
+      at = target;
+      weight = 1.0f;
+    }
   } else {
     const float4 sums = rows.sums[row];
     Q = sums.x;
     l = sums.y;
     state = static_cast<int>(sums.z);
+    if (state == 1 && threadIdx.x < k) {
+      const int64_t slot = static_cast<int64_t>(row) * k + threadIdx.x;
+      const int col = rows.column[slot];
+      at = col == kAbsent ? -1 : col;
+      weight = rows.q[slot];
+      if (threadIdx.x > 0) before = rows.column[slot - 1];
+    }
   }
+  if (at >= 0) y = rows.pick[static_cast<int64_t>(row) * k + threadIdx.x] * c;
   float m = -INFINITY, s = 0.0f;
   for (int g = threadIdx.x; g < rows.groups; g += kFinishThreads) {
     const float2 v = part[g];
@@ -256,26 +273,18 @@ __global__ void __launch_bounds__(kFinishThreads)
   S *= exp2f(-kHeadShift);  // relative to 2^base
   const float log_S = log2f(S);
 
-  // the row's targets
-  const int k = tg.k == 0 ? 1 : tg.k;
-  const float* pick = rows.pick + static_cast<int64_t>(row) * k;
-  const int* column = tg.k == 0 ? nullptr : rows.column + static_cast<int64_t>(row) * k;
-  const float* q = tg.k == 0 ? nullptr : rows.q + static_cast<int64_t>(row) * k;
-  if (warp == 0 && lead) {
+  if (threadIdx.x < ((k + 31) & ~31)) {
     // sum_k q (lse - z_k) as base - y_k + log2 S: what a likely target's y has
     // in common with the maximum cancels before anything is rounded
+    const float t = warp_sum(at >= 0 && weight != 0.0f ? weight * ((base - y) + log_S) : 0.0f);
+    if (lane == 0) red[2][warp] = t;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && lead) {
     float t = 0.0f;
-    if (state == 1)
-      for (int j = lane; j < k; j += 32) {
-        if (tg.k != 0 && column[j] == kAbsent) continue;
-        const float w = tg.k == 0 ? 1.0f : q[j];
-        if (w != 0.0f) t += w * ((base - pick[j] * c) + log_S);
-      }
-    t = warp_sum(t);
-    if (lane == 0) {
-      if (lse_out) lse_out[row] = (base + log_S) * kLn2;
-      loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : fmaf(t, kLn2, l);
-    }
+    for (int w = 0; w < (k + 31) / 32; ++w) t += red[2][w];
+    if (lse_out) lse_out[row] = (base + log_S) * kLn2;
+    loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : fmaf(t, kLn2, l);
   }
   if (!e) return;
 
@@ -327,22 +336,17 @@ __global__ void __launch_bounds__(kFinishThreads)
   for (int i = threadIdx.x + blockIdx.y * kFinishThreads; i < d / 8; i += kFinishThreads * gridDim.y) xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
   if (!has) return;
   __syncthreads();
-  for (int j = threadIdx.x; j < k; j += kFinishThreads) {
-    int64_t v = y0;
-    float w = 1.0f;
-    if (tg.k != 0) {
-      // entries of one column are neighbours: the first carries their weights
-      v = column[j];
-      if (v == kAbsent || (j > 0 && column[j - 1] == v)) continue;
-      w = 0.0f;
-      for (int o = j; o < k && column[o] == v; ++o) w += q[o];
-    }
-    if (v < static_cast<int64_t>(u0) * 8 || v >= static_cast<int64_t>(u1) * 8) continue;  // another block's
-    const float ev = exp2f(pick[j] * c - base);
-    // xent: minus the sum of the others, which is what p - 1 leaves of a sure target
-    const float dz = tg.k == 0 ? f * ((ev - S) / S) : f * (Q * (ev / S) - w);
-    er[v] = __bfloat16_as_ushort(__float2bfloat16(dz));
-  }
+  // this thread's entry, if its column lies in this block's slice; entries of
+  // one column are neighbours, and the first carries their weights
+  if (at < static_cast<int64_t>(u0) * 8 || at >= static_cast<int64_t>(u1) * 8 || (tg.k != 0 && before == at)) return;
+  float w = weight;
+  if (tg.k != 0)
+    for (int j = threadIdx.x + 1; j < k && rows.column[static_cast<int64_t>(row) * k + j] == at; ++j)
+      w += rows.q[static_cast<int64_t>(row) * k + j];
+  const float ev = exp2f(y - base);
+  // xent: minus the sum of the others, which is what p - 1 leaves of a sure target
+  const float dz = tg.k == 0 ? f * ((ev - S) / S) : f * (Q * (ev / S) - w);
+  er[at] = __bfloat16_as_ushort(__float2bfloat16(dz));
 }
 
 // dX from the fp32 sums of its ranges of the vocabulary, in order; a thread
@@ -499,7 +503,7 @@ HeadLayout choose_layout(const dgl_head_desc& h, int k, int64_t bytes) {
 dgl_status check_extents(const dgl_head_desc* h, int32_t k) {
   if (!h || k < 0 || k > kMaxK) return DGL_ERR_ARG;
   if (h->T < 0 || h->V <= 0 || h->d <= 0) return DGL_ERR_ARG;
-  if (h->T > INT32_MAX || h->V > INT32_MAX - 64 || h->d > INT32_MAX) return DGL_ERR_SHAPE;
+  if (h->T > INT32_MAX || h->V > INT32_MAX - 512 || h->d > INT32_MAX) return DGL_ERR_SHAPE;
   if (h->d % 8 != 0) return DGL_ERR_ALIGN;
   if (h->d * 4 > INT32_MAX) return DGL_ERR_SHAPE;
   if (h->dw_dtype != DGL_OUT_BF16 && h->dw_dtype != DGL_OUT_F32) return DGL_ERR_ARG;

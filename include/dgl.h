@@ -422,7 +422,7 @@ dgl_status dgl_head_workspace(const dgl_head_desc* head, int32_t k, int64_t* min
  * and nothing else.  Errors: DGL_ERR_ARG (null pointers, negative extents,
  * V or d of 0, a scale that is not finite, accumulate without an fp32 dW, a
  * workspace below the minimum), DGL_ERR_ALIGN, DGL_ERR_SHAPE (extents past
- * 2^31 - 1), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.
+ * 2^31 - 1, V past 2^31 - 513), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.
  */
 dgl_status dgl_linear_xent(const dgl_head_desc* head, const int64_t* target, int64_t ignore_index, void* stream);
 
