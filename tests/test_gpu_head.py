@@ -238,6 +238,27 @@ def test_xent_sure_rows():
     _check(X, W, 1.0, _wanted_xent(T, V, target), grad, got)
 
 
+@pytest.mark.parametrize("T,V,d", [(2, 46, 128), (1, 1306, 440), (94, 3000, 1000), (207, 2600, 376)])
+def test_xent_probabilities_down_to_nothing(T, V, d):
+    """Logits spread over hundreds: an entry below 2^-40 of the largest of its 128
+    columns may count as zero, so dz is also off by up to 2^-40 |g| an entry."""
+    X, W, target, grad = _inputs(T, V, d, w_std=0.5)
+    loss, lse, dX, dW = dgl.linear_cross_entropy(X, W, target, grad, logit_scale=3.0)
+    _status()
+    _check(X, W, 3.0, _wanted_xent(T, V, target), None, (loss, lse))
+    x, w = X.double(), W.double()
+    z = 3.0 * (x @ w.T)
+    ez = ((d / 16 + 4) * 4 * 2.0**-24) * 3.0 * (x.abs() @ w.abs().T).amax(1)
+    p = torch.softmax(z, 1)
+    g = grad.double()[:, None]
+    dz = g * (p - torch.zeros_like(p).scatter_(1, target[:, None], 1.0))
+    e_dz = dz.abs() * (3 * 2.0**-9 + 2.0**-13) + g.abs() * p * (2 * ez[:, None] + 2.0**-17) + g.abs() * 2.0**-40
+    # (the target's entry carries the rounding of its own sum of the others)
+    e_dz.scatter_add_(1, target[:, None], g.abs() * 2.0**-20)
+    for have, ref, err in ((dX, dz @ w, e_dz @ w.abs()), (dW, dz.T @ x, e_dz.T @ x.abs())):
+        assert ((have.double() - 3.0 * ref).abs() <= 3.0 * err + 2.0**-8 * (3.0 * ref).abs() + 1e-30).all()
+
+
 def test_strides_and_untouched_padding():
     T, V, d = 150, 999, 72
     X, W, target, grad = _inputs(T, V, d)
