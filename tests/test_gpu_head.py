@@ -373,6 +373,19 @@ def test_other_stream_and_graph():
     assert all(torch.equal(x, y) for x, y in zip(ref, cap))
 
 
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing but their inputs."""
+    T, V, d = 900, 9001, 256
+    X, W, target, grad = _inputs(T, V, d)
+    ref = dgl.linear_cross_entropy(X, W, target, grad)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [dgl.linear_cross_entropy(X, W, target, grad, stream=s) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(x, y) for x, y in zip(ref, g))
+
+
 def _teacher(T, V, k, seed=1, absent=0.2):
     g = _gen(seed)
     indices = torch.stack([torch.randperm(V, device=DEV, generator=g)[:k] for _ in range(T)]) if k <= V else \
