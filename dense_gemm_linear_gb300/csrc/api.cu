@@ -558,6 +558,7 @@ dgl_status run_impl(Problem pr, const dgl_plan_info* forced, cudaStream_t stream
   // adding to C is done by the TMA stores: fp32 rows of whole 16-byte units
   if (pr.c_add && (!f32 || !c_tma || pr.n % 4 != 0)) return DGL_ERR_UNSUPPORTED;
   std::memset(&tc, 0, sizeof(tc));
+  if ((pr.k_splits > 1 || pr.c_add || pr.tight_a) && !pr.out_scale) return DGL_ERR_UNSUPPORTED;
   if (pr.k_splits > 1 && (!f32 || !c_tma || pr.c_add || linear || plan.tile_m == 64)) return DGL_ERR_UNSUPPORTED;
   const int64_t slab_rows = (pr.m + plan.tile_m - 1) / plan.tile_m * plan.tile_m;
   const int64_t c_rows = pr.k_splits > 1 ? pr.k_splits * slab_rows : pr.m;

@@ -65,19 +65,19 @@ struct TcParams {
   int tiles_m, tiles_n, num_tiles, num_kb;
   int group_m;          // tile raster: group_m row-tiles share each column sweep
   int c_tma;            // 1: C is written by TMA tensor stores (16-byte aligned pitch and base)
-  // k_splits > 1: each tile's k-stages dealt to k_splits segments (segment s
+  // HEAD = 3, k_splits > 1: each tile's k-stages dealt to k_splits segments (segment s
   // takes s, s + k_splits, ...: segments in step read neighbouring pieces of the
   // same rows), whose fp32 sums go each to a C of its own, slab_rows rows
   // further on; the caller adds them.  No stream-K or half tiles then.
   int k_splits;
   int slab_rows;
-  // Rows of A's K-major box when they are fewer than the tile's (0: all): rows
+  // HEAD: rows of A's K-major box when they are fewer than the tile's (0: all): rows
   // past the box hold whatever the ring held, and only feed rows of C past m.
   // A box that reached past m would spend the copy engine's time on its zeros.
   int a_box_rows;
   int b_once;           // HEAD, 1: B's lines leave L2 first
   int c_keep;           // HEAD, 1: C's lines stay in L2 longest
-  int c_add;            // 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
+  int c_add;            // HEAD = 3, 1: the TMA stores add to C (fp32 C with c_tma set) instead of replacing it
   int* status;          // device status word
   // Schedule.  `workers` CTAs (or CTA pairs) run at once.  Tiles below
   // dp_tiles run whole, worker w taking w, w + workers, ...  The remaining

@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kFinishThreads)
 // a row.  Bound by latency and L2: nine ranges of 1024 x 512 (19 MB) in 4.4 us.
 __global__ void __launch_bounds__(256)
     head_join_kernel(const float* __restrict__ part, int64_t slab, int splits, __nv_bfloat16* __restrict__ out,
-                     int64_t ldo, int rows, int cols, const float* __restrict__ scale) {
+                     int64_t ldo, int rows, int cols) {
   griddep_wait();
   griddep_launch_dependents();  // dW loads its operands beside this (PDL_BATCH_NEXT)
   const int64_t i = blockIdx.x * static_cast<int64_t>(256) + threadIdx.x;
@@ -372,8 +372,7 @@ __global__ void __launch_bounds__(256)
     s.z += v.z;
     s.w += v.w;
   }
-  const float m = *scale;
-  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x * m, s.y * m), __floats2bfloat162_rn(s.z * m, s.w * m)};
+  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(s.x, s.y), __floats2bfloat162_rn(s.z, s.w)};
   const int64_t r = i / (cols / 4), c = i % (cols / 4) * 4;
   *reinterpret_cast<uint2*>(out + r * ldo + c) = *reinterpret_cast<const uint2*>(o);
 }
@@ -720,7 +719,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       px.b_k = h.V;
       px.k_splits = splits;
       px.tight_a = 1;
-      px.out_scale = splits > 1 ? nullptr : out_scale;  // else by the adding kernel
+      px.out_scale = out_scale;
       // dW needs nothing of dX: it loads its operands while dX's last tiles, or
       // the kernel that adds its ranges, run
       if (h.dW && splits == 1) px.pdl_mode = PDL_BATCH_HEAD;
@@ -728,7 +727,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
       const int64_t slab = round_up(n, plan.tile_m) * h.d;  // elements of a range's sums
       const int64_t quads = static_cast<int64_t>(n) * (h.d / 4);
       if (splits > 1 && launch_dependent(head_join_kernel, static_cast<unsigned>((quads + 255) / 256), 256, stream,
-                                         scratch.ws, slab, splits, dx, h.lddx, n, d, out_scale) != cudaSuccess)
+                                         scratch.ws, slab, splits, dx, h.lddx, n, d) != cudaSuccess)
         return DGL_ERR_CUDA;
     }
     if (h.dW) {

@@ -57,6 +57,7 @@ struct Problem {
   // bf16 operands, a TMA-stored C on 128- or 256-wide tiles: factor of every
   // element (device scalar); else null
   const float* out_scale = nullptr;
+  // (the next three with out_scale only)
   // 1: A's box holds only the rows that exist when those are fewer than the tile's
   int tight_a = 0;
   // > 1: the sum over K in this many ranges, each with an fp32 C of its own:

@@ -70,11 +70,14 @@ struct TcConfig {
   static constexpr bool EPI = EPI_;
   // HEAD: kernels of a linear head's losses.  1, 2: the logits' epilogue
   // (HeadEpi) takes the place of the others', 1 statistics only, 2 the
-  // exponentials are stored too; 3: a plain GEMM whose elements are scaled by
+  // exponentials are stored too; 3: a GEMM whose elements are scaled by
   // out_scale (1024 x 50257 x 512's dW: 46 us, 49 us with the linear layer's
-  // epilogue, whose activations it does not need).
+  // epilogue, whose activations it does not need) and that knows k_splits,
+  // c_add and a_box_rows, which every other variant ignores (read there at run
+  // time they cost the ragged sweep 2.5%).
   static constexpr int HEAD = HEAD_;
   static constexpr bool LOGITS = HEAD_ == 1 || HEAD_ == 2;
+  static constexpr bool SCALED = HEAD_ == 3;
   // Rows of C per CTA: 128, or 64 for the small rungs of the ladder (one CTA,
   // an M = 64 MMA).  An M = 64 accumulator puts row 16 q + r (r < 16) in
   // tensor-memory lane 32 q + r, so each epilogue warp of lane quarter q holds
@@ -263,8 +266,7 @@ struct StageIter {
   int kb = 0, kb1 = 0, mb = 0, nb = 0;
   int tiles_m, tiles_n, group_m;
   __device__ StageIter(int worker, const TcParams& prm)
-      : it(worker, prm.workers, prm.num_kb, prm.dp_tiles, prm.sk_units, prm.half_tiles, prm.sk_workers,
-           prm.k_splits),
+      : it(worker, prm.workers, prm.num_kb, prm.dp_tiles, prm.sk_units, prm.half_tiles, prm.sk_workers),
         tiles_m(prm.tiles_m),
         tiles_n(prm.tiles_n), group_m(prm.group_m) {}
   __device__ bool next(int& mb_out, int& nb_out, int& kb_out) {
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // loads read after the wait below is current whatever the previous kernel
     // wrote.
     SegmentIter it0(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
-                   p.k_splits);
+                   Cfg::SCALED ? p.k_splits : 0);
     Segment s0;
     if (it0.next(s0) && !s0.half) {
       int mb, nb;
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       uint32_t stage = 0, phase = 0;
       int64_t issued = 0;
       SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
-                   p.k_splits);
+                   Cfg::SCALED ? p.k_splits : 0);
       Segment sg;
       while (!fail && it.next(sg)) {
         int mb, nb;
@@ -689,15 +691,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int b_rows = sg.half ? Cfg::B_ROWS / 2 : Cfg::B_ROWS;
         // a stage's transaction bytes: what the copies read from global
         // memory (packed 4-bit B lands in twice its size of shared memory)
+        const uint32_t a_bytes = Cfg::HEAD != 0 && p.a_box_rows ? static_cast<uint32_t>(p.a_box_rows) * Cfg::ROW_BYTES
+                                                                : static_cast<uint32_t>(Cfg::A_STAGE_BYTES);
         const uint32_t stage_bytes =
-            (p.a_box_rows ? static_cast<uint32_t>(p.a_box_rows) * Cfg::ROW_BYTES : Cfg::A_STAGE_BYTES) + ((sg.half ? Cfg::B_STAGE_BYTES / 2 : Cfg::B_STAGE_BYTES) >> p.b_tx_shift);
+            a_bytes + ((sg.half ? Cfg::B_STAGE_BYTES / 2 : Cfg::B_STAGE_BYTES) >> p.b_tx_shift);
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
           const bool ok = mbar_wait(&empty[stage], phase ^ 1);
           if (!ok) {
             fail = STATUS_TIMEOUT_PRODUCER;
             break;
           }
-          const int k0 = (p.k_splits > 1 ? sg.split + kb * p.k_splits : kb) * Cfg::BK;
+          const int k0 = (Cfg::SCALED && p.k_splits > 1 ? sg.split + kb * p.k_splits : kb) * Cfg::BK;
           if constexpr (CG == 2) {
             // Both CTAs' loads complete on the leader's barrier; the leader
             // alone announces the pair's bytes.  A peer's bytes may land
@@ -753,7 +757,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued_any = false;
       SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
-                   p.k_splits);
+                   Cfg::SCALED ? p.k_splits : 0);
       Segment sg;
       while (!fail && it.next(sg)) {
         const bool ok = mbar_wait(&tempty[acc], acc_phase ^ 1);
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // ------------------------------------------------------------ epilogue
     // C, the split schedule's workspace and its flags are written here only
     if (p.pdl_mode == PDL_BATCH_NEXT) griddep_wait();
-    const float out_scale = Cfg::HEAD == 3 ? *p.out_scale : 1.0f;
+    const float out_scale = Cfg::SCALED ? *p.out_scale : 1.0f;
     const int e = warp - 2;                 // 0..7
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31 are reachable from this warp
     const int half = e >> 2;                // this warp takes chunks [c_first, c_first + nc)
@@ -856,7 +860,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint32_t stg_addr = smem_u32(stg);
     uint32_t acc = 0, acc_phase = 0, fx_phase = 0, head_buf = 0;
     SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
-                   p.k_splits);
+                   Cfg::SCALED ? p.k_splits : 0);
     Segment sg;
     while (it.next(sg)) {
       int mb, nb;
@@ -940,7 +944,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
-      if (Cfg::STREAM_K && sg.kb1 < p.num_kb && p.k_splits <= 1) {
+      if (Cfg::STREAM_K && sg.kb1 < p.num_kb && !(Cfg::SCALED && p.k_splits > 1)) {
         // Finisher: the tile's other k-stages belong to workers cluster_id + 1
         // .. w_last (an empty range holds none).  This is the worker's last
         // segment, so every MMA has finished and the operand ring is free:
@@ -1083,10 +1087,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             __syncwarp();
             if (lane == 0) {
               if (row0 < p.m && col0 < p.n) {
-                if (Cfg::OUT_F32 && p.c_add)
+                if (Cfg::SCALED && Cfg::OUT_F32 && p.c_add)
                   tma_reduce_add_2d(&tmC, stg_u, col0, row0);
                 else
-                  tma_store_2d(&tmC, stg_u, col0, row0 + sg.split * p.slab_rows);
+                  tma_store_2d(&tmC, stg_u, col0, Cfg::SCALED ? row0 + sg.split * p.slab_rows : row0);
               }
               bulk_commit();  // an empty group too: the waits above count groups
             }
@@ -1152,7 +1156,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               for (int j = 0; j < 32; ++j)
                 v[j] = __float_as_uint((__uint_as_float(v[j]) * row_scale) * __shfl_sync(0xffffffffu, col_scale, j));
             }
-            if constexpr (Cfg::HEAD == 3) {
+            if constexpr (Cfg::SCALED) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * out_scale);
             }
@@ -1237,7 +1241,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                            __shfl_sync(0xffffffffu, col_scale, j));
             }
           }
-          if constexpr (Cfg::HEAD == 3) {
+          if constexpr (Cfg::SCALED) {
 #pragma unroll
             for (int uu = 0; uu < G; ++uu)
 #pragma unroll
@@ -1336,8 +1340,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (p.pdl_mode == PDL_BATCH_NEXT) griddep_wait();
       const int q = warp & 3;
       uint32_t acc = 0, acc_phase = 0;
-      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers,
-                     p.k_splits);
+      SegmentIter it(cluster_id, p.workers, p.num_kb, p.dp_tiles, p.sk_units, p.half_tiles, p.sk_workers);
       Segment sg;
       HeadPicks ahead;
       auto look = [&](int& row, int& nb) {  // the next tile's picks; row -1 after the last
