@@ -604,3 +604,55 @@ def test_refusals_of_the_binding():
         dgl.linear_distill(X, W, torch.zeros(10, 129, dtype=torch.int64, device=DEV), torch.zeros(10, 129, device=DEV))
     with pytest.raises(dgl.DglError):
         dgl.linear_distill(X, W, target[:, None].contiguous(), torch.zeros(10, 1, device=DEV), temperature=0.0)
+
+
+def test_c_call_with_padded_rows_and_no_lse():
+    """The C entry with a row pitch for every matrix, lse NULL and an fp32 dW: what lies between the rows stays."""
+    T, V, d = 301, 777, 72
+    X, W, target, grad = _inputs(T, V, d)
+    want = dgl.linear_cross_entropy(X, W, target, grad, dw_dtype=dgl.OUT_F32)
+
+    def padded(t, pad):
+        p = torch.full((t.shape[0] + 1, t.shape[1] + pad), 5.0, device=DEV, dtype=t.dtype)
+        p[:-1, :t.shape[1]] = t
+        return p
+
+    Xp, Wp = padded(X, 16), padded(W, 8)
+    dXp, dWp = padded(torch.zeros_like(X), 24), padded(torch.zeros(V, d, device=DEV), 40)
+    loss = torch.full((T + 1,), 5.0, device=DEV)
+    h = dgl.HeadDesc(T=T, V=V, d=d, X=Xp.data_ptr(), ldx=d + 16, W=Wp.data_ptr(), ldw=d + 8, loss=loss.data_ptr(),
+                     grad=grad.data_ptr(), dX=dXp.data_ptr(), lddx=d + 24, dW=dWp.data_ptr(), lddw=d + 40,
+                     logit_scale=1.0, dw_dtype=dgl.OUT_F32)
+    low, best = dgl.dgl_head_workspace(h)
+    for size in (low, best):
+        ws = torch.full((size + 256,), 255, dtype=torch.uint8, device=DEV)
+        h.ws, h.ws_bytes = ws.data_ptr(), size
+        assert dgl.dgl_linear_xent(h, target.data_ptr(), IGNORE, torch.cuda.current_stream().cuda_stream) == dgl.DGL_OK
+        _status()
+        assert (ws[size:] == 255).all()
+        assert loss[T] == 5.0
+        if size == best:  # the same chunks as the call above (chunks of 128 rows take other tiles)
+            assert torch.equal(loss[:T], want[0]) and torch.equal(dXp[:T, :d], want[2])
+            assert torch.equal(dWp[:V, :d], want[3])
+        _check(X, W, 1.0, _wanted_xent(T, V, target), grad, (loss[:T], want[1], dXp[:T, :d], dWp[:V, :d]))
+        for p, t in ((dXp, X), (dWp, W)):
+            assert (p[-1] == 5.0).all() and (p[:, t.shape[1]:] == 5.0).all()
+
+
+def test_distill_graph_in_chunks():
+    T, V, d, k = 300, 1500, 64, 7
+    X, W, _, grad = _inputs(T, V, d)
+    indices, logits = _teacher(T, V, k)
+    low, _ = _workspace(T, V, d, k, dgl.OUT_BF16)
+    ws = torch.empty(low, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = dgl.linear_distill(X, W, indices, logits, grad, workspace=ws)
+    X2, _, _, _ = _inputs(T, V, d, 8)
+    X.copy_(X2)
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = dgl.linear_distill(X, W, indices, logits, grad, workspace=torch.empty_like(ws))
+    _status()
+    assert all(torch.equal(x, y) for x, y in zip(ref, cap))
+    _check(X, W, 1.0, _wanted_distill(T, V, indices, logits, 1.0), grad, ref)
