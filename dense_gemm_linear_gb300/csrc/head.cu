@@ -434,13 +434,18 @@ constexpr int kSplitSlots = 160;  // partial tiles of 128 x 256: one per CTA
 // Column groups of a row: halves of the logits' tiles.
 int64_t head_groups(int64_t V, int tile_n) { return 2 * ((V + tile_n - 1) / tile_n); }
 
-// The tile of the logits' product.  Up to 128 rows W's reads set the time and
-// narrow tiles spread it evenly; above, the cost model's cheaper of 128 x 256
-// tiles and 256 x 256 CTA pairs (333 rows: 3 row tiles against 2 of twice the
-// height).
+// The tile of the logits' product.  Up to 128 rows W's reads set the time: the
+// narrower tile when it leaves the busiest SM fewer columns (V = 50257 on 152
+// SMs, 3 x 128 against 2 x 256: 1 x 50257 x 2048 39.8 against 42.6 us; V = 32000,
+// 2 x 128 against 1 x 256: 16 x 32000 x 4096 49.0 against 47.1).  Above, the cost
+// model's cheaper of 128 x 256 tiles and 256 x 256 CTA pairs (333 rows: 3 row
+// tiles against 2 of twice the height, 34 against 39 us).
 constexpr int64_t kNarrowRows = 128;
 
-int logits_tile_n(int64_t rows) { return rows > kNarrowRows ? 256 : 128; }
+int logits_tile_n(int64_t rows, int64_t V, int num_sms) {
+  auto most = [&](int64_t cols) { return ((V + cols - 1) / cols + num_sms - 1) / num_sms * cols; };
+  return rows <= kNarrowRows && most(128) < most(256) ? 128 : 256;
+}
 
 int logits_tile_m(int64_t rows, int64_t V, int64_t d, int num_sms) {
   if (rows <= kNarrowRows) return 128;
@@ -466,8 +471,8 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   l.chunk = chunk;
   const bool grad = h.grad != nullptr;
   const int64_t rows = std::min(chunk, round_up(std::max<int64_t>(h.T, 1), kChunkRows));
-  // statistics of the whole chunk, or of a last one on the narrower tiles
-  const int64_t groups = head_groups(h.V, logits_tile_n(rows));
+  // statistics of the chunk, or of one of few rows on the narrower tiles
+  const int64_t groups = head_groups(h.V, 256);
   const int64_t narrow = std::min(rows, kNarrowRows) * head_groups(h.V, 128);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
@@ -631,7 +636,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     const int n = static_cast<int>(std::min(lay.chunk, h.T - t0));
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(h.X) + t0 * h.ldx;
     const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(h.W);
-    const int tile_m = logits_tile_m(n, h.V, h.d, ds->num_sms), tile_n = logits_tile_n(n);
+    const int tile_m = logits_tile_m(n, h.V, h.d, ds->num_sms), tile_n = logits_tile_n(n, h.V, ds->num_sms);
     tg.index = targets.index + t0 * std::max(tg.k, 1);
     if (tg.k > 0) tg.logits = targets.logits + t0 * tg.k;
     if (tg.teacher_lse) tg.teacher_lse = targets.teacher_lse + t0;
@@ -697,7 +702,8 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     p.head.pick = rows.pick;
     if (launch_tc_head(grad, tile_m, tile_n, ta, tb, tc, p, p.workers * cg, stream) != cudaSuccess) return DGL_ERR_CUDA;
 
-    // few rows: enough blocks for every SM to hold several, of at least 2048 columns
+    // few rows: enough blocks for every SM to hold several, of at least 2048
+    // columns (100 x 50257 x 512: 73 -> 66 us in all, 4 x 50257 x 2048: 155 -> 148)
     const int64_t slices = grad ? std::min<int64_t>(int64_t(8) * ds->num_sms / n, h.V / 2048) : 1;
     const dim3 finish(static_cast<unsigned>(n), static_cast<unsigned>(std::max<int64_t>(1, slices)));
     if (launch_dependent(grad ? head_finish_kernel<kFinishThreadsGrad> : head_finish_kernel<kFinishThreadsForward>, finish,
