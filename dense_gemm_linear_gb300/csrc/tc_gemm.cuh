@@ -396,7 +396,7 @@ __device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int 
 // lane, whichever rows they belong to, so that a row with many entries in one
 // tile (frequent tokens have neighbouring numbers) costs no chain of its own:
 // their columns are read at once; each column is then read out of tensor memory
-// for all 32 rows, eight in flight, and the entry's row hands its value over.
+// for all 32 rows, four in flight, and the entry's row hands its value over.
 __device__ __forceinline__ void head_pick(const HeadEpi& h, HeadPicks want, uint32_t t0, int row0, int col0, int lane) {
   constexpr uint32_t ALL = 0xFFFFFFFFu;
   const int count = want.last - want.first;
@@ -418,24 +418,22 @@ __device__ __forceinline__ void head_pick(const HeadEpi& h, HeadPicks want, uint
       if (__shfl_sync(ALL, upto, r + step - 1) <= mine) r += step;
     const int nth = mine - __shfl_sync(ALL, upto - count, r);
     const int64_t slot = static_cast<int64_t>(row0 + r) * h.k + __shfl_sync(ALL, want.first, r) + nth;
-    int col = __shfl_sync(ALL, want.at, r);
+    int col = __shfl_sync(ALL, want.at, r);  // 0, a column like any, where there is no entry
     if (h.start && mine < total) col = h.column[slot] - col0;
     const int n = min(32, total - base);
     uint32_t value = 0;
 #pragma unroll 1
-    for (int i = 0; i < n; i += 8) {
-      uint32_t v[8];
+    for (int i = 0; i < n; i += 4) {
+      uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j < n) tmem_ld_32x32b_x1(t0 + __shfl_sync(ALL, col, i + j), v[j]);
+      for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x1(t0 + __shfl_sync(ALL, col, i + j), v[j]);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + j < n) {
-          asm volatile("" : "+r"(v[j]));  // not used before the wait
-          const uint32_t x = __shfl_sync(ALL, v[j], __shfl_sync(ALL, r, i + j));
-          if (lane == i + j) value = x;
-        }
+      for (int j = 0; j < 4; ++j) {
+        asm volatile("" : "+r"(v[j]));  // not used before the wait
+        const uint32_t x = __shfl_sync(ALL, v[j], r);
+        if (lane == i + j) value = x;
+      }
     }
     if (mine < total) h.pick[slot] = __uint_as_float(value);
   }
