@@ -396,7 +396,7 @@ __device__ __forceinline__ HeadPicks head_picks(const TcParams& p, int row, int 
 // lane, whichever rows they belong to, so that a row with many entries in one
 // tile (frequent tokens have neighbouring numbers) costs no chain of its own:
 // their columns are read at once; each column is then read out of tensor memory
-// for all 32 rows, four in flight, and the entry's row hands its value over.
+// for all 32 rows, eight in flight, and the entry's row hands its value over.
 __device__ __forceinline__ void head_pick(const HeadEpi& h, HeadPicks want, uint32_t t0, int row0, int col0, int lane) {
   constexpr uint32_t ALL = 0xFFFFFFFFu;
   const int count = want.last - want.first;
@@ -423,13 +423,13 @@ __device__ __forceinline__ void head_pick(const HeadEpi& h, HeadPicks want, uint
     const int n = min(32, total - base);
     uint32_t value = 0;
 #pragma unroll 1
-    for (int i = 0; i < n; i += 4) {
-      uint32_t v[4];
+    for (int i = 0; i < n; i += 8) {
+      uint32_t v[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x1(t0 + __shfl_sync(ALL, col, i + j), v[j]);
+      for (int j = 0; j < 8; ++j) tmem_ld_32x32b_x1(t0 + __shfl_sync(ALL, col, i + j), v[j]);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         asm volatile("" : "+r"(v[j]));  // not used before the wait
         const uint32_t x = __shfl_sync(ALL, v[j], r);
         if (lane == i + j) value = x;
