@@ -373,12 +373,12 @@ dgl_status dgl_linear(int32_t dtype, const void* A, const void* B, const float* 
  *
  * Accuracy.  Products and sums are fp32, statistics and losses fp32.  The
  * exponentials of a gradient wait for their sum in fp16, relative to the
- * largest of their row's 128 columns (64 of a call on at most 128 tokens): 11
- * bits down to 2^-29 of it, and nothing below 2^-40.  dz is then rounded to
- * bf16 (up to 2^-8 an entry; a target's entry is minus the sum of the others,
- * not p - 1) as the operand of the two products, without the significand that
- * the rows' common grad has, which the products' results are multiplied by in
- * fp32.  dX and a bf16 dW are rounded once more.
+ * largest of their row's 128 columns (or 64, where at most 128 tokens are taken
+ * at a time): 11 bits down to 2^-29 of it, and nothing below 2^-40.  dz is then
+ * rounded to bf16 (up to 2^-8 an entry; a target's entry is minus the sum of
+ * the others, not p - 1) as the operand of the two products, without the
+ * significand that the rows' common grad has, which the products' results are
+ * multiplied by in fp32.  dX and a bf16 dW are rounded once more.
  *
  * Rows without a target.  dgl_linear_xent: target_t == ignore_index gives loss
  * 0 and no gradient, whatever x_t holds (NaN and infinities included: the row
