@@ -29,7 +29,11 @@ def _rows(t, name, dtype, shape):
     pitch, step = t.stride()
     if step != 1 and shape[1] > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return pitch if shape[0] > 1 else shape[1]
+    if shape[0] <= 1:
+        return shape[1]
+    if pitch < shape[1]:  # a row repeated by expand() has pitch 0, which the C call reads as packed rows
+        raise ValueError(f"the rows of {name} must not overlap")
+    return pitch
 
 
 def _packed(t, name, dtype, shape):

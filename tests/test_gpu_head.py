@@ -606,6 +606,26 @@ def test_refusals_of_the_binding():
         dgl.linear_distill(X, W, target[:, None].contiguous(), torch.zeros(10, 1, device=DEV), temperature=0.0)
 
 
+def test_rows_that_overlap_are_refused():
+    # one row seen as many has pitch 0, which the C call takes for packed rows: it would read past the buffer
+    X, W, target, grad = _inputs(10, 100, 64)
+    one = X[:1].expand(10, 64)
+    with pytest.raises(ValueError):
+        dgl.linear_cross_entropy(one, W, target)
+    with pytest.raises(ValueError):
+        dgl.linear_cross_entropy(X, W[:1].expand(100, 64), target)
+    with pytest.raises(ValueError):
+        dgl.linear_cross_entropy(X, W, target, grad, dW=torch.zeros(1, 64, device=DEV).expand(100, 64))
+    with pytest.raises(ValueError):
+        dgl.linear_distill(one, W, target[:, None].contiguous(), torch.zeros(10, 1, device=DEV))
+    with pytest.raises(ValueError):
+        dgl.linear_cross_entropy(X.flatten().as_strided((10, 64), (8, 1)), W, target)
+    # one token has no pitch
+    loss, lse = dgl.linear_cross_entropy(X[:1].expand(1, 64), W, target[:1])
+    z = X[:1].double() @ W.double().T
+    assert torch.allclose(lse.double(), torch.logsumexp(z, 1), rtol=0, atol=1e-4)
+
+
 def test_c_call_with_padded_rows_and_no_lse():
     """The C entry with a row pitch for every matrix, lse NULL and an fp32 dW: what lies between the rows stays."""
     T, V, d = 301, 777, 72
