@@ -62,6 +62,8 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
     ldx = _rows(X, "X", _BF16, (T, d))
     ldw = _rows(W, "W", _BF16, (V, d))
     device = X.device
+    if dw_dtype not in (OUT_BF16, OUT_F32):
+        raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
     p_grad = p_dx = p_dw = lddw = 0
     dw_type = OUT_BF16
     dX = None
@@ -76,7 +78,7 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
             if dW is None:
                 if accumulate:
                     raise ValueError("accumulate adds to the fp32 dW that is passed in")
-                dw_type = OUT_F32 if dw_dtype == OUT_F32 else OUT_BF16
+                dw_type = dw_dtype
                 dW = torch.empty((V, d), dtype=_F32 if dw_type == OUT_F32 else _BF16, device=device)
                 lddw = d
             else:

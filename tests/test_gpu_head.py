@@ -626,6 +626,14 @@ def test_rows_that_overlap_are_refused():
     assert torch.allclose(lse.double(), torch.logsumexp(z, 1), rtol=0, atol=1e-4)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, 7])
+def test_dw_dtype_is_one_of_the_two(dtype):
+    X, W, target, grad = _inputs(10, 100, 64)
+    with pytest.raises(ValueError):
+        dgl.linear_cross_entropy(X, W, target, grad, dw_dtype=dtype)
+    assert dgl.linear_cross_entropy(X, W, target, grad, dw_dtype=dgl.OUT_F32)[3].dtype == torch.float32
+
+
 def test_c_call_with_padded_rows_and_no_lse():
     """The C entry with a row pitch for every matrix, lse NULL and an fp32 dW: what lies between the rows stays."""
     T, V, d = 301, 777, 72
