@@ -54,6 +54,9 @@ struct HeadEpi {
 // fp16 holds the exponentials of a group with its 11 bits from the largest,
 // 2^15, down to 2^-14, 2^-29 of the largest; what is below 2^-40 of it is zero.
 constexpr float kHeadShift = 15.0f;
+// From this |Y| on an exponential's argument is taken from the accumulators'
+// differences; below it kHeadShift - Y is rounded by at most 2^-17.
+constexpr float kHeadFar = 256.0f;
 
 // Persistent tcgen05 tile kernel: problem and schedule.
 struct TcParams {

@@ -497,7 +497,13 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
   }
   const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
   const float top = m == -INFINITY ? m : m * c;
-  const float less = top == -INFINITY ? 0.0f : kHeadShift - top;
+  // The exponent is y - Y + kHeadShift in one multiply-add, which rounds
+  // kHeadShift - Y.  Where Y is so large that this would show, the largest
+  // accumulator is subtracted first, which is exact near it.
+  const bool far = fabsf(top) > kHeadFar && m != -INFINITY;
+  const bool any_far = __any_sync(0xFFFFFFFFu, far);
+  const uint32_t minus = far ? __float_as_uint(-m) : 0u;
+  const float less = top == -INFINITY ? 0.0f : far ? kHeadShift : kHeadShift - top;
   const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c));
   const uint64_t less2 = pack2(__float_as_uint(less), __float_as_uint(less));
 
@@ -507,6 +513,13 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
     uint32_t r[2][32];
     load(r, u);
     if (u + 2 >= NC) hand_back();
+    if (any_far) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          r[i][j] = __float_as_uint(__uint_as_float(r[i][j]) + __uint_as_float(minus));
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll

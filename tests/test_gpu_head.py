@@ -227,6 +227,44 @@ def test_xent_wide_logits(spread, V):
     _check(X, W, 1.0, _wanted_xent(T, V, target), grad, got)
 
 
+@pytest.mark.parametrize("T,V", [(90, 700), (300, 2500)])
+@pytest.mark.parametrize("size", [2.0**10, 2.0**17, 2.0**24, 2.0**30])
+def test_xent_huge_logits(size, T, V):
+    """Logits so large that their own last bit is worth more than a factor of
+    two: each is one exact product, and what is next to the largest is either
+    equal to it or at least 2^-9 of it lower, so the answer is still sharp."""
+    d = 64
+    _, W, target, grad = _inputs(T, V, d)
+    W = torch.where(W == 0, 0.25, W.float().sign() * (0.25 + W.float().abs())).bfloat16()
+    rows = torch.arange(T, device=DEV)
+    X = torch.zeros(T, d, device=DEV)
+    X[rows, rows % d] = torch.where(rows % 3 == 0, -size, size)
+    X = X.bfloat16()
+    x, w = X.double(), W.double()
+    z = x @ w.T
+    high = z.amax(1, keepdim=True)
+    target = torch.where(rows % 2 == 0, z.argmax(1), target)
+    loss, lse, dX, dW = dgl.linear_cross_entropy(X, W, target, grad)
+    _status()
+    p = torch.softmax(z, 1)
+    rest = torch.where(z < high, p, 0.0)
+    q = torch.zeros_like(p).scatter_(1, target[:, None], 1.0)
+    # y = z log2(e) is rounded once, the difference of two of them carries both
+    ez = 2.0**-23 * z.abs().amax(1, keepdim=True)
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() <= 2.0**-20 * (1 + want.abs())).all()
+    at = z.gather(1, target[:, None])
+    short = (high - at + (p.sum(1, keepdim=True) / p.amax(1, keepdim=True)).log())[:, 0]
+    e_loss = 2.0**-20 * (1 + short) + torch.where(at < high, 2 * ez, 0.0)[:, 0] + (2 * ez * rest.sum(1, keepdim=True))[:, 0]
+    assert ((loss.double() - short).abs() <= e_loss).all()
+    g = grad.double()[:, None]
+    dz = g * (p - q)
+    e_dz = dz.abs() * (3 * 2.0**-9 + 2.0**-13) + g.abs() * (p * 2.0**-17 + q * 2.0**-20 + 2.0**-40) \
+        + g.abs() * 2 * ez * (rest + p * rest.sum(1, keepdim=True))
+    for have, ref, err in ((dX, dz @ w, e_dz @ w.abs()), (dW, dz.T @ x, e_dz.T @ x.abs())):
+        assert ((have.double() - ref).abs() <= err + 2.0**-8 * ref.abs() + 1e-30).all()
+
+
 def test_xent_sure_rows():
     """Targets with probability close to one: the gradient is the small rest."""
     T, V, d = 64, 400, 128
