@@ -193,12 +193,12 @@ __device__ __forceinline__ float common_significand(float g) {
   return normal ? __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u) : 1.0f;
 }
 
-// Threads of a block: a gradient moves whole rows of e (1024 x 50257 x 512 in
-// all: 128 / 256 / 512 threads 191 / 184 / 184 us), a forward pass only reads
-// statistics (2047 x 50257 x 1024 in all: 32 / 64 / 128 / 256 threads 136 / 139 /
-// 136 / 143 us; 1 x 50257 x 2048: 41.8 / 40.5 / 40.0 / 40.3 us).
-constexpr int kFinishThreadsGrad = 256;
-constexpr int kFinishThreadsForward = 128;
+// A gradient's blocks of short rows (or slices) are of 128 threads, so that all
+// that an SM has room for hide each other's first and last steps, long rows'
+// of 256 (128 / 256 threads, us in all: 1000 x 4095 x 512 38 / 43, 6000 x 11007 x
+// 256 179 / 200, 4000 x 20000 x 256 224 / 228, 2000 x 32000 x 256 168.9 / 169.4,
+// 1024 x 50257 x 512 180 / 177, 1500 x 50257 x 256 210 / 201).
+constexpr int64_t kFinishShort = 32768;  // columns
 
 // One block per row, and with few rows several, each for a slice of the
 // vocabulary (gridDim.y; all of them reduce the row's statistics): statistics
@@ -206,8 +206,8 @@ constexpr int kFinishThreadsForward = 128;
 // place (zero up to a multiple of 8 columns), and x for dW = dz^T x, zero where
 // the row has no gradient (0 x NaN would reach dW).  A gradient is bound by
 // reading e and writing dz: 10240 x 50257 in 305 us, 6.8 TB/s.
-template <int kFinishThreads>
-__global__ void __launch_bounds__(kFinishThreads)
+template <bool GRAD, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
                        const float* __restrict__ first_grad, int first_rows, float* __restrict__ out_scale,
                        float* __restrict__ loss, float* __restrict__ lse_out, uint16_t* __restrict__ e, int64_t lde,
@@ -215,18 +215,41 @@ __global__ void __launch_bounds__(kFinishThreads)
                        int* __restrict__ flags, int nflags) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int WARPS = kFinishThreads / 32;
+  constexpr int WARPS = THREADS / 32;
   __shared__ float red[3][WARPS];
   const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool lead = blockIdx.y == 0;
   if (row == 0 && lead)
-    for (int i = threadIdx.x; i < nflags; i += kFinishThreads) flags[i] = 0;
+    for (int i = threadIdx.x; i < nflags; i += THREADS) flags[i] = 0;
   const float2* part = rows.part + static_cast<int64_t>(row) * rows.groups;
-  const float g32 = e && lane < first_rows ? first_grad[lane] * scale : 0.0f;
-  const float g_row = e ? grad[row] * scale : 0.0f;
+  // gradient: this block's slice of e, in units of eight columns.  A thread has U
+  // loads in flight: the first beside the row's statistics, then the next ones
+  // beside the arithmetic and stores of the ones before (1024 x 50257 x 512 in
+  // all: 182 us with U = 4 loads at the loop's head, 176 so; 180 / 183 with U =
+  // 2 / 8)
+  uint16_t* er = e + row * lde;
+  uint4* e8 = reinterpret_cast<uint4*>(er);
+  const int units = (V + 7) / 8, share = (units + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+  const int u0 = min(units, share * static_cast<int>(blockIdx.y)), u1 = min(units, u0 + share);
+  constexpr int U = 4;
+  uint4 v[U];
+  float v_top[U];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i < u1) {
+        v[u] = e8[i];
+        v_top[u] = part[8 * i >> rows.group_shift].x;
+      }
+    }
+  };
+  if (GRAD) fetch(u0 + threadIdx.x);
+  const float g32 = GRAD && lane < first_rows ? first_grad[lane] * scale : 0.0f;
+  const float g_row = GRAD ? grad[row] * scale : 0.0f;
   // the row's targets, entry j (of k, at most kMaxK) with thread j: its column
   // (-1: none), weight and y
-  static_assert(kFinishThreads >= kMaxK, "an entry a thread");
+  static_assert(THREADS >= kMaxK, "an entry a thread");
   const int k = tg.k == 0 ? 1 : tg.k;
   int state;
   float Q = 1.0f, l = 0.0f, weight = 0.0f, y = 0.0f;
@@ -254,7 +277,7 @@ __global__ void __launch_bounds__(kFinishThreads)
   }
   if (at >= 0) y = rows.pick[static_cast<int64_t>(row) * k + threadIdx.x] * c;
   float m = -INFINITY, s = 0.0f;
-  for (int g = threadIdx.x; g < rows.groups; g += kFinishThreads) {
+  for (int g = threadIdx.x; g < rows.groups; g += THREADS) {
     const float2 v = part[g];
     const float top = fmaxf(m, v.x);
     // a group without a maximum sums to zero, or to NaN
@@ -289,54 +312,44 @@ __global__ void __launch_bounds__(kFinishThreads)
     if (lse_out) lse_out[row] = (base + log_S) * kLn2;
     loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : fmaf(t, kLn2, l);
   }
-  if (!e) return;
+  if (!GRAD) return;
 
   const bool has = state == 1;
   const float common = common_significand(g32);
   if (row == 0 && lead && threadIdx.x == 0) *out_scale = common;
   const float f = has ? __fdiv_rn(g_row, common) : 0.0f;
   const float fS = f * (Q / S);
-  uint16_t* er = e + row * lde;
-  uint4* e8 = reinterpret_cast<uint4*>(er);
-  // this block's slice, in units of eight columns
-  const int units = (V + 7) / 8;
-  const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.y / gridDim.y);
-  const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.y + 1) / gridDim.y);
   if (!has) {
-    for (int i = u0 + threadIdx.x; i < u1; i += kFinishThreads) e8[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = u0 + threadIdx.x; i < u1; i += THREADS) e8[i] = make_uint4(0u, 0u, 0u, 0u);
   } else {
-    // four loads in flight a thread
-    constexpr int U = 4;
-    for (int i0 = u0 + threadIdx.x; i0 < u1; i0 += U * kFinishThreads) {
-      uint4 v[U];
-      float top[U];
+    for (int i0 = u0 + threadIdx.x; i0 < u1; i0 += U * THREADS) {
+      uint4 now[U];
+      float now_top[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kFinishThreads;
-        if (i < u1) {
-          v[u] = e8[i];
-          top[u] = part[8 * i >> rows.group_shift].x;
-        }
+        now[u] = v[u];
+        now_top[u] = v_top[u];
       }
+      fetch(i0 + U * THREADS);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * kFinishThreads;
+        const int i = i0 + u * THREADS;
         if (i >= u1) break;
-        const float a = fS * exp2f((top[u] - base) - kHeadShift);
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v[u]);
+        const float a = fS * exp2f((now_top[u] - base) - kHeadShift);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&now[u]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 p2 = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(p2.x * a, p2.y * a);
           w[j] = *reinterpret_cast<const uint32_t*>(&b2);
         }
-        e8[i] = v[u];
+        e8[i] = now[u];
       }
     }
   }
   const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
   uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
-  for (int i = threadIdx.x + blockIdx.y * kFinishThreads; i < d / 8; i += kFinishThreads * gridDim.y)
+  for (int i = threadIdx.x + blockIdx.y * THREADS; i < d / 8; i += THREADS * gridDim.y)
     xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
   if (!has) return;
   __syncthreads();
@@ -706,8 +719,11 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
     // columns (100 x 50257 x 512: 73 -> 66 us in all, 4 x 50257 x 2048: 155 -> 148)
     const int64_t slices = grad ? std::min<int64_t>(int64_t(8) * ds->num_sms / n, h.V / 2048) : 1;
     const dim3 finish(static_cast<unsigned>(n), static_cast<unsigned>(std::max<int64_t>(1, slices)));
-    if (launch_dependent(grad ? head_finish_kernel<kFinishThreadsGrad> : head_finish_kernel<kFinishThreadsForward>, finish,
-                         grad ? kFinishThreadsGrad : kFinishThreadsForward, stream, tg, rows, V, scale, c,
+    const bool small = grad && h.V / finish.y <= kFinishShort;
+    if (launch_dependent(!grad   ? head_finish_kernel<false, 256>
+                         : small ? head_finish_kernel<true, 128>
+                                 : head_finish_kernel<true, 256>,
+                         finish, small ? 128 : 256, stream, tg, rows, V, scale, c,
                          grad ? h.grad + t0 : nullptr, h.grad, static_cast<int>(std::min<int64_t>(h.T, 32)), out_scale,
                          h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
                          xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
