@@ -79,7 +79,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 constexpr int kPrepareWarps = 4;
 
 // Distill, one warp per row: the teacher's distribution over the row's entries
-// in fp32 (maximum first), the entries sorted by column (an entry's place is the
+// in fp32, the entries sorted by column (an entry's place is the
 // number of entries before it, k^2 comparisons by 32 lanes), and the number of
 // them before each tile of columns.  Bound by latency: 4.7 us at k = 1, 7.4 us at
 // k = 64 (1024 rows, V = 50257).
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
       const int64_t c64 = tg.index[static_cast<int64_t>(row) * k + j];
       bad |= c64 >= V;
       if (c64 >= 0 && c64 < V) {
-        const float v = tg.logits[static_cast<int64_t>(row) * k + j] * tg.inv_temp;
+        const float v = tg.logits[static_cast<int64_t>(row) * k + j];
         if (!(v == -INFINITY)) {  // minus infinity: no probability; NaN stays, and reaches the loss
           col[i] = static_cast<int>(c64);
           l[i] = v;
@@ -123,22 +123,35 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   bad = __any_sync(0xffffffffu, bad);
   some = __any_sync(0xffffffffu, some);
   high = warp_max(high);
-  const float base = tg.teacher_lse ? tg.teacher_lse[row] : high;
+  // log q and q.  Without teacher_lse log q is (l - high) / temperature - log
+  // sum: the difference to the row's largest logit is taken first, in which what
+  // the logits have in common goes before anything is rounded, and nothing of
+  // their size is added again (log sum is at most log k).
+  const bool share = tg.teacher_lse != nullptr;
+  const float whole = share ? tg.teacher_lse[row] : 0.0f;
+  float lq[PER], q[PER];
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) sum += col[i] != kAbsent ? expf(l[i] - base) : 0.0f;
-  sum = warp_sum(sum);
-  const float log_total = tg.teacher_lse ? base : base + logf(sum);
-  float Q = 0.0f, qlogq = 0.0f;
-  float q[PER];
-#pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const float lq = l[i] - log_total;
-    q[i] = col[i] != kAbsent ? expf(lq) : 0.0f;
-    Q += q[i];
-    qlogq += q[i] != 0.0f ? q[i] * lq : 0.0f;
+    lq[i] = share ? fmaf(l[i], tg.inv_temp, -whole) : (l[i] - high) * tg.inv_temp;
+    q[i] = col[i] != kAbsent ? expf(lq[i]) : 0.0f;
+    sum += q[i];
   }
-  Q = warp_sum(Q);
+  float Q = sum = warp_sum(sum);
+  if (!share && some) {
+    const float log_sum = logf(sum);
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      lq[i] -= log_sum;
+      q[i] = __fdiv_rn(q[i], sum);
+      total += q[i];
+    }
+    Q = warp_sum(total);
+  }
+  float qlogq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) qlogq += q[i] != 0.0f ? q[i] * lq[i] : 0.0f;
   qlogq = warp_sum(qlogq);
   const int state = bad ? -1 : some ? 1 : 0;
   if (lane == 0) rows.sums[row] = make_float4(Q, qlogq, static_cast<float>(state), 0.0f);
