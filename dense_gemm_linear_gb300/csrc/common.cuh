@@ -33,11 +33,12 @@ enum : int { PDL_SERIAL = 0, PDL_BATCH_HEAD = 1, PDL_BATCH_NEXT = 2 };
 // The tile's accumulators are logits up to the factor `scale`; in units of
 // log 2 they are y = acc c, c = scale log2(e).  A warp holds 32 rows by one
 // column group (half a tile's columns); per row and group it leaves in part
-// the largest y, Y, and the sum of 2^(y - Y + kHeadShift), and with HEAD = 2
-// writes 2^(y - Y + kHeadShift) in fp16 as the tile's output.
+// the group's base B, its largest y but for a rounding, and the sum of
+// e = 2^(y - B + kHeadShift), and with HEAD = 2 writes e in fp16 as the tile's
+// output.
 struct HeadEpi {
   float c;      // scale log2(e); its sign is applied to the accumulators first
-  float2* part;  // [rows][part_ld] (Y, sum) per column group
+  float2* part;  // [rows][part_ld] (B, sum) per column group
   int part_ld;
   // Accumulators to pick out of the tile, [rows][k] into pick: one target per
   // row (start null; others than 0 .. n - 1 are not picked), or the row's k
@@ -54,9 +55,31 @@ struct HeadEpi {
 // fp16 holds the exponentials of a group with its 11 bits from the largest,
 // 2^15, down to 2^-14, 2^-29 of the largest; what is below 2^-40 of it is zero.
 constexpr float kHeadShift = 15.0f;
-// From this |Y| on an exponential's argument is taken from the accumulators'
-// differences; below it kHeadShift - Y is rounded by at most 2^-17.
-constexpr float kHeadFar = 256.0f;
+// The argument y - B + kHeadShift is one multiply-add, acc c + (kHeadShift - B),
+// and B is chosen so that kHeadShift - B is exact: the sum, e and whoever forms
+// a term again (head_argument) mean the same B, and a target's own term cancels
+// out of its row's sum.  Up to |B| = kHeadFar the largest argument is within
+// 0.1 of kHeadShift (half a last bit of y, 2^-5 there, and of kHeadShift - y,
+// 2^-4), and e within fp16's range, 2^16.  Beyond it the largest accumulator is
+// subtracted first, exactly near it, and B is its rounded product.
+constexpr float kHeadFar = 1048576.0f;
+
+__device__ __forceinline__ bool head_far(float base) { return fabsf(base) > kHeadFar; }
+// The base of a near group whose largest y is `top`, and kHeadShift - base,
+// rounded as a first step.  The second is exact: from kHeadShift / 2 down top
+// leaves less at least that large, and its last bit holds the result's; above,
+// less is exact itself.
+__device__ __forceinline__ float head_base(float top, float& less) {
+  less = kHeadShift - top;
+  return kHeadShift - less;
+}
+// The argument of one accumulator's exponential in a group of base B, as the
+// epilogue formed it (past kHeadFar: to the last bit of y).
+__device__ __forceinline__ float head_argument(float acc, float c, float base) {
+  if (!head_far(base)) return fmaf(acc, c, kHeadShift - base);
+  const float y = __fmul_rn(acc, c);
+  return base == -INFINITY ? y : (y - base) + kHeadShift;
+}
 
 // Persistent tcgen05 tile kernel: problem and schedule.
 struct TcParams {

@@ -4,8 +4,8 @@
 // Tokens are taken in chunks.  In units of log 2, with y = s log2(e) x . w:
 //   prepare  (distill; one warp per row) the teacher's weights q, sorted by column
 //   logits   (tile kernel, HEAD) y in fp32, never stored: per row and group of
-//            columns its largest Y and the sum of 2^(y - Y), the y of the
-//            targets, and for a gradient e = 2^(y - Y) in fp16
+//            columns a base B near its largest y and the sum of 2^(y - B), the
+//            targets' accumulators, and for a gradient e = 2^(y - B) in fp16
 //   finish   (one block per row) S = sum e, lse, loss, and for the gradient
 //            dz = (grad s / m) (Q e / S - q) in bf16 in the place of e
 //   dX = m dz W, dW = m dz^T x  (tile kernel)
@@ -41,6 +41,7 @@ constexpr int kMaxK = DGL_DISTILL_MAX_K;
 constexpr int kAbsent = INT_MAX - 1;  // the column of an absent entry; one more does not overflow
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kUnshift = 1.0f / 32768.0f;  // 2^-kHeadShift
 
 // What a row asks of the softmax: xent (k == 0) one target, distill k entries.
 struct HeadTargets {
@@ -61,7 +62,7 @@ struct HeadRows {
   int start_ld;
   int group_shift;   // a group is 2^group_shift columns, half a tile
   float* pick;       // [rows][max(k, 1)] accumulators of the entries
-  float2* part;      // [rows][groups] (largest y, sum of the exponentials)
+  float2* part;      // [rows][groups] (base B, sum of the exponentials relative to it)
   int groups;
 };
 
@@ -261,11 +262,11 @@ __global__ void __launch_bounds__(THREADS)
   const float g32 = GRAD && lane < first_rows ? first_grad[lane] * scale : 0.0f;
   const float g_row = GRAD ? grad[row] * scale : 0.0f;
   // the row's targets, entry j (of k, at most kMaxK) with thread j: its column
-  // (-1: none), weight and y
+  // (-1: none), weight, accumulator and its group's base
   static_assert(THREADS >= kMaxK, "an entry a thread");
   const int k = tg.k == 0 ? 1 : tg.k;
   int state;
-  float Q = 1.0f, l = 0.0f, weight = 0.0f, y = 0.0f;
+  float Q = 1.0f, l = 0.0f, weight = 0.0f, acc = 0.0f, own = 0.0f;
   int64_t at = -1;
   int before = -1;  // the column of entry j - 1
   if (tg.k == 0) {
@@ -288,7 +289,10 @@ __global__ void __launch_bounds__(THREADS)
       if (threadIdx.x > 0) before = rows.column[slot - 1];
     }
   }
-  if (at >= 0) y = rows.pick[static_cast<int64_t>(row) * k + threadIdx.x] * c;
+  if (at >= 0) {
+    acc = rows.pick[static_cast<int64_t>(row) * k + threadIdx.x];
+    own = part[at >> rows.group_shift].x;
+  }
   float m = -INFINITY, s = 0.0f;
   for (int g = threadIdx.x; g < rows.groups; g += THREADS) {
     const float2 v = part[g];
@@ -309,13 +313,26 @@ __global__ void __launch_bounds__(THREADS)
   for (int i = 1; i < WARPS; ++i) base = fmaxf(base, red[0][i]);
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) S += red[0][i] == -INFINITY ? red[1][i] : red[1][i] * exp2f(red[0][i] - base);
-  S *= exp2f(-kHeadShift);  // relative to 2^base
+  S *= kUnshift;  // relative to 2^base
   const float log_S = log2f(S);
 
+  // The entry's term is formed as the epilogue formed it, so that it is the very
+  // number that S holds (but for a factor, 1 in the group of the row's maximum):
+  // S - term is the sum of the others', never below zero, and a sure token's
+  // loss and dz are what they leave.
+  float term = 0.0f, short_of = 0.0f;  // 2^(y - base), and ((term - S) / S, p - 1)
   if (threadIdx.x < ((k + 31) & ~31)) {
-    // sum_k q (lse - z_k) as base - y_k + log2 S: what a likely target's y has
-    // in common with the maximum cancels before anything is rounded
-    const float t = warp_sum(at >= 0 && weight != 0.0f ? weight * ((base - y) + log_S) : 0.0f);
+    float t = 0.0f;
+    if (at >= 0) {
+      const float arg = head_argument(acc, c, own);
+      term = ex2(arg) * (kUnshift * exp2f(own - base));
+      short_of = (term - S) / S;
+      // -log p, as -log(1 + (p - 1)) where p is large, else as log2 S - (y - base)
+      if (weight != 0.0f)
+        t = weight * (short_of > -0.5f ? -log1pf(short_of)
+                                       : (log_S - ((arg - kHeadShift) + (own - base))) * kLn2);
+    }
+    t = warp_sum(t);
     if (lane == 0) red[2][warp] = t;
   }
   __syncthreads();
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(THREADS)
     float t = 0.0f;
     for (int w = 0; w < (k + 31) / 32; ++w) t += red[2][w];
     if (lse_out) lse_out[row] = (base + log_S) * kLn2;
-    loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : fmaf(t, kLn2, l);
+    loss[row] = state < 0 ? NAN : state == 0 ? 0.0f : l + t;
   }
   if (!GRAD) return;
 
@@ -373,9 +390,8 @@ __global__ void __launch_bounds__(THREADS)
   if (tg.k != 0)
     for (int j = threadIdx.x + 1; j < k && rows.column[static_cast<int64_t>(row) * k + j] == at; ++j)
       w += rows.q[static_cast<int64_t>(row) * k + j];
-  const float ev = exp2f(y - base);
-  // xent: minus the sum of the others, which is what p - 1 leaves of a sure target
-  const float dz = tg.k == 0 ? f * ((ev - S) / S) : f * (Q * (ev / S) - w);
+  // Q p - w; of a likely token Q (p - 1) + (Q - w), the sums of the others
+  const float dz = short_of > -0.5f ? f * fmaf(Q, short_of, Q - w) : f * (Q * (term / S) - w);
   er[at] = __bfloat16_as_ushort(__float2bfloat16(dz));
 }
 

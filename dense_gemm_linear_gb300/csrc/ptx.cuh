@@ -545,4 +545,11 @@ __device__ __forceinline__ bool wait_flag_gpu(const int* p, int v) {
     if (global_timer_ns() - t0 > DGL_WAIT_LIMIT_NS) return false;
   }
 }
+
+// 2^x, subnormal results as zero.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 }  // namespace dgl

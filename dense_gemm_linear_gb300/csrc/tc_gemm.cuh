@@ -340,12 +340,6 @@ __device__ __forceinline__ void store_chunk_16(const CUtensorMap* map, uint8_t* 
   buf ^= 1u;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 operations in one instruction: the epilogue shares its schedulers
 // with the warp that issues the MMAs.
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -496,14 +490,17 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
       m4[j & 3] = fmaxf(m4[j & 3], fmaxf(__uint_as_float(r[0][j]), __uint_as_float(r[1][j])));
   }
   const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-  const float top = m == -INFINITY ? m : m * c;
-  // The exponent is y - Y + kHeadShift in one multiply-add, which rounds
-  // kHeadShift - Y.  Where Y is so large that this would show, the largest
-  // accumulator is subtracted first, which is exact near it.
-  const bool far = fabsf(top) > kHeadFar && m != -INFINITY;
+  // (rounded, not merged into the subtraction: see kHeadFar)
+  const float top = m == -INFINITY ? m : __fmul_rn(m, c);
+  const bool far = head_far(top) && m != -INFINITY;
   const bool any_far = __any_sync(0xFFFFFFFFu, far);
   const uint32_t minus = far ? __float_as_uint(-m) : 0u;
-  const float less = top == -INFINITY ? 0.0f : far ? kHeadShift : kHeadShift - top;
+  float less;
+  float base = head_base(top, less);
+  if (head_far(top)) {
+    base = top;
+    less = top == -INFINITY ? 0.0f : kHeadShift;
+  }
   const uint64_t c2 = pack2(__float_as_uint(c), __float_as_uint(c));
   const uint64_t less2 = pack2(__float_as_uint(less), __float_as_uint(less));
 
@@ -559,7 +556,7 @@ __device__ __forceinline__ void head_epilogue(const TcParams& p, const CUtensorM
   if (row < p.m) {
     float lo, hi;
     unpack2(add2(add2(s2[0], s2[1]), add2(s2[2], s2[3])), lo, hi);
-    h.part[static_cast<int64_t>(row) * h.part_ld + group] = make_float2(top, lo + hi);
+    h.part[static_cast<int64_t>(row) * h.part_ld + group] = make_float2(base, lo + hi);
   }
 }
 

@@ -371,12 +371,15 @@ dgl_status dgl_linear(int32_t dtype, const void* A, const void* B, const float* 
  *   size is the one reported as best.  Its contents mean nothing between
  *   calls.
  *
- * Accuracy.  Products and sums are fp32, statistics and losses fp32.  The
+ * Accuracy.  Products and sums are fp32, statistics and losses fp32; no loss of
+ * dgl_linear_xent is below zero.  The tensor cores' sums drop the bits below the
+ * last instead of rounding them: a logit is off by about 3e-6 of itself at
+ * d = 4096, and lse and the losses with it.  The
  * exponentials of a gradient wait for their sum in fp16, relative to the
  * largest of their row's 128 columns (or 64, where at most 128 tokens are taken
  * at a time): 11 bits down to 2^-29 of it, and nothing below 2^-40.  dz is then
- * rounded to bf16 (up to 2^-8 an entry; a target's entry is minus the sum of
- * the others, not p - 1) as the operand of the two products, without the
+ * rounded to bf16 (up to 2^-8 an entry; of a target with p above 1/2, p - 1 is
+ * minus the sum of the others) as the operand of the two products, without the
  * significand that the rows' common grad has, which the products' results are
  * multiplied by in fp32.  dX and a bf16 dW are rounded once more.
  *
