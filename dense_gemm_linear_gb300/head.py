@@ -1,7 +1,8 @@
 """Losses of a linear head on torch CUDA tensors (dgl_linear_xent, dgl_linear_distill).
 
 The helpers check their arguments, allocate what is not passed in with torch,
-and make one call of the library on torch's current stream.  On a few tokens
+and make one call of the library on torch's current stream.  The tensors are on
+the current device, where the library launches.  On a few tokens
 the kernels take about as long as this module does, so the checks are written
 out rather than shared.
 """
@@ -18,10 +19,17 @@ _BF16, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
 _byref = ctypes.byref
 
 
-def _rows(t, name, dtype, shape):
-    """Checks a CUDA matrix of `shape` whose rows are contiguous; returns its row pitch in elements."""
+def _on_device(t, name, device):
+    """Checks that a tensor is on the current device, where the library launches."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{device}")
+
+
+def _rows(t, name, dtype, shape, device):
+    """Checks a matrix of `shape` whose rows are contiguous; returns its row pitch in elements."""
+    _on_device(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -36,10 +44,9 @@ def _rows(t, name, dtype, shape):
     return pitch
 
 
-def _packed(t, name, dtype, shape):
-    """Checks a contiguous CUDA tensor; returns its address."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _packed(t, name, dtype, shape, device):
+    """Checks a contiguous tensor; returns its address."""
+    _on_device(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -53,22 +60,21 @@ def _workspace_bytes(T, V, d, grad, dX, dW, dw_dtype, k):
     return max(1, dgl_head_workspace(h, k)[1])
 
 
-def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, k):
+def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, k, device):
     """Checks and allocates on the current stream; returns the descriptor and the tensors to return."""
     if not isinstance(X, torch.Tensor) or X.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise TypeError("X and W must be 2-D CUDA tensors")
     T, d = X.shape
     V = W.shape[0]
-    ldx = _rows(X, "X", _BF16, (T, d))
-    ldw = _rows(W, "W", _BF16, (V, d))
-    device = X.device
+    ldx = _rows(X, "X", _BF16, (T, d), device)
+    ldw = _rows(W, "W", _BF16, (V, d), device)
     if dw_dtype not in (OUT_BF16, OUT_F32):
         raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
     p_grad = p_dx = p_dw = lddw = 0
     dw_type = OUT_BF16
     dX = None
     if grad is not None:
-        p_grad = _packed(grad, "grad", _F32, (T,))
+        p_grad = _packed(grad, "grad", _F32, (T,), device)
         if not (need_dx or need_dw):
             raise ValueError("a call with grad computes dX, dW or both")
         if need_dx:
@@ -84,7 +90,7 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
             else:
                 if dW.dtype not in (_F32, _BF16):
                     raise TypeError(f"dW must be fp32 or bf16, got {dW.dtype}")
-                lddw = _rows(dW, "dW", dW.dtype, (V, d))
+                lddw = _rows(dW, "dW", dW.dtype, (V, d), device)
                 dw_type = OUT_F32 if dW.dtype == _F32 else OUT_BF16
             p_dw = dW.data_ptr()
         elif dW is not None or accumulate:
@@ -96,8 +102,10 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
     if workspace is None:
         size = _workspace_bytes(T, V, d, p_grad != 0, p_dx != 0, p_dw != 0, dw_type, k)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    else:
+        _on_device(workspace, "workspace", device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
     h = HeadDesc(T, V, d, X.data_ptr(), ldx, W.data_ptr(), ldw, loss.data_ptr(), lse.data_ptr(), p_grad, p_dx, d, p_dw,
                  lddw, workspace.data_ptr(), workspace.nbytes, logit_scale, dw_type, 1 if accumulate else 0)
     # the workspace is returned to be held until the call has been made
@@ -113,7 +121,8 @@ def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_sc
     final scalar by each loss (1 / tokens for a mean), returns (loss, lse, dX,
     dW): dX bf16, dW bf16 or fp32 (dw_dtype, or the type of the dW passed in;
     accumulate adds to an fp32 dW).  workspace: a CUDA buffer of at least
-    dgl_head_workspace bytes, made when None.
+    dgl_head_workspace bytes, made when None.  All tensors are on the current
+    device (stream's, when one is given).
     """
     if stream is not None:
         # buffers made here belong to the stream that uses them, so the
@@ -122,9 +131,10 @@ def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_sc
             return linear_cross_entropy(X, W, target, grad, ignore_index=ignore_index, logit_scale=logit_scale,
                                         need_dx=need_dx, need_dw=need_dw, dW=dW, dw_dtype=dw_dtype,
                                         accumulate=accumulate, workspace=workspace)
-    h, out, held = _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, 0)
-    at = _packed(target, "target", _I64, (X.shape[0],))
-    st = load_library().dgl_linear_xent(_byref(h), at, ignore_index, torch._C._cuda_getCurrentRawStream(X.device.index))
+    device = torch.cuda.current_device()
+    h, out, held = _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, 0, device)
+    at = _packed(target, "target", _I64, (X.shape[0],), device)
+    st = load_library().dgl_linear_xent(_byref(h), at, ignore_index, torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_linear_xent")
     return out
@@ -149,13 +159,14 @@ def linear_distill(X, W, indices, logits, grad=None, *, temperature=1.0, teacher
     k = indices.shape[1] if indices.dim() == 2 else 0
     if not 1 <= k <= DISTILL_MAX_K:
         raise ValueError(f"indices must be [T, k] with 1 <= k <= {DISTILL_MAX_K}")
-    h, out, held = _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, k)
+    device = torch.cuda.current_device()
+    h, out, held = _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, k, device)
     shape = (X.shape[0], k)
-    at = _packed(indices, "indices", _I64, shape)
-    values = _packed(logits, "logits", _F32, shape)
-    lse_at = None if teacher_lse is None else _packed(teacher_lse, "teacher_lse", _F32, shape[:1])
+    at = _packed(indices, "indices", _I64, shape, device)
+    values = _packed(logits, "logits", _F32, shape, device)
+    lse_at = None if teacher_lse is None else _packed(teacher_lse, "teacher_lse", _F32, shape[:1], device)
     st = load_library().dgl_linear_distill(_byref(h), at, values, lse_at, k, temperature,
-                                           torch._C._cuda_getCurrentRawStream(X.device.index))
+                                           torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_linear_distill")
     return out
