@@ -264,8 +264,17 @@ def dgl_version() -> int:
 
 
 # ---------------------------------------------------------------- torch helpers
-def _stream_handle(stream):
+def _stream_handle(stream, *tensors):
+    """The handle of `stream` (None: the current one) for a call on `tensors`: they and the stream are on the
+    current device, where the library launches."""
     import torch
+    if tensors:
+        device = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{device}")
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, but the current device is cuda:{device}")
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -302,7 +311,7 @@ def gemm_bf16(A, B, out=None, *, out_dtype=OUT_BF16, stream=None, plan: PlanInfo
     if K != K2:
         raise ValueError("inner dimensions differ")
     C, ldc, rows = _out_tensor(out, m, n, out_dtype, A.device)
-    s = _stream_handle(stream)
+    s = _stream_handle(stream, A, B, C)
     if plan is None:
         st = dgl_gemm_bf16(A.data_ptr(), B.data_ptr(), C.data_ptr(), rows, ldc, K, m, n, out_dtype, s)
     else:
@@ -325,7 +334,7 @@ def gemm_fp8(A, B, sa, sb, out=None, *, out_dtype=OUT_BF16, stream=None, plan: P
         if s_.dtype != torch.float32 or not s_.is_cuda or s_.numel() != length or not s_.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of length {length}")
     C, ldc, rows = _out_tensor(out, m, n, out_dtype, A.device)
-    s = _stream_handle(stream)
+    s = _stream_handle(stream, A, B, sa, sb, C)
     if plan is None:
         st = dgl_gemm_fp8(A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), C.data_ptr(), rows, ldc, K,
                           m, n, out_dtype, s)
@@ -352,7 +361,7 @@ def gemm_mxfp4(A, B, sfa, sfb, K, out=None, *, out_dtype=OUT_BF16, stream=None):
             raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor of shape {shape}")
     C, ldc, rows = _out_tensor(out, m, n, out_dtype, A.device)
     st = dgl_gemm_mxfp4(A.data_ptr(), B.data_ptr(), sfa.data_ptr(), sfb.data_ptr(), C.data_ptr(), rows, ldc, K, m,
-                        n, out_dtype, _stream_handle(stream))
+                        n, out_dtype, _stream_handle(stream, A, B, sfa, sfb, C))
     _check(st, "dgl_gemm_mxfp4")
     return C
 
@@ -376,7 +385,7 @@ def gemm_w4a8(A, B, sa, sb, K, out=None, *, out_dtype=OUT_BF16, stream=None):
             raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of length {length}")
     C, ldc, rows = _out_tensor(out, m, n, out_dtype, A.device)
     st = dgl_gemm_w4a8(A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), C.data_ptr(), rows, ldc, K, m, n,
-                       out_dtype, _stream_handle(stream))
+                       out_dtype, _stream_handle(stream, A, B, sa, sb, C))
     _check(st, "dgl_gemm_w4a8")
     return C
 
@@ -424,7 +433,7 @@ def linear(A, B, bias=None, out=None, *, act=ACT_NONE, gated=False, sa=None, sb=
     st = dgl_linear(DTYPE_E4M3 if e4m3 else DTYPE_BF16, A.data_ptr(), B.data_ptr(),
                     sa.data_ptr() if e4m3 else None, sb.data_ptr() if e4m3 else None,
                     bias.data_ptr() if bias is not None else None, C.data_ptr(), rows, ldc, K, m, n, out_dtype,
-                    int(act), int(bool(gated)), plan, _stream_handle(stream))
+                    int(act), int(bool(gated)), plan, _stream_handle(stream, A, B, C, *(v for _, v, _ in vecs)))
     _check(st, "dgl_linear")
     return C
 
