@@ -112,6 +112,19 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
     return h, ((loss, lse) if grad is None else (loss, lse, dX, dW)), workspace
 
 
+def _on_stream(stream, call, *tensors):
+    """Makes a call on `stream` in place of the current one."""
+    # buffers made by the call belong to the stream that uses them, and the
+    # caller's are marked as used there: the allocator hands either out again
+    # only after its work
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return out
+
+
 def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_scale=1.0, need_dx=True, need_dw=True,
                          dW=None, dw_dtype=OUT_BF16, accumulate=False, workspace=None, stream=None):
     """Softmax cross entropy of the head z = logit_scale X . W^T, without keeping the logits.
@@ -125,12 +138,9 @@ def linear_cross_entropy(X, W, target, grad=None, *, ignore_index=-100, logit_sc
     device (stream's, when one is given).
     """
     if stream is not None:
-        # buffers made here belong to the stream that uses them, so the
-        # allocator hands them out again only after its work
-        with torch.cuda.stream(stream):
-            return linear_cross_entropy(X, W, target, grad, ignore_index=ignore_index, logit_scale=logit_scale,
-                                        need_dx=need_dx, need_dw=need_dw, dW=dW, dw_dtype=dw_dtype,
-                                        accumulate=accumulate, workspace=workspace)
+        return _on_stream(stream, lambda: linear_cross_entropy(
+            X, W, target, grad, ignore_index=ignore_index, logit_scale=logit_scale, need_dx=need_dx, need_dw=need_dw,
+            dW=dW, dw_dtype=dw_dtype, accumulate=accumulate, workspace=workspace), X, W, target, grad, dW, workspace)
     device = torch.cuda.current_device()
     h, out, held = _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, workspace, 0, device)
     at = _packed(target, "target", _I64, (X.shape[0],), device)
@@ -152,10 +162,10 @@ def linear_distill(X, W, indices, logits, grad=None, *, temperature=1.0, teacher
     Otherwise as linear_cross_entropy.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return linear_distill(X, W, indices, logits, grad, temperature=temperature, teacher_lse=teacher_lse,
-                                  logit_scale=logit_scale, need_dx=need_dx, need_dw=need_dw, dW=dW, dw_dtype=dw_dtype,
-                                  accumulate=accumulate, workspace=workspace)
+        return _on_stream(stream, lambda: linear_distill(
+            X, W, indices, logits, grad, temperature=temperature, teacher_lse=teacher_lse, logit_scale=logit_scale,
+            need_dx=need_dx, need_dw=need_dw, dW=dW, dw_dtype=dw_dtype, accumulate=accumulate, workspace=workspace),
+            X, W, indices, logits, grad, teacher_lse, dW, workspace)
     k = indices.shape[1] if indices.dim() == 2 else 0
     if not 1 <= k <= DISTILL_MAX_K:
         raise ValueError(f"indices must be [T, k] with 1 <= k <= {DISTILL_MAX_K}")
