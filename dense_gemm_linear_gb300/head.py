@@ -19,17 +19,17 @@ _BF16, _F32, _I64 = torch.bfloat16, torch.float32, torch.int64
 _byref = ctypes.byref
 
 
-def _on_device(t, name, device):
-    """Checks that a tensor is on the current device, where the library launches."""
+def _not_here(t, name, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{device}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{device}")
 
 
 def _rows(t, name, dtype, shape, device):
-    """Checks a matrix of `shape` whose rows are contiguous; returns its row pitch in elements."""
-    _on_device(t, name, device)
+    """Checks a matrix of `shape` whose rows are contiguous on the current device, where the library launches;
+    returns its row pitch in elements."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _not_here(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -45,8 +45,9 @@ def _rows(t, name, dtype, shape, device):
 
 
 def _packed(t, name, dtype, shape, device):
-    """Checks a contiguous tensor; returns its address."""
-    _on_device(t, name, device)
+    """Checks a contiguous tensor on the current device; returns its address."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _not_here(t, name, device)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -103,7 +104,8 @@ def _head(X, W, grad, logit_scale, need_dx, need_dw, dW, dw_dtype, accumulate, w
         size = _workspace_bytes(T, V, d, p_grad != 0, p_dx != 0, p_dw != 0, dw_type, k)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
-        _on_device(workspace, "workspace", device)
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device:
+            _not_here(workspace, "workspace", device)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
     h = HeadDesc(T, V, d, X.data_ptr(), ldx, W.data_ptr(), ldw, loss.data_ptr(), lse.data_ptr(), p_grad, p_dx, d, p_dw,
