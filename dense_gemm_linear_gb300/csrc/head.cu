@@ -10,7 +10,7 @@
 //            dz = (grad s / m) (Q e / S - q) in bf16 in the place of e
 //   dX = m dz W, dW = m dz^T x  (tile kernel)
 // m, between 1 and 2, is the significand of one row's |grad s|: where all rows
-// have the same grad (a mean), grad s / m is a power of two, and the targets'
+// have the same grad (a mean) or none, grad s / m is a power of two, and the targets'
 // entries, near -grad s in every row that does not predict them, do not all
 // carry the rounding of that one number into dX and dW.
 // T x V values take 2 bytes of workspace for the chunk's tokens, are written
@@ -199,12 +199,38 @@ __global__ void __launch_bounds__(32 * kPrepareWarps)
   }
 }
 
-// m of the call: the significand of |grad s| of its first row, of the first 32,
-// with a nonzero grad; lane i holds row i's (0 past the last).  By one warp.
+// m of a chunk: the significand of |grad s| of its first row whose grad s is a
+// normal number (1 where none is).
+__device__ __forceinline__ bool is_normal(float g) { return fabsf(g) >= 1.17549435e-38f && fabsf(g) < INFINITY; }
+__device__ __forceinline__ float significand(float g) {
+  return __uint_as_float((__float_as_uint(g) & 0x007FFFFFu) | 0x3F800000u);
+}
+// By a warp: m where one of the first 32 rows decides it (lane i holds row i's
+// grad s, 0 past the last), else 0.
 __device__ __forceinline__ float common_significand(float g) {
-  const uint32_t normal = __ballot_sync(0xffffffffu, fabsf(g) >= 1.17549435e-38f && fabsf(g) < INFINITY);
-  const uint32_t bits = __shfl_sync(0xffffffffu, __float_as_uint(g), normal ? __ffs(normal) - 1 : 0);
-  return normal ? __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u) : 1.0f;
+  const uint32_t normal = __ballot_sync(0xffffffffu, is_normal(g));
+  const float first = __shfl_sync(0xffffffffu, g, normal ? __ffs(normal) - 1 : 0);
+  return normal ? significand(first) : 0.0f;
+}
+// By a block, for a chunk that starts with 32 rows or more without a grad (a
+// prompt that is masked by its weights): rows 32 .. n - 1, 4 THREADS at a time.
+template <int THREADS>
+__device__ float search_significand(const float* __restrict__ grad, float scale, int n, int* found) {
+  for (int i0 = 32; i0 < n; i0 += 4 * THREADS) {
+    int mine = INT_MAX;
+#pragma unroll
+    for (int u = 3; u >= 0; --u) {
+      const int i = i0 + u * THREADS + threadIdx.x;
+      if (i < n && is_normal(grad[i] * scale)) mine = i;
+    }
+    mine = __reduce_min_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) found[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 32; ++w) mine = min(mine, found[w]);
+    if (mine != INT_MAX) return significand(grad[mine] * scale);
+    __syncthreads();  // read by all before it is written again
+  }
+  return 1.0f;
 }
 
 // A gradient's blocks of short rows (or slices) are of 128 threads, so that all
@@ -223,10 +249,9 @@ constexpr int64_t kFinishShort = 32768;  // columns
 template <bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,
-                       const float* __restrict__ first_grad, int first_rows, float* __restrict__ out_scale,
-                       float* __restrict__ loss, float* __restrict__ lse_out, uint16_t* __restrict__ e, int64_t lde,
-                       const __nv_bfloat16* __restrict__ x, int64_t ldx, __nv_bfloat16* __restrict__ xs, int d,
-                       int* __restrict__ flags, int nflags) {
+                       float* __restrict__ out_scale, float* __restrict__ loss, float* __restrict__ lse_out,
+                       uint16_t* __restrict__ e, int64_t lde, const __nv_bfloat16* __restrict__ x, int64_t ldx,
+                       __nv_bfloat16* __restrict__ xs, int d, int* __restrict__ flags, int nflags) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int WARPS = THREADS / 32;
@@ -259,7 +284,7 @@ __global__ void __launch_bounds__(THREADS)
     }
   };
   if (GRAD) fetch(u0 + threadIdx.x);
-  const float g32 = GRAD && lane < first_rows ? first_grad[lane] * scale : 0.0f;
+  const float g32 = GRAD && lane < gridDim.x ? grad[lane] * scale : 0.0f;
   const float g_row = GRAD ? grad[row] * scale : 0.0f;
   // the row's targets, entry j (of k, at most kMaxK) with thread j: its column
   // (-1: none), weight, accumulator and its group's base
@@ -345,9 +370,16 @@ __global__ void __launch_bounds__(THREADS)
   if (!GRAD) return;
 
   const bool has = state == 1;
-  const float common = common_significand(g32);
-  if (row == 0 && lead && threadIdx.x == 0) *out_scale = common;
-  const float f = has ? __fdiv_rn(g_row, common) : 0.0f;
+  const bool writes = row == 0 && lead;
+  float common = common_significand(g32);
+  // rows that need m and do not see it yet look for it, as far as themselves
+  // where their own grad would do
+  if (common == 0.0f && (writes || (has && g_row != 0.0f))) {
+    __shared__ int found[WARPS];
+    common = search_significand<THREADS>(grad, scale, is_normal(g_row) ? row + 1 : gridDim.x, found);
+  }
+  if (writes && threadIdx.x == 0) *out_scale = common;
+  const float f = has && g_row != 0.0f ? __fdiv_rn(g_row, common) : 0.0f;
   const float fS = f * (Q / S);
   if (!has) {
     for (int i = u0 + threadIdx.x; i < u1; i += THREADS) e8[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -753,9 +785,8 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
                          : small ? head_finish_kernel<true, 128>
                                  : head_finish_kernel<true, 256>,
                          finish, small ? 128 : 256, stream, tg, rows, V, scale, c,
-                         grad ? h.grad + t0 : nullptr, h.grad, static_cast<int>(std::min<int64_t>(h.T, 32)), out_scale,
-                         h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde, x, h.ldx,
-                         xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
+                         grad ? h.grad + t0 : nullptr, out_scale, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde,
+                         x, h.ldx, xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
       return DGL_ERR_CUDA;
 
     if (h.dX) {
