@@ -243,8 +243,8 @@ constexpr int64_t kFinishShort = 32768;  // columns
 // One block per row, and with few rows several, each for a slice of the
 // vocabulary (gridDim.y; all of them reduce the row's statistics): statistics
 // of the row's column groups -> loss and lse; with e (gradient), e -> dz in
-// place (zero up to a multiple of 8 columns), and x for dW = dz^T x, zero where
-// the row has no gradient (0 x NaN would reach dW).  A gradient is bound by
+// place (zero up to a multiple of 8 columns), and, when dW is asked for, x for dW =
+// dz^T x, zero where the row has no gradient (0 x NaN would reach dW).  A gradient is bound by
 // reading e and writing dz: 10240 x 50257 in 305 us, 6.8 TB/s.
 template <bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS)
@@ -409,10 +409,12 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
-  uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
-  for (int i = threadIdx.x + blockIdx.y * THREADS; i < d / 8; i += THREADS * gridDim.y)
-    xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
+  if (xs) {
+    const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+    uint4* xo = reinterpret_cast<uint4*>(xs + static_cast<int64_t>(row) * d);
+    for (int i = threadIdx.x + blockIdx.y * THREADS; i < d / 8; i += THREADS * gridDim.y)
+      xo[i] = has ? xr[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
   if (!has) return;
   __syncthreads();
   // this thread's entry, if its column lies in this block's slice; entries of
@@ -485,9 +487,9 @@ __global__ void head_to_bf16_kernel(const float* __restrict__ src, int64_t lds, 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Chunk and workspace.  Rows of a chunk hold e (gradient), the prepared rows
-// and the column groups' statistics; the gradient also needs x, the fp32 sums of
-// dX's ranges or partial tiles and, when several chunks add up to a bf16 dW, its
-// fp32 sums.
+// and the column groups' statistics; dX also needs the fp32 sums of its ranges or
+// partial tiles, dW the rows of x and, when several chunks add up to a bf16 one,
+// its fp32 sums.
 struct HeadLayout {
   int64_t chunk = 0;  // tokens at a time (0: does not fit)
   int64_t lde = 0;    // row pitch of e, elements
@@ -556,9 +558,11 @@ HeadLayout layout_for(const dgl_head_desc& h, int k, int64_t chunk) {
   };
   if (grad) {
     l.e = take(rows * l.lde * 2);
-    l.xs = take(rows * h.d * 2);
-    l.split = take(int64_t(kSplitSlots) * 128 * 256 * 4);
-    l.flags = take(kSplitSlots * 4);
+    if (h.dW) l.xs = take(rows * h.d * 2);
+    if (h.dX) {
+      l.split = take(int64_t(kSplitSlots) * 128 * 256 * 4);
+      l.flags = take(kSplitSlots * 4);
+    }
     l.out_scale = take(4);
   }
   l.part = take(std::max(rows * groups, narrow) * 8);
@@ -694,7 +698,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
   const bool grad = h.grad != nullptr;
   uint8_t* ws = static_cast<uint8_t*>(h.ws);
   uint16_t* e = grad ? reinterpret_cast<uint16_t*>(ws + lay.e) : nullptr;
-  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(ws + lay.xs);
+  __nv_bfloat16* xs = h.dW ? reinterpret_cast<__nv_bfloat16*>(ws + lay.xs) : nullptr;
   SplitScratch scratch;
   scratch.ws = reinterpret_cast<float*>(ws + lay.split);
   scratch.ws_bytes = size_t(kSplitSlots) * 128 * 256 * 4;
@@ -786,7 +790,7 @@ dgl_status run_head(const dgl_head_desc* hp, const HeadTargets& targets, float s
                                  : head_finish_kernel<true, 256>,
                          finish, small ? 128 : 256, stream, tg, rows, V, scale, c,
                          grad ? h.grad + t0 : nullptr, out_scale, h.loss + t0, h.lse ? h.lse + t0 : nullptr, e, lay.lde,
-                         x, h.ldx, xs, d, scratch.flags, grad ? kSplitSlots : 0) != cudaSuccess)
+                         x, h.ldx, xs, d, scratch.flags, h.dX ? kSplitSlots : 0) != cudaSuccess)
       return DGL_ERR_CUDA;
 
     if (h.dX) {
