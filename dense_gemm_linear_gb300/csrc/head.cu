@@ -866,8 +866,10 @@ dgl_status dgl_linear_xent(const dgl_head_desc* head, const int64_t* target, int
 
 dgl_status dgl_linear_distill(const dgl_head_desc* head, const int64_t* indices, const float* logits,
                               const float* teacher_lse, int32_t k, float temperature, void* stream) {
-  if (!head || k < 1 || !(temperature > 0.0f) || !std::isfinite(temperature)) return DGL_ERR_ARG;
-  const HeadTargets tg{indices, 0, logits, teacher_lse, 1.0f / temperature, k};
+  const float inv_temp = 1.0f / temperature;
+  if (!head || k < 1 || !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(inv_temp))
+    return DGL_ERR_ARG;
+  const HeadTargets tg{indices, 0, logits, teacher_lse, inv_temp, k};
   return run_head(head, tg, head->logit_scale / temperature, static_cast<cudaStream_t>(stream));
 }
 

@@ -437,12 +437,13 @@ dgl_status dgl_linear_xent(const dgl_head_desc* head, const int64_t* target, int
  * Distillation of a linear head from a teacher's top logits.  indices: int64
  * [T][k], rows of W or negative for an absent entry; logits: fp32 [T][k], the
  * teacher's logits of those entries; 1 <= k <= DGL_DISTILL_MAX_K.  Both
- * distributions are taken at `temperature` (> 0): the student's logits are
- * z / temperature, and lse is theirs.  teacher_lse NULL: q_t is the softmax of
- * the row's entries, which then sum to one.  teacher_lse fp32 [T]: the
- * teacher's log-normaliser over its whole vocabulary at that temperature, and
- * q_tk = exp(logit / temperature - teacher_lse_t), which sum to the kept mass
- * Q_t.  An index given twice counts twice.  Errors as dgl_linear_xent.
+ * distributions are taken at `temperature` (> 0, its reciprocal finite): the
+ * student's logits are z / temperature, and lse is theirs.  teacher_lse NULL:
+ * q_t is the softmax of the row's entries, which then sum to one.  teacher_lse
+ * fp32 [T]: the teacher's log-normaliser over its whole vocabulary at that
+ * temperature, and q_tk = exp(logit / temperature - teacher_lse_t), which sum to
+ * the kept mass Q_t.  An index given twice counts twice.  Errors as
+ * dgl_linear_xent.
  */
 dgl_status dgl_linear_distill(const dgl_head_desc* head, const int64_t* indices, const float* logits,
                               const float* teacher_lse, int32_t k, float temperature, void* stream);
