@@ -438,8 +438,6 @@ def linear(A, B, bias=None, out=None, *, act=ACT_NONE, gated=False, sa=None, sb=
     return C
 
 
-
-
 def __getattr__(name):
     # the head losses' helpers (head.py) import torch when they are first used
     if name in ("linear_cross_entropy", "linear_distill"):

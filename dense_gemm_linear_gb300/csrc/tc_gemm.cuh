@@ -1148,7 +1148,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         next_acc<Cfg::ACC_BUFS>(acc, acc_phase);
         continue;
       }
-      bool gated_done = Cfg::LOGITS;
+      bool gated_done = false;
       if constexpr (BN == 256) {
         if (sg.half) {
           // ---- a half tile of the split tail: BN / 2 columns in TMEM
