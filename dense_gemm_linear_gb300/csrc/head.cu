@@ -80,9 +80,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 constexpr int kPrepareWarps = 4;
 
 // Distill, one warp per row: the teacher's distribution over the row's entries
-// in fp32, the entries sorted by column (an entry's place is the
-// number of entries before it, k^2 comparisons by 32 lanes), and the number of
-// them before each tile of columns.  Bound by latency: 4.7 us at k = 1, 7.4 us at
+// in fp32, the entries sorted by column (an entry's place is the number of
+// entries before it, k^2 comparisons by 32 lanes), and the number of them before
+// each tile of columns.  Bound by latency: 4.7 us at k = 1, 7.6 us at
 // k = 64 (1024 rows, V = 50257).
 // PER: entries a lane holds (k at most 32 PER).
 template <int PER>
@@ -243,9 +243,10 @@ constexpr int64_t kFinishShort = 32768;  // columns
 // One block per row, and with few rows several, each for a slice of the
 // vocabulary (gridDim.y; all of them reduce the row's statistics): statistics
 // of the row's column groups -> loss and lse; with e (gradient), e -> dz in
-// place (zero up to a multiple of 8 columns), and, when dW is asked for, x for dW =
-// dz^T x, zero where the row has no gradient (0 x NaN would reach dW).  A gradient is bound by
-// reading e and writing dz: 10240 x 50257 in 305 us, 6.8 TB/s.
+// place (zero up to a multiple of 8 columns), and, when dW is asked for, x for
+// dW = dz^T x, zero where the row has no gradient (0 x NaN would reach dW).  A
+// gradient is bound by reading e and writing dz: 10240 x 50257 in 305 to 328 us,
+// 6.8 to 6.3 TB/s, on different GPUs.
 template <bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     head_finish_kernel(HeadTargets tg, HeadRows rows, int V, float scale, float c, const float* __restrict__ grad,

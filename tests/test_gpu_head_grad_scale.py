@@ -24,16 +24,23 @@ GRAD = 1.0 + 2.0**-8
 @pytest.mark.parametrize("zeros,how", [(0, "grad"), (31, "grad"), (40, "grad"), (300, "grad"), (1100, "grad"), (700, "ignored")])
 @pytest.mark.parametrize("workspace", ["one chunk", "chunks"])
 def test_common_significand(op, zeros, how, workspace):
-    T, V, d = zeros + 150, 8192, 64
+    _common_significand(op, zeros, how, workspace, 8192)
+
+
+def test_common_significand_of_long_rows():
+    """Rows past 32768 columns, each finished by one larger block."""
+    _common_significand("xent", 1100, "grad", "one chunk", 40001)
+
+
+def _common_significand(op, zeros, how, workspace, V):
+    T, d = zeros + 150, 64
     g = _gen(0)
     X = torch.randn(T, d, device=DEV, generator=g).bfloat16()
     W = (0.002 * torch.randn(V, d, device=DEV, generator=g)).bfloat16()
     target = torch.randperm(V, device=DEV, generator=g)[:T].contiguous()
     grad = torch.full((T,), GRAD, device=DEV)
-    if how == "grad":
-        grad[:zeros] = 0.0
-    else:
-        grad[:zeros] = 0.0
+    grad[:zeros] = 0.0
+    if how == "ignored":
         target[:zeros] = IGNORE
     ws = None
     if workspace == "chunks":
