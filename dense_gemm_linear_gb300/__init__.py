@@ -43,9 +43,12 @@ MN_MAJOR = 1
 EXPORTED = ["dgl_gemm_bf16", "dgl_gemm_fp8", "dgl_gemm_planned", "dgl_plan", "dgl_tile_metrics",
             "dgl_device_status", "dgl_status_string", "dgl_version", "dgl_gemm_noalloc", "dgl_linear",
             "dgl_plan_linear", "dgl_gemm_bf16_ex", "dgl_gemm_mxfp4", "dgl_shutdown", "dgl_gemm_w4a8",
-            "dgl_gemm_batch", "dgl_head_workspace", "dgl_linear_xent", "dgl_linear_distill"]
+            "dgl_gemm_batch", "dgl_head_workspace", "dgl_linear_xent", "dgl_linear_distill",
+            "dgl_embedding", "dgl_embedding_grad", "dgl_embedding_workspace", "dgl_layer_norm", "dgl_layer_norm_grad",
+            "dgl_layer_norm_workspace", "dgl_adamw"]
 
 DISTILL_MAX_K = 128
+ADAMW_BLOCK = 128
 
 
 class PlanInfo(ctypes.Structure):
@@ -75,6 +78,42 @@ class HeadDesc(ctypes.Structure):
                 ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("ws", ctypes.c_void_p),
                 ("ws_bytes", ctypes.c_int64), ("logit_scale", ctypes.c_float), ("dw_dtype", ctypes.c_int32),
                 ("accumulate", ctypes.c_int32)]
+
+
+class EmbedDesc(ctypes.Structure):
+    """Arguments of the embedding's calls (the C struct dgl_embed_desc)."""
+    _fields_ = [("T", ctypes.c_int64), ("V", ctypes.c_int64), ("d", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("ignore_index", ctypes.c_int64), ("W", ctypes.c_void_p), ("dW", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("Y", ctypes.c_void_p), ("dY", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("w_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    """Arguments of the layer norm's calls (the C struct dgl_norm_desc)."""
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("dw_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """A tensor of an AdamW step (the C struct dgl_adamw_tensor)."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class AdamWDesc(ctypes.Structure):
+    """What the tensors of an AdamW step share (the C struct dgl_adamw_desc)."""
+    _fields_ = [("steps", ctypes.c_void_p), ("ticket", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("lr_at", ctypes.c_void_p), ("lr", ctypes.c_double), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double), ("seed", ctypes.c_uint64),
+                ("state_bits", ctypes.c_int32)]
 
 
 class DglError(RuntimeError):
@@ -125,6 +164,18 @@ def load_library(path: str | None = None):
     lib.dgl_linear_xent.restype = i32
     lib.dgl_linear_distill.argtypes = [ctypes.POINTER(HeadDesc), vp, vp, vp, i32, ctypes.c_float, vp]
     lib.dgl_linear_distill.restype = i32
+    for name in ("dgl_embedding", "dgl_embedding_grad"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(EmbedDesc), vp]
+        getattr(lib, name).restype = i32
+    lib.dgl_embedding_workspace.argtypes = [ctypes.POINTER(EmbedDesc), ctypes.POINTER(i64)]
+    lib.dgl_embedding_workspace.restype = i32
+    for name in ("dgl_layer_norm", "dgl_layer_norm_grad"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(NormDesc), vp]
+        getattr(lib, name).restype = i32
+    lib.dgl_layer_norm_workspace.argtypes = [ctypes.POINTER(NormDesc), ctypes.POINTER(i64)]
+    lib.dgl_layer_norm_workspace.restype = i32
+    lib.dgl_adamw.argtypes = [ctypes.POINTER(AdamWDesc), ctypes.POINTER(AdamWTensor), i32, vp]
+    lib.dgl_adamw.restype = i32
     lib.dgl_plan.argtypes = [i32, i64, i64, i64, i32, i32, ctypes.POINTER(PlanInfo)]
     lib.dgl_plan.restype = i32
     lib.dgl_tile_metrics.argtypes = [i64, i64, i32, i32, i32, ctypes.POINTER(PlanInfo)]
@@ -228,6 +279,45 @@ def dgl_linear_xent(head: HeadDesc, target, ignore_index=-100, stream=0) -> int:
 def dgl_linear_distill(head: HeadDesc, indices, logits, teacher_lse, k, temperature=1.0, stream=0) -> int:
     """Distillation of a linear head from a teacher's top logits (see include/dgl.h)."""
     return load_library().dgl_linear_distill(ctypes.byref(head), indices, logits, teacher_lse, k, temperature, stream)
+
+
+def dgl_embedding(embed: EmbedDesc, stream=0) -> int:
+    """Embedding lookup (see include/dgl.h)."""
+    return load_library().dgl_embedding(ctypes.byref(embed), stream)
+
+
+def dgl_embedding_grad(embed: EmbedDesc, stream=0) -> int:
+    """The gradient of an embedding (see include/dgl.h)."""
+    return load_library().dgl_embedding_grad(ctypes.byref(embed), stream)
+
+
+def dgl_embedding_workspace(embed: EmbedDesc) -> int:
+    """Workspace bytes of dgl_embedding_grad."""
+    size = ctypes.c_int64()
+    _check(load_library().dgl_embedding_workspace(ctypes.byref(embed), ctypes.byref(size)), "dgl_embedding_workspace")
+    return size.value
+
+
+def dgl_layer_norm(norm: NormDesc, stream=0) -> int:
+    """Layer norm, forward (see include/dgl.h)."""
+    return load_library().dgl_layer_norm(ctypes.byref(norm), stream)
+
+
+def dgl_layer_norm_grad(norm: NormDesc, stream=0) -> int:
+    """Layer norm, backward (see include/dgl.h)."""
+    return load_library().dgl_layer_norm_grad(ctypes.byref(norm), stream)
+
+
+def dgl_layer_norm_workspace(norm: NormDesc) -> int:
+    """Workspace bytes of dgl_layer_norm_grad's weight gradients."""
+    size = ctypes.c_int64()
+    _check(load_library().dgl_layer_norm_workspace(ctypes.byref(norm), ctypes.byref(size)), "dgl_layer_norm_workspace")
+    return size.value
+
+
+def dgl_adamw(desc: AdamWDesc, tensors, stream=0) -> int:
+    """A step of AdamW over many tensors (see include/dgl.h); tensors: an array of AdamWTensor."""
+    return load_library().dgl_adamw(ctypes.byref(desc), tensors, len(tensors), stream)
 
 
 def dgl_plan(dtype, m, n, K, out_dtype=OUT_BF16, num_sms=0) -> PlanInfo:
@@ -438,11 +528,14 @@ def linear(A, B, bias=None, out=None, *, act=ACT_NONE, gated=False, sa=None, sb=
     return C
 
 
+# helpers of modules that import torch when they are first used
+_LAZY = {"linear_cross_entropy": "head", "linear_distill": "head", "embedding": "embed", "embedding_grad": "embed",
+         "layer_norm": "norm", "layer_norm_grad": "norm", "AdamW": "optim"}
+
+
 def __getattr__(name):
-    # the head losses' helpers (head.py) import torch when they are first used
-    if name in ("linear_cross_entropy", "linear_distill"):
-        from . import head
-        globals()["linear_cross_entropy"] = head.linear_cross_entropy
-        globals()["linear_distill"] = head.linear_distill
+    if name in _LAZY:
+        import importlib
+        globals()[name] = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -25,7 +25,7 @@ COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--
                 "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["api.cu", "plan.cpp", "tc_bf16.cu", "tc_e4m3.cu", "tc_bf16_m64.cu", "tc_e4m3_m64.cu", "tc_bf16_epi.cu",
            "tc_e4m3_epi.cu", "tc_mxfp4.cu", "decode.cu", "head.cu",
-           "tc_head.cu", "tc_scaled.cu"]
+           "tc_head.cu", "tc_scaled.cu", "embed.cu", "norm.cu", "adamw.cu"]
 
 
 def nvcc() -> str:

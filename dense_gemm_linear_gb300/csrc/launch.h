@@ -23,6 +23,28 @@ cudaError_t set_smem_attr_once(Kernel kern, int bytes, std::atomic<uint64_t>& do
   return e;
 }
 
+// Launch of a kernel that starts with griddep_wait; smem: its dynamic shared memory.
+template <class... Params, class... Args>
+cudaError_t launch_dependent_smem(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                                  cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t stream,
+                             const Args&... args) {
+  return launch_dependent_smem(kernel, grid, threads, 0, stream, args...);
+}
+
 // tcgen05 tile kernel.  out: 0 bf16, 1 fp32.  tile_m: 128 (one CTA per tile)
 // or 256 (a CTA pair per tile, launched as clusters of two), or 64 (passed on
 // to the 64-row variants below; tbh unused).  tile_n: 64, 128 or 256, and 224

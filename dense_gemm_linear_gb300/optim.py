@@ -1,0 +1,152 @@
+"""AdamW over many torch CUDA tensors (dgl_adamw)."""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ADAMW_BLOCK, AdamWDesc, AdamWTensor, _check, load_library
+from .head import _not_here, _packed
+from .norm import _code
+
+_F32 = torch.float32
+_STATES = {32: (_F32, _F32), 8: (torch.float8_e4m3fn, torch.float8_e5m2)}
+
+
+def _flat(t, name, device):
+    """Checks a contiguous tensor on the current device; returns its address."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        _not_here(t, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class AdamW:
+    """AdamW (Adam with decoupled weight decay) over a list of tensors, all in one launch a step.
+
+    params: bf16 or fp32 CUDA tensors, contiguous, updated in place.  grads: a
+    gradient for each, bf16 or fp32, of the same shape: the buffers that every
+    step reads unless it is given others (None: each step is given them).
+    weight_decay: a number, or one for each tensor.  master: fp32 copies of bf16
+    params, which are then updated, params becoming their roundings; True makes
+    them from the params.  state_bits: 32, or 8 for E4M3 and E5M2 states with an
+    fp32 scale for each 128 elements, rounded at random with `seed`.
+
+    exp_avg, exp_avg_sq, in 8 bits also exp_avg_scale and exp_avg_sq_scale
+    (lists of 1-D tensors), and steps (int64 [1], the steps taken) are the state: made
+    as zeros when None, kept as attributes of those names, and enough with the
+    params and masters to go on from a checkpoint.  All tensors are on the
+    device that is current, then and at every step.
+    """
+
+    def __init__(self, params, grads=None, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=None,
+                 state_bits=32, exp_avg=None, exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None, steps=None,
+                 seed=0):
+        device = torch.cuda.current_device()
+        params = list(params)
+        n = len(params)
+        if exp_avg is not None and len(exp_avg) and exp_avg[0].dtype != _F32:
+            state_bits = 8
+        if state_bits not in _STATES:
+            raise ValueError("state_bits must be 8 or 32")
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if master is True:
+            master = [p.detach().to(_F32, copy=True).contiguous() if p.dtype == torch.bfloat16 else None for p in params]
+        if len(decay) != n or (master is not None and len(master) != n):
+            raise ValueError("weight_decay and master have one entry for each of params")
+        self.device, self.params, self.master, self.state_bits = device, params, master, state_bits
+        self.lr = lr
+        table = (AdamWTensor * n)()
+        for i, p in enumerate(params):
+            t = table[i]
+            t.param_dtype = _code(p, f"params[{i}]")
+            t.param, t.n, t.weight_decay = _flat(p, f"params[{i}]", device), p.numel(), decay[i]
+            if master is not None and master[i] is not None:
+                if p.dtype != torch.bfloat16:
+                    raise TypeError(f"master[{i}] is given beside a param of fp32")
+                t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
+        sizes = [p.numel() for p in params]
+        blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
+        m_type, v_type = _STATES[state_bits]
+        scaled = state_bits == 8
+        if not scaled and (exp_avg_scale is not None or exp_avg_sq_scale is not None):
+            raise ValueError("states of 32 bits have no scales")
+        self.exp_avg = self._state("exp_avg", exp_avg, sizes, m_type, table)
+        self.exp_avg_sq = self._state("exp_avg_sq", exp_avg_sq, sizes, v_type, table)
+        self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, blocks, _F32, table) if scaled else None
+        self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, blocks, _F32, table) if scaled else None
+        self.steps = torch.zeros(1, dtype=torch.int64, device=device) if steps is None else steps
+        self._ticket = torch.zeros(1, dtype=torch.int32, device=device)
+        self._table = table
+        self._desc = AdamWDesc(_packed(self.steps, "steps", torch.int64, (1,), device), self._ticket.data_ptr(), None,
+                               None, 0.0, betas[0], betas[1], eps, seed & (2**64 - 1), state_bits)
+        self.grads = None
+        if grads is not None:
+            self._take(grads, table)
+            self.grads = list(grads)
+
+    def _state(self, name, given, sizes, dtype, table):
+        """A state's tensors and their addresses in the table.  Those made here lie in one buffer, each in whole
+        blocks of 128 elements."""
+        if given is None:
+            slots = [-(-k // ADAMW_BLOCK) * ADAMW_BLOCK for k in sizes]
+            whole = torch.zeros(sum(slots), dtype=torch.uint8 if dtype != _F32 else _F32, device=self.device).view(dtype)
+            given = [s[:k] for s, k in zip(whole.split(slots), sizes)] if slots else []
+        elif len(given) != len(sizes):
+            raise ValueError(f"{name} has one entry for each of params")
+        for i, (t, k) in enumerate(zip(given, sizes)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != k:
+                raise TypeError(f"{name}[{i}] must be a {dtype} CUDA tensor of {k} elements")
+            setattr(table[i], name, _flat(t, f"{name}[{i}]", self.device))
+        return list(given)
+
+    def _take(self, grads, table):
+        if len(grads) != len(self.params):
+            raise ValueError("grads has one entry for each of params")
+        for t, g, p in zip(table, grads, self.params):
+            t.grad_dtype = _code(g, "a gradient")
+            if g.shape != p.shape:
+                raise ValueError(f"a gradient of shape {tuple(g.shape)} for a param of shape {tuple(p.shape)}")
+            t.grad = _flat(g, "a gradient", self.device)
+
+    def step(self, grads=None, *, lr=None, grad_scale=None, stream=None):
+        """One step, of the gradients given or of those given at the start.
+
+        lr: a number, or an fp32 CUDA tensor of one element (self.lr when None).
+        grad_scale: an fp32 CUDA tensor of one element that every gradient is
+        multiplied by (clipping), or None.  May be captured into a CUDA graph,
+        of which each replay takes the next step.  The host's number for lr is
+        then part of the graph; a tensor is read anew.
+        """
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                self.step(grads, lr=lr, grad_scale=grad_scale)
+            mine = [self.params, self.master, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
+                    self.grads if grads is None else grads, [self.steps, self._ticket, lr, grad_scale]]
+            for t in (t for group in mine if group for t in group):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
+            return
+        if torch.cuda.current_device() != self.device:
+            raise ValueError(f"the optimizer is on cuda:{self.device}, but the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        table, desc = self._table, self._desc
+        if grads is not None:
+            table = type(table)()
+            ctypes.memmove(table, self._table, ctypes.sizeof(table))
+            self._take(grads, table)
+        elif self.grads is None:
+            raise ValueError("step needs the gradients: none were given at the start")
+        if lr is None:
+            lr = self.lr
+        if isinstance(lr, torch.Tensor):
+            desc.lr, desc.lr_at = 0.0, _packed(lr, "lr", _F32, lr.shape if lr.numel() == 1 else (1,), self.device)
+        else:
+            desc.lr, desc.lr_at = lr, None
+        desc.grad_scale = None if grad_scale is None else _packed(
+            grad_scale, "grad_scale", _F32, grad_scale.shape if grad_scale.numel() == 1 else (1,), self.device)
+        st = load_library().dgl_adamw(ctypes.byref(desc), table, len(table),
+                                      torch._C._cuda_getCurrentRawStream(self.device))
+        if st:
+            _check(st, "dgl_adamw")

@@ -449,6 +449,224 @@ dgl_status dgl_linear_distill(const dgl_head_desc* head, const int64_t* indices,
                               const float* teacher_lse, int32_t k, float temperature, void* stream);
 
 /*
+ * Embedding lookup and its gradient: the other end of a model whose head is
+ * dgl_linear_xent's, and with tied weights the same matrix.
+ *   dgl_embedding       Y[t] = scale W[token_t]
+ *   dgl_embedding_grad  dW[v] = scale sum_{t: token_t = v} dY[t]
+ *
+ * Fields.  T, V, d: tokens, rows of W, width (V, d > 0).
+ *   tokens: int64 [T], rows of W or ignore_index.
+ *   W, dW: V rows of d elements of w_dtype, pitch ldw; Y, dY: T rows of
+ *   y_dtype, pitch ldy (types DGL_OUT_BF16 or DGL_OUT_F32; pitches in elements,
+ *   0 = d, else at least d; aligned to their elements).  Rows that are whole units of 16
+ *   bytes, as the rules of dgl_norm_desc say, are accessed in those; others in
+ *   smaller ones.
+ *   scale: finite.
+ *   accumulate: 1 adds to an fp32 dW (the head's gradient of tied weights, an
+ *   earlier micro-batch) and leaves rows without a token as they are; 0 writes
+ *   all of dW.
+ *   ws, ws_bytes: device scratch of dgl_embedding_grad, 256-byte aligned, of at
+ *   least the bytes that dgl_embedding_workspace reports.
+ *
+ * Tokens without a row.  A token equal to ignore_index (whether or not it is
+ * in [0, V)) gives a row of zeros and adds nothing to dW, whatever its row of dY
+ * holds (NaN and infinities included).  Any other token outside [0, V) gives a
+ * row of NaN and adds nothing.
+ *
+ * Sums are fp32 in an order fixed by the tokens, so that equal calls give equal
+ * bits; a bf16 dW is rounded once.
+ */
+typedef struct dgl_embed_desc {
+  int64_t T, V, d;
+  const int64_t* tokens;
+  int64_t ignore_index;
+  const void* W;
+  void* dW;
+  int64_t ldw;
+  void* Y;
+  const void* dY;
+  int64_t ldy;
+  void* ws;
+  int64_t ws_bytes;
+  float scale;
+  int32_t w_dtype, y_dtype;
+  int32_t accumulate;
+} dgl_embed_desc;
+
+/* Scratch bytes of dgl_embedding_grad.  Reads T, V, d and the types.  Pure host logic. */
+dgl_status dgl_embedding_workspace(const dgl_embed_desc* embed, int64_t* bytes);
+
+/*
+ * Embedding lookup.  Enqueues work on `stream` only, allocates nothing, and
+ * may be captured into a CUDA graph.  Errors: DGL_ERR_ARG (null pointers,
+ * negative extents, V or d of 0, a pitch below d, a scale that is not finite,
+ * an unknown type), DGL_ERR_ALIGN, DGL_ERR_SHAPE (T past 2^31 - 1, V past 2^31 -
+ * 513, d past 2^28 - 1), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.
+ */
+dgl_status dgl_embedding(const dgl_embed_desc* embed, void* stream);
+
+/*
+ * The gradient of an embedding.  As dgl_embedding; also DGL_ERR_ARG for
+ * accumulate without an fp32 dW or a workspace below the reported size.  T == 0
+ * writes a zero dW (unless accumulate).
+ */
+dgl_status dgl_embedding_grad(const dgl_embed_desc* embed, void* stream);
+
+/*
+ * Layer norm of the rows of a matrix, which a linear layer or a head reads
+ * next, and its gradient:
+ *   mean_r = mean_j x_rj,   rstd_r = 1 / sqrt(mean_j (x_rj - mean_r)^2 + eps),   h = (x - mean) rstd
+ *   dgl_layer_norm       y = h weight + bias
+ *   dgl_layer_norm_grad  u = dy weight,   dx = rstd (u - mean_j u - h mean_j (u h)),
+ *                        dweight = sum_r dy h,   dbias = sum_r dy
+ *
+ * Fields.  rows, d: the matrices' extents (d > 0).
+ *   x, y, dy, dx: rows of d elements of x_dtype (DGL_OUT_BF16 or DGL_OUT_F32),
+ *   row pitches ldx, ldy, lddy, lddx in elements (0 = d, else at least d),
+ *   aligned to their elements.  Matrices whose bases and pitches are multiples
+ *   of 16 bytes, with d a whole number of such units, are read and written in
+ *   16-byte units; others in smaller ones.  y may be x; otherwise outputs
+ *   overlap no input.
+ *   weight, bias: [d] of w_dtype; NULL: ones, zeros.
+ *   mean, rstd: fp32 [rows]; written by dgl_layer_norm (either may be NULL),
+ *   read by dgl_layer_norm_grad.
+ *   eps: at least 0 (dgl_layer_norm).
+ *   dx, dweight, dbias: the gradients wanted, at least one; NULL: not wanted.
+ *   dweight and dbias are [d] of dw_dtype; accumulate: 1 adds to them (fp32).
+ *   ws, ws_bytes: device scratch, 256-byte aligned, of at least the bytes that
+ *   dgl_layer_norm_workspace reports; for dweight and dbias only.
+ *
+ * Sums and statistics are fp32, the variance a sum of squares around the mean.
+ * A row's results depend on that row alone; the sums over rows have an order
+ * fixed by rows and d, so that equal calls give equal bits.
+ */
+typedef struct dgl_norm_desc {
+  int64_t rows, d;
+  const void* x;
+  int64_t ldx;
+  const void* weight;
+  const void* bias;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  const void* dy;
+  int64_t lddy;
+  void* dx;
+  int64_t lddx;
+  void* dweight;
+  void* dbias;
+  void* ws;
+  int64_t ws_bytes;
+  float eps;
+  int32_t x_dtype, w_dtype, dw_dtype;
+  int32_t accumulate;
+} dgl_norm_desc;
+
+/* Scratch bytes of dgl_layer_norm_grad for the weight's gradients.  Reads rows and d.  Pure host logic. */
+dgl_status dgl_layer_norm_workspace(const dgl_norm_desc* norm, int64_t* bytes);
+
+/*
+ * Layer norm, forward.  Enqueues work on `stream` only, allocates nothing, and
+ * may be captured into a CUDA graph.  rows == 0 does nothing.  Errors:
+ * DGL_ERR_ARG (null pointers, negative extents, d of 0, a pitch below d, an eps
+ * that is negative or not finite, an unknown type), DGL_ERR_ALIGN,
+ * DGL_ERR_SHAPE (rows past 2^31 - 1, d past 2^28 - 1), DGL_ERR_UNSUPPORTED,
+ * DGL_ERR_CUDA.
+ */
+dgl_status dgl_layer_norm(const dgl_norm_desc* norm, void* stream);
+
+/*
+ * Layer norm, backward.  As dgl_layer_norm; also DGL_ERR_ARG for no gradient
+ * asked for, accumulate without fp32 sums of the weight's, or a workspace below
+ * the reported size.  rows == 0 writes zeros to dweight and dbias (unless
+ * accumulate) and nothing else.
+ */
+dgl_status dgl_layer_norm_grad(const dgl_norm_desc* norm, void* stream);
+
+/* Elements of an 8-bit AdamW state that share a scale. */
+#define DGL_ADAMW_BLOCK 128
+
+/*
+ * A tensor of dgl_adamw: n elements, contiguous, in memory.
+ *   param, grad: of param_dtype and grad_dtype (DGL_OUT_BF16 or DGL_OUT_F32).
+ *   master: the fp32 copy of a bf16 param, which is then updated, and param
+ *   becomes its rounding; NULL: param is updated itself.
+ *   exp_avg, exp_avg_sq: m and v; fp32 (state_bits 32), or E4M3 and E5M2 bytes
+ *   with the fp32 scales exp_avg_scale and exp_avg_sq_scale, one for each
+ *   DGL_ADAMW_BLOCK elements (the last block may be short): a value is its code's times
+ *   its block's scale.  Zeros at the start.
+ *   weight_decay: wd, at least 0.
+ * Tensors whose addresses are multiples of 32 bytes (fp32), 16 (bf16) and 8
+ * (8-bit states) are accessed in such units; others may have any address that
+ * is aligned to their elements.
+ */
+typedef struct dgl_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+} dgl_adamw_tensor;
+
+/*
+ * What the tensors of a step share.
+ *   steps: device, the steps taken before this call; the call takes step
+ *   t = *steps + 1 and writes t back when it is done.
+ *   ticket: device word, zero before the first call, which leaves it zero.
+ *   grad_scale: device scalar that every gradient is multiplied by (clipping,
+ *   loss scaling), or NULL.
+ *   lr_at: device scalar that takes the place of lr (a schedule in a captured
+ *   graph), or NULL.
+ *   lr (finite), beta1, beta2 (in [0, 1)), eps (finite, at least 0).
+ *   seed: of the 8-bit states' random rounding.
+ *   state_bits: 8 or 32.
+ */
+typedef struct dgl_adamw_desc {
+  int64_t* steps;
+  uint32_t* ticket;
+  const float* grad_scale;
+  const float* lr_at;
+  double lr, beta1, beta2, eps;
+  uint64_t seed;
+  int32_t state_bits;
+} dgl_adamw_desc;
+
+/*
+ * A step of AdamW (Adam with decoupled weight decay) over many tensors at
+ * once, such as the fp32 dW of dgl_linear_xent and dgl_gemm_bf16_ex:
+ *   g = grad_scale grad,   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32; a bf16 param is rounded to nearest even.
+ *
+ * 8-bit states.  A block's scale is the power of two that takes its largest m
+ * into [2^7, 2^8), its largest v into [2^14, 2^15) (no scale is below 2^-118
+ * and 2^-125).  Each value is rounded to the code below or above it with
+ * probabilities that keep its expectation (to 2^-16 of a step between codes): rounded to the
+ * nearest code, a v that changes by a thousandth a step would never move.  The
+ * random numbers are a function of seed, t and the element's place among the
+ * call's tensors, each padded to whole blocks: equal calls give equal bits.  A v above zero stays above
+ * zero.  A state that is not finite is stored as NaN and does not affect the
+ * others of its block.
+ *
+ * tensors: host array of `count` descriptors, read during the call only; no
+ * two may overlap.  Every tensor is checked before anything is enqueued.
+ * Enqueues one launch for each 336 tensors, allocates nothing, and may be
+ * captured into a CUDA graph (each replay takes the next step).  count == 0
+ * and empty tensors are allowed; the step is counted all the same.  Errors:
+ * DGL_ERR_ARG (null pointers, a negative n, a master beside an fp32 param, a
+ * scalar out of its range, an unknown type), DGL_ERR_ALIGN, DGL_ERR_SHAPE (n
+ * past 2^40), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.
+ */
+dgl_status dgl_adamw(const dgl_adamw_desc* desc, const dgl_adamw_tensor* tensors, int32_t count, void* stream);
+
+/*
  * The plan the library would use for a problem of m x n x K (valid extents)
  * on a device with num_sms SMs (num_sms <= 0: query the current device).
  * Pure host logic when num_sms > 0: needs no GPU.
