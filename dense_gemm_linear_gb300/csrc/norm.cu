@@ -34,6 +34,7 @@ constexpr int kElems = 16;                  // elements a thread holds of a row
 constexpr int kWide = 1024 * kElems;        // the widest row that a block holds
 constexpr int kMid = 512 * kElems;          // and with 128 registers a thread
 constexpr int kSlowThreads = 512;           // a block of the kernels for wider rows
+constexpr int kFewWarps = 8;                // warps whose sums each thread adds up by itself
 constexpr int kFewThreads = 128;            // a block whose rows take a warp or less
 
 struct NormArgs {
@@ -42,6 +43,7 @@ struct NormArgs {
   const void* w;
   const void* b;
   int w_f32;    // type of w and b
+  int w_fits;   // they can be read in the row's units
   void* y;
   int64_t ldy;
   float* mean;
@@ -68,65 +70,138 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-// A lane's units of a row.
+// A lane's elements are in pairs, for the packed fp32 instructions.
+__device__ __forceinline__ void put(float2 (&f)[kElems / 2], int i, float v) {
+  if (i % 2) f[i / 2].y = v;
+  else f[i / 2].x = v;
+}
+__device__ __forceinline__ float get(const float2 (&f)[kElems / 2], int i) { return i % 2 ? f[i / 2].y : f[i / 2].x; }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A lane's units of a row, on their way from memory.  Units of 4 bytes or more
+// pass through shared memory: a lane copies its own units of DEPTH - 1 rows
+// ahead (cp.async) and reads them back itself, so nothing synchronises, no register
+// waits and far more is in flight than registers would hold.  bf16 rows off
+// 4 bytes are held in registers, one row ahead.  Forward, 10240 x 2048 bf16:
+// 23.4 us with one row ahead in registers.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes, int have) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 template <class T, int VEC>
 struct RowUnits {
-  static constexpr int U = kElems / VEC;
-  Unit<T, VEC> u[U];
+  static constexpr int U = kElems / VEC, kBytes = VEC * static_cast<int>(sizeof(T));
+  static constexpr bool kRing = kBytes >= 4;
+  Unit<T, VEC> u[kRing ? 1 : U];
+  uint8_t* ring;  // [DEPTH][U][threads] units
 
-  __device__ __forceinline__ void load(const T* row, int lane, int lanes, int units) {
+  // The units of row `r` of a matrix into a slot; zeros past the row's end and for no row.
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t r, int64_t rows, int slot, int lane, int lanes,
+                                       int units) {
+    const T* row = base + (r < rows ? r * ld : 0);
+    units = r < rows ? units : 0;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int at = lane + i * lanes;
-      if (at < units) u[i] = load_unit_once<T, VEC>(row + static_cast<int64_t>(at) * VEC);
-      else u[i] = Unit<T, VEC>{};
+      if constexpr (kRing) {
+        copy_async(smem_u32(ring + ((slot * U + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kBytes),
+                   row + (at < units ? at * VEC : 0), kBytes, at < units ? kBytes : 0);
+      } else {
+        u[i] = at < units ? load_unit_once<T, VEC>(row + at * VEC) : Unit<T, VEC>{};
+      }
     }
   }
-  __device__ __forceinline__ void get(float (&f)[kElems]) const {
+  __device__ __forceinline__ void get(int slot, float2 (&f)[kElems / 2]) const {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float e[VEC];
-      unpack<T, VEC>(u[i], e);
+      if constexpr (kRing)
+        unpack<T, VEC>(*reinterpret_cast<const Unit<T, VEC>*>(
+                           ring + ((slot * U + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kBytes),
+                       e);
+      else
+        unpack<T, VEC>(u[i], e);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[i * VEC + j] = e[j];
+      for (int j = 0; j < VEC; ++j) put(f, i * VEC + j, e[j]);
     }
   }
 };
 
-// The same columns of a vector (the weight or the bias); `fill` where there are none.
+// Rows that a lane has under way and at hand: 160 KB of an SM's shared memory
+// at the residencies below.
+template <class T, int VEC>
+constexpr int kDepth = !RowUnits<T, VEC>::kRing ? 2 : sizeof(T) == 2 ? 4 : 3;
+template <class T, int VEC>
+constexpr int kRingBytes = RowUnits<T, VEC>::kRing ? kDepth<T, VEC> * kElems * static_cast<int>(sizeof(T)) : 0;  // a thread
+
+// The lanes of a group that is whole warps; `groups` in the block.
+__device__ __forceinline__ void group_sync(int group, int lanes, int groups) {
+  if (groups == 1) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
+}
+
+// The same columns of a vector (the weight or the bias); `fill` where there are
+// none.  In units where its address allows: read element by element, a warp's 32 lanes touch 32
+// sectors for each of 32 loads, and a grid's blocks spent half their time on that.
 template <int VEC>
-__device__ __forceinline__ void lane_columns(const void* v, int f32, float fill, int lane, int lanes, int units,
-                                             float (&f)[kElems]) {
+__device__ __forceinline__ void lane_columns(const void* v, int f32, int units_fit, float fill, int lane, int lanes,
+                                             int units, float2 (&f)[kElems / 2]) {
 #pragma unroll
-  for (int i = 0; i < kElems; ++i) {
-    const int at = lane + i / VEC * lanes;
-    f[i] = v && at < units ? element(v, f32, at * VEC + i % VEC) : fill;
+  for (int i = 0; i < kElems / VEC; ++i) {
+    const int at = lane + i * lanes;
+    float e[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) e[j] = fill;
+    if (v && at < units) {
+      if (units_fit) {
+        if (f32) unpack<float, VEC>(load_unit<float, VEC>(static_cast<const float*>(v) + at * VEC), e);
+        else unpack<bf16, VEC>(load_unit<bf16, VEC>(static_cast<const bf16*>(v) + at * VEC), e);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) e[j] = element(v, f32, at * VEC + j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) put(f, i * VEC + j, e[j]);
   }
 }
 
 template <class T, int VEC>
-__device__ __forceinline__ void store_row(T* row, int lane, int lanes, int units, const float (&f)[kElems]) {
+__device__ __forceinline__ void store_row(T* row, int lane, int lanes, int units, const float2 (&f)[kElems / 2]) {
 #pragma unroll
   for (int i = 0; i < kElems / VEC; ++i) {
     const int at = lane + i * lanes;
     if (at >= units) continue;
     float e[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) e[j] = f[i * VEC + j];
+    for (int j = 0; j < VEC; ++j) e[j] = get(f, i * VEC + j);
     store_unit<T, VEC>(row + static_cast<int64_t>(at) * VEC, e);
   }
 }
 
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
-// apart and loads the next row while it works on this one.
-// THREADS: the most in a block (1024: neither the weight nor the next row fit
-// beside a row in 64 registers; the weight is read again for each row, from L1).
+// apart.
+// THREADS: the most in a block (1024: the weight does not fit beside a row in 64
+// registers and is read again for each row, from L1).
 template <class XT, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr bool kKeep = THREADS <= 512;
+  constexpr int DEPTH = kDepth<XT, VEC>;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
+  __shared__ float2 counts[32];  // elements of a warp, and one over that
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
   const bool whole = lanes > 32;  // the block is one group
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (blockDim.x / lanes);
@@ -134,68 +209,94 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
   const float inv_d = 1.0f / static_cast<float>(a.d);
 
-  // elements that this lane holds, and its warp or group
+  const XT* x = static_cast<const XT*>(a.x);
+  RowUnits<XT, VEC> rows;
+  rows.ring = ring;
+#pragma unroll
+  for (int k = 0; k < DEPTH - 1; ++k) {
+    rows.load(x, a.ldx, row + k * groups, a.rows, k, lane, lanes, units);
+    copy_async_commit();
+  }
+
+  // elements that this lane holds, its warp (or smaller group), and each warp of its block
+  const bool full = units == lanes * (kElems / VEC);
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kElems / VEC; ++i) mine += lane + i * lanes < units ? VEC : 0;
   const float held = lanes_sum(static_cast<float>(mine), lanes < 32 ? lanes : 32);
   const float inv_held = held > 0.0f ? 1.0f / held : 0.0f;
-  float other_held = 0.0f;  // of warp `in_warp`
   if (whole) {
-    if (in_warp == 0) red[0][warp].x = held;
-    __syncthreads();
-    if (in_warp < warps) other_held = red[0][in_warp].x;
+    if (in_warp == 0) counts[warp] = make_float2(held, inv_held);
     __syncthreads();
   }
 
-  float w[kElems], b[kElems];
+  float2 w[kElems / 2], b[kElems / 2];
   if constexpr (kKeep) {
-    lane_columns<VEC>(a.w, a.w_f32, 1.0f, lane, lanes, units, w);
-    lane_columns<VEC>(a.b, a.w_f32, 0.0f, lane, lanes, units, b);
+    lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
+    lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
   }
-  const XT* x = static_cast<const XT*>(a.x);
-  RowUnits<XT, VEC> next;
   // all lanes of a warp go round together: the rows of its groups may end apart
   const int64_t turns = (a.rows + groups - 1) / groups;
-  if (kKeep && row < a.rows) next.load(x + row * a.ldx, lane, lanes, units);
+  int slot = 0;
   for (int64_t turn = 0; turn < turns; ++turn, row += groups) {
     const bool live = row < a.rows;
-    float f[kElems];
-    if constexpr (!kKeep) {
-      if (live) next.load(x + row * a.ldx, lane, lanes, units);
-    }
-    next.get(f);
-    if (kKeep && row + groups < a.rows) next.load(x + (row + groups) * a.ldx, lane, lanes, units);
+    float2 f[kElems / 2];
+    copy_async_wait<DEPTH - 2>();
+    rows.get(slot, f);
+    const int free = slot == 0 ? DEPTH - 1 : slot - 1;
+    slot = slot == DEPTH - 1 ? 0 : slot + 1;
+    rows.load(x, a.ldx, row + (DEPTH - 1) * groups, a.rows, free, lane, lanes, units);
+    copy_async_commit();
     // the warp's (or group's) mean and squares around it, then the block's
-    float s = 0.0f;
+    float2 t = f[0];
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) s += f[i];
-    s = lanes_sum(s, lanes < 32 ? lanes : 32);
-    float mean = s * inv_held, q = 0.0f;
+    for (int i = 1; i < kElems / 2; ++i) t = __fadd2_rn(t, f[i]);
+    const float s = lanes_sum(t.x + t.y, lanes < 32 ? lanes : 32);
+    float mean = s * inv_held, q;
+    {
+      float2 squares = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) {
-      const float c = lane + i / VEC * lanes < units ? f[i] - mean : 0.0f;
-      q = fmaf(c, c, q);
+      for (int i = 0; i < kElems / 2; ++i) {
+        float2 c = __fadd2_rn(f[i], both(-mean));
+        if (!full) {
+          if (lane + 2 * i / VEC * lanes >= units) c.x = 0.0f;
+          if (lane + (2 * i + 1) / VEC * lanes >= units) c.y = 0.0f;
+        }
+        squares = __ffma2_rn(c, c, squares);
+      }
+      q = lanes_sum(squares.x + squares.y, lanes < 32 ? lanes : 32);
     }
-    q = lanes_sum(q, lanes < 32 ? lanes : 32);
     if (whole) {
       float2* r = red[turn & 1];  // two in turn: one barrier a row
       if (in_warp == 0) r[warp] = make_float2(s, q);
       __syncthreads();
-      const float2 o = in_warp < warps ? r[in_warp] : make_float2(0.0f, 0.0f);
-      const float warp_mean = other_held > 0.0f ? o.x / other_held : 0.0f;
-      mean = lanes_sum(o.x, 32) * inv_d;
-      const float c = warp_mean - mean;
-      q = lanes_sum(fmaf(other_held * c, c, o.y), 32);
+      if (warps <= kFewWarps) {
+        // each thread by itself: fewer steps one after another than ten shuffles
+        float sum = 0.0f;
+        for (int k = 0; k < warps; ++k) sum += r[k].x;
+        mean = sum * inv_d;
+        q = 0.0f;
+        for (int k = 0; k < warps; ++k) {
+          const float c = fmaf(r[k].x, counts[k].y, -mean);
+          q += fmaf(counts[k].x * c, c, r[k].y);
+        }
+      } else {
+        const float2 o = in_warp < warps ? r[in_warp] : both(0.0f);
+        const float2 n = in_warp < warps ? counts[in_warp] : both(0.0f);
+        mean = lanes_sum(o.x, 32) * inv_d;
+        const float c = fmaf(o.x, n.y, -mean);
+        q = lanes_sum(fmaf(n.x * c, c, o.y), 32);
+      }
     }
     const float rstd = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
     if (!live) continue;
     if constexpr (!kKeep) {
-      lane_columns<VEC>(a.w, a.w_f32, 1.0f, lane, lanes, units, w);
-      lane_columns<VEC>(a.b, a.w_f32, 0.0f, lane, lanes, units, b);
+      lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
+      lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
     }
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) f[i] = fmaf((f[i] - mean) * rstd, w[i], b[i]);
+    for (int i = 0; i < kElems / 2; ++i)
+      f[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i], both(-mean)), both(rstd)), w[i], b[i]);
     store_row<XT, VEC>(static_cast<XT*>(a.y) + row * a.ldy, lane, lanes, units, f);
     if (lane == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -241,137 +342,197 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
   }
 }
 
-// Backward.  As forward, with x and dy of a row in registers; mean_j u and
-// mean_j (u h) take one barrier a row.  The lane's sums of dw and db are in
-// registers (THREADS 512) or, for rows past 8192, in shared memory, which only
-// the lane itself reads and writes, and leave as a row of `part`.
+// Backward.  As forward, with x and dy of a row; mean_j u and mean_j (u h) take
+// one barrier a row.  The lanes' sums of dw and db leave as a row of `part` for
+// each block.
+// THREADS 512: a block of several groups fills an SM by itself, so that `part`
+// has as many rows as there are SMs; the sums are in registers and the block's
+// groups join theirs in shared memory.  THREADS 1024 (rows past 8192, one group): the
+// sums are in shared memory, which only the lane itself reads and writes, and
+// nothing is loaded ahead.
 template <class XT, int VEC, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr bool kKeep = THREADS <= 512;
-  extern __shared__ float sums[];  // !kKeep: [2][kElems][THREADS]
+  constexpr int DEPTH = kDepth<XT, VEC>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  float* sums = reinterpret_cast<float*>(ring);  // [2 kElems][threads]
   __shared__ float2 red[2][32];
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
-  const bool whole = lanes > 32;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (blockDim.x / lanes);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
+  const bool whole = lanes > 32;  // a group is whole warps
+  const int in_block = blockDim.x / lanes, group = threadIdx.x / lanes;
+  const int64_t groups = static_cast<int64_t>(gridDim.x) * in_block;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * in_block + group;
+  const int warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
+  const int group_warps = lanes / 32, first_warp = group * group_warps;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const bool want_w = a.part != nullptr;
 
-  float dw[kKeep ? kElems : 1], db[kKeep ? kElems : 1];
+  const XT* x = static_cast<const XT*>(a.x);
+  const XT* dy = static_cast<const XT*>(a.dy);
+  RowUnits<XT, VEC> rows_x, rows_g;
+  rows_x.ring = ring;
+  rows_g.ring = ring + kRingBytes<XT, VEC> * blockDim.x;
+  auto load = [&](int64_t r, int slot) {
+    rows_x.load(x, a.ldx, r, a.rows, slot, lane, lanes, units);
+    rows_g.load(dy, a.lddy, r, a.rows, slot, lane, lanes, units);
+  };
+  float next_mean = 0.0f, next_rstd = 0.0f;  // of the next row
+  auto load_statistics = [&](int64_t r) {
+    next_mean = r < a.rows ? a.mean[r] : 0.0f;
+    next_rstd = r < a.rows ? a.rstd[r] : 0.0f;
+  };
+  load_statistics(row);
   if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) dw[i] = db[i] = 0.0f;
+    for (int k = 0; k < DEPTH - 1; ++k) {
+      load(row + k * groups, k);
+      copy_async_commit();
+    }
+  }
+
+  float2 dw[kKeep ? kElems / 2 : 1], db[kKeep ? kElems / 2 : 1];
+  float2 wv[kElems / 2];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kElems / 2; ++i) dw[i] = db[i] = both(0.0f);
+    lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, wv);
   } else {
 #pragma unroll
     for (int i = 0; i < 2 * kElems; ++i) sums[i * THREADS + threadIdx.x] = 0.0f;
   }
-  float wv[kElems];
-  if constexpr (kKeep) lane_columns<VEC>(a.w, a.w_f32, 1.0f, lane, lanes, units, wv);
-  RowUnits<XT, VEC> next_x, next_g;
   const int64_t turns = (a.rows + groups - 1) / groups;
-  const XT* x = static_cast<const XT*>(a.x);
-  const XT* dy = static_cast<const XT*>(a.dy);
-  if (kKeep && row < a.rows) {
-    next_x.load(x + row * a.ldx, lane, lanes, units);
-    next_g.load(dy + row * a.lddy, lane, lanes, units);
-  }
+  int slot = 0;
   for (int64_t turn = 0; turn < turns; ++turn, row += groups) {
+    // (a row that does not exist, and columns past the row's, are zeros of dy and add nothing)
     const bool live = row < a.rows;
-    float h[kElems], g[kElems];
-    if constexpr (!kKeep) {
-      if (live) {
-        next_x.load(x + row * a.ldx, lane, lanes, units);
-        next_g.load(dy + row * a.lddy, lane, lanes, units);
-      }
-    }
-    next_x.get(h);
-    next_g.get(g);
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
-    if (kKeep && row + groups < a.rows) {
-      next_x.load(x + (row + groups) * a.ldx, lane, lanes, units);
-      next_g.load(dy + (row + groups) * a.lddy, lane, lanes, units);
-    }
-    if constexpr (!kKeep) lane_columns<VEC>(a.w, a.w_f32, 1.0f, lane, lanes, units, wv);
-    float s = 0.0f, q = 0.0f;
+    float2 h[kElems / 2], g[kElems / 2];
+    const float mean = next_mean, rstd = next_rstd;
+    load_statistics(row + groups);
+    if constexpr (kKeep) {
+      copy_async_wait<DEPTH - 2>();
+      rows_x.get(slot, h);
+      rows_g.get(slot, g);
+      const int free = slot == 0 ? DEPTH - 1 : slot - 1;
+      slot = slot == DEPTH - 1 ? 0 : slot + 1;
+      load(row + (DEPTH - 1) * groups, free);
+      copy_async_commit();
+    } else {
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) {
-      h[i] = (h[i] - mean) * rstd;
-      // (a row that has ended, and columns past the row's, add nothing: g is zero there or unused)
-      if (live && lane + i / VEC * lanes < units) {
-        const float u = g[i] * wv[i];
-        s += u;
-        q = fmaf(u, h[i], q);
-        if (want_w) {
-          if constexpr (kKeep) {
-            dw[i] = fmaf(g[i], h[i], dw[i]);
-            db[i] += g[i];
-          } else {
-            float* m = sums + i * THREADS + threadIdx.x;
-            *m = fmaf(g[i], h[i], *m);
-            m[kElems * THREADS] += g[i];
+      for (int i = 0; i < kElems / VEC; ++i) {
+        const int at = lane + i * lanes;
+        float e[2][VEC] = {};
+        if (live && at < units) {
+          unpack<XT, VEC>(load_unit_once<XT, VEC>(x + row * a.ldx + at * VEC), e[0]);
+          unpack<XT, VEC>(load_unit_once<XT, VEC>(dy + row * a.lddy + at * VEC), e[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          put(h, i * VEC + j, e[0][j]);
+          put(g, i * VEC + j, e[1][j]);
+        }
+      }
+      lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, wv);
+    }
+    float2 sum = both(0.0f), dot = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < kElems / 2; ++i) {
+      h[i] = __fmul2_rn(__fadd2_rn(h[i], both(-mean)), both(rstd));
+      if (want_w) {
+        if constexpr (kKeep) {
+          dw[i] = __ffma2_rn(g[i], h[i], dw[i]);
+          db[i] = __fadd2_rn(db[i], g[i]);
+        } else {
+#pragma unroll
+          for (int j = 2 * i; j < 2 * i + 2; ++j) {
+            float* m = sums + j * THREADS + threadIdx.x;
+            *m = fmaf(get(g, j), get(h, j), *m);
+            m[kElems * THREADS] += get(g, j);
           }
         }
       }
+      g[i] = __fmul2_rn(g[i], wv[i]);  // u
+      sum = __fadd2_rn(sum, g[i]);
+      dot = __ffma2_rn(g[i], h[i], dot);
     }
     if (!a.dx) continue;
-    s = lanes_sum(s, lanes < 32 ? lanes : 32);
-    q = lanes_sum(q, lanes < 32 ? lanes : 32);
+    float s = lanes_sum(sum.x + sum.y, lanes < 32 ? lanes : 32);
+    float q = lanes_sum(dot.x + dot.y, lanes < 32 ? lanes : 32);
     if (whole) {
       float2* r = red[turn & 1];
       if (in_warp == 0) r[warp] = make_float2(s, q);
-      __syncthreads();
-      const float2 o = in_warp < warps ? r[in_warp] : make_float2(0.0f, 0.0f);
-      s = lanes_sum(o.x, 32);
-      q = lanes_sum(o.y, 32);
+      group_sync(group, lanes, in_block);
+      if (group_warps <= kFewWarps) {
+        float2 o = both(0.0f);
+        for (int k = 0; k < group_warps; ++k) o = __fadd2_rn(o, r[first_warp + k]);
+        s = o.x;
+        q = o.y;
+      } else {
+        const float2 o = in_warp < group_warps ? r[first_warp + in_warp] : both(0.0f);
+        s = lanes_sum(o.x, 32);
+        q = lanes_sum(o.y, 32);
+      }
     }
     if (!live) continue;
-    s *= inv_d;
-    q *= inv_d;
+    s *= -inv_d * rstd;
+    q *= -inv_d * rstd;
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) g[i] = rstd * (fmaf(g[i], wv[i], -s) - h[i] * q);
+    for (int i = 0; i < kElems / 2; ++i) g[i] = __ffma2_rn(g[i], both(rstd), __ffma2_rn(h[i], both(q), both(s)));
     store_row<XT, VEC>(static_cast<XT*>(a.dx) + row * a.lddx, lane, lanes, units, g);
   }
   if (!want_w) return;
   float* part = a.part + blockIdx.x * 2 * static_cast<int64_t>(a.d);
   if constexpr (kKeep) {
-    if (!whole) {
-      // the groups of the warp, then of the block's warps, in a fixed order
-      __shared__ float across[kFewThreads / 32][2 * kElems][32];
+    const int stride = whole ? lanes : 32;  // the block's groups, or warps of smaller ones
+    if (static_cast<int>(blockDim.x) > stride || lanes < 32) {
+      // the groups of a warp, then of the block, in a fixed order
+      for (int o = lanes; o < 32; o *= 2) {
+#pragma unroll
+        for (int i = 0; i < kElems / 2; ++i) {
+          dw[i].x += __shfl_xor_sync(0xffffffffu, dw[i].x, o);
+          dw[i].y += __shfl_xor_sync(0xffffffffu, dw[i].y, o);
+          db[i].x += __shfl_xor_sync(0xffffffffu, db[i].x, o);
+          db[i].y += __shfl_xor_sync(0xffffffffu, db[i].y, o);
+        }
+      }
+      __syncthreads();  // (copies have all been waited for by their own threads)
 #pragma unroll
       for (int i = 0; i < kElems; ++i) {
-        for (int o = lanes; o < 32; o *= 2) {
-          dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-          db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
-        }
-        across[warp][i][in_warp] = dw[i];
-        across[warp][kElems + i][in_warp] = db[i];
+        sums[i * blockDim.x + threadIdx.x] = get(dw, i);
+        sums[(kElems + i) * blockDim.x + threadIdx.x] = get(db, i);
       }
       __syncthreads();
       if (threadIdx.x >= lanes) return;
 #pragma unroll
       for (int i = 0; i < kElems; ++i) {
-        for (int k = 1; k < warps; ++k) {
-          dw[i] += across[k][i][in_warp];
-          db[i] += across[k][kElems + i][in_warp];
+        float sw = 0.0f, sb = 0.0f;
+        for (int k = threadIdx.x; k < static_cast<int>(blockDim.x); k += stride) {
+          sw += sums[i * blockDim.x + k];
+          sb += sums[(kElems + i) * blockDim.x + k];
         }
+        put(dw, i, sw);
+        put(db, i, sb);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kElems; ++i) {
-    const int at = lane + i / VEC * lanes;
+  for (int i = 0; i < kElems / VEC; ++i) {
+    const int at = lane + i * lanes;
     if (at >= units) continue;
-    float* to = part + at * VEC + i % VEC;
-    if constexpr (kKeep) {
-      to[0] = dw[i];
-      to[a.d] = db[i];
-    } else {
-      to[0] = sums[i * THREADS + threadIdx.x];
-      to[a.d] = sums[(kElems + i) * THREADS + threadIdx.x];
+    float e[2][VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if constexpr (kKeep) {
+        e[0][j] = get(dw, i * VEC + j);
+        e[1][j] = get(db, i * VEC + j);
+      } else {
+        e[0][j] = sums[(i * VEC + j) * THREADS + threadIdx.x];
+        e[1][j] = sums[(kElems + i * VEC + j) * THREADS + threadIdx.x];
+      }
     }
+    store_unit<float, VEC>(part + at * VEC, e[0]);
+    store_unit<float, VEC>(part + a.d + at * VEC, e[1]);
   }
 }
 
@@ -460,15 +621,6 @@ int lanes_for(int64_t d) {
 
 int threads_for(int lanes) { return lanes > 32 ? lanes : kFewThreads; }
 
-// Blocks of a persistent grid: `threads` a block, about `per_sm` threads on an SM.
-int64_t grid_for(int64_t rows, int lanes, int threads, int per_sm, int num_sms) {
-  const int64_t in_block = threads / lanes;
-  const int64_t most = static_cast<int64_t>(num_sms) * std::max(1, per_sm / threads);
-  return std::min((rows + in_block - 1) / in_block, most);
-}
-
-constexpr int kForwardThreads = 768, kBackwardThreads = 512;
-
 struct BackwardPlan {
   int lanes, threads;
   int64_t grid, groups;  // blocks, rows of `part`
@@ -483,8 +635,10 @@ BackwardPlan backward_plan(int64_t rows, int64_t d, int num_sms) {
     return p;
   }
   p.lanes = lanes_for(d);
-  p.threads = threads_for(p.lanes);
-  p.grid = grid_for(rows, p.lanes, p.threads, kBackwardThreads, num_sms);
+  // one block an SM: its registers, at 512 threads, and its shared memory are full
+  const int64_t in_block = std::max<int64_t>(1, d > kMid ? 1 : std::min<int64_t>(512 / p.lanes, rows));
+  p.threads = static_cast<int>(p.lanes < 32 ? std::max<int64_t>(32, (in_block * p.lanes + 31) / 32 * 32) : in_block * p.lanes);
+  p.grid = std::min<int64_t>((rows * p.lanes + p.threads - 1) / p.threads, num_sms);
   p.groups = p.grid;
   return p;
 }
@@ -546,9 +700,43 @@ dgl_status prepare(dgl_norm_desc& n, bool backward, NormArgs& a, int64_t& vec) {
       if (!n.mean || !n.rstd) return DGL_ERR_ARG;
     }
   }
-  a = NormArgs{n.x,    n.ldx, n.weight, n.bias, n.w_dtype == DGL_OUT_F32, n.y, n.ldy,  n.mean, n.rstd, n.dy, n.lddy, n.dx,
+  a = NormArgs{n.x,    n.ldx, n.weight, n.bias, n.w_dtype == DGL_OUT_F32,
+               aligned(n.weight, 16) && aligned(n.bias, 16), n.y, n.ldy,  n.mean, n.rstd, n.dy, n.lddy, n.dx,
                n.lddx, nullptr, n.rows, static_cast<int>(n.d), 0, n.eps};
   return DGL_OK;
+}
+
+// A persistent grid of as many blocks as are resident together (one more an SM
+// would run alone afterwards and double the time).
+template <class X, int VEC, int THREADS>
+cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> resident[33] = {};  // blocks of so many warps on an SM
+  const auto kernel = norm_forward_kernel<X, VEC, THREADS>;
+  const int threads = threads_for(a.lanes), smem = kRingBytes<X, VEC> * threads;
+  cudaError_t e = set_smem_attr_once(kernel, kRingBytes<X, VEC> * THREADS, done);
+  if (e != cudaSuccess) return e;
+  int fit = resident[threads / 32].load(std::memory_order_relaxed);
+  if (fit == 0) {
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem)) != cudaSuccess) return e;
+    resident[threads / 32].store(fit = std::max(fit, 1), std::memory_order_relaxed);
+  }
+  const int64_t in_block = threads / a.lanes;
+  const int64_t grid = std::min<int64_t>((a.rows + in_block - 1) / in_block, static_cast<int64_t>(fit) * num_sms);
+  return launch_dependent_smem(kernel, static_cast<unsigned>(grid), threads, smem, stream, a);
+}
+
+template <class X, int VEC, int THREADS>
+cudaError_t launch_backward(const NormArgs& a, const BackwardPlan& plan, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int kSums = 2 * kElems * static_cast<int>(sizeof(float));  // a thread
+  constexpr int kEach = THREADS <= 512 ? std::max(2 * kRingBytes<X, VEC>, kSums) : kSums;
+  const auto kernel = norm_backward_kernel<X, VEC, THREADS>;
+  const cudaError_t e = set_smem_attr_once(kernel, kEach * THREADS, done);
+  if (e != cudaSuccess) return e;
+  // (the 1024-thread kernel's sums have a pitch of 1024)
+  const int smem = kEach * (THREADS <= 512 ? plan.threads : THREADS);
+  return launch_dependent_smem(kernel, static_cast<unsigned>(plan.grid), plan.threads, smem, stream, a);
 }
 
 dgl_status run_forward(dgl_norm_desc n, cudaStream_t stream) {
@@ -570,14 +758,11 @@ dgl_status run_forward(dgl_norm_desc n, cudaStream_t stream) {
     return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
   }
   a.lanes = lanes_for(n.d);
-  const int threads = threads_for(a.lanes);
-  const unsigned grid =
-      static_cast<unsigned>(grid_for(n.rows, a.lanes, threads, n.d > kMid ? 1024 : kForwardThreads, ds->num_sms));
   const cudaError_t e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
     using X = decltype(x);
-    return n.d > kMid
-               ? launch_dependent(norm_forward_kernel<X, decltype(v)::value, 1024>, grid, threads, stream, a)
-               : launch_dependent(norm_forward_kernel<X, decltype(v)::value, 512>, grid, threads, stream, a);
+    constexpr int kVec = decltype(v)::value;
+    return n.d > kMid ? launch_forward<X, kVec, 1024>(a, ds->num_sms, stream)
+                      : launch_forward<X, kVec, 512>(a, ds->num_sms, stream);
   });
   return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
 }
@@ -630,13 +815,8 @@ dgl_status run_backward(dgl_norm_desc n, cudaStream_t stream) {
       e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
         using X = decltype(x);
         constexpr int kVec = decltype(v)::value;
-        if (n.d <= kMid)
-          return launch_dependent(norm_backward_kernel<X, kVec, 512>, grid, plan.threads, stream, a);
-        static std::atomic<uint64_t> done{0};
-        constexpr int kBytes = 2 * kElems * 1024 * static_cast<int>(sizeof(float));
-        const cudaError_t err = set_smem_attr_once(norm_backward_kernel<X, kVec, 1024>, kBytes, done);
-        if (err != cudaSuccess) return err;
-        return launch_dependent_smem(norm_backward_kernel<X, kVec, 1024>, grid, plan.threads, kBytes, stream, a);
+        return n.d <= kMid ? launch_backward<X, kVec, 512>(a, plan, stream)
+                           : launch_backward<X, kVec, 1024>(a, plan, stream);
       });
     }
     if (e != cudaSuccess) return DGL_ERR_CUDA;

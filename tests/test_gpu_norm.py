@@ -59,7 +59,8 @@ def check(name, got, want, tol):
 
 SHAPES = [(1, 1), (1, 8), (3, 7), (5, 16), (130, 17), (257, 24), (64, 100), (33, 129), (300, 512), (77, 513),
           (40, 1023), (9, 1024), (700, 1025), (6, 2048), (2100, 768), (19, 4096), (3, 4100), (11, 8191), (5, 8192),
-          (4, 8194), (7, 12288), (3, 16383), (2, 16384), (3, 16392), (2, 20001)]
+          (4, 8194), (7, 12288), (3, 16383), (2, 16384), (3, 16392), (2, 20001), (1300, 4096), (400, 8200),
+          (333, 12288), (700, 16400), (5000, 40), (90000, 8)]
 TYPES = [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16), (BF16, None)]
 
 
