@@ -53,11 +53,20 @@ __device__ __forceinline__ Unit<T, N> load_unit_once(const T* p) {
 
 template <class T, int N>
 __device__ __forceinline__ void unpack(const Unit<T, N>& u, float (&f)[N]) {
-  const T* e = reinterpret_cast<const T*>(&u);
+  if constexpr (sizeof(T) == 2 && N >= 2) {
+    const uint32_t* two = reinterpret_cast<const uint32_t*>(&u);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (sizeof(T) == 2) f[i] = __bfloat162float(e[i]);
-    else f[i] = e[i];
+    for (int i = 0; i < N; i += 2) {  // a bf16 is the upper half of an fp32
+      f[i] = __uint_as_float(two[i / 2] << 16);
+      f[i + 1] = __uint_as_float(two[i / 2] & 0xffff0000u);
+    }
+  } else {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 2) f[i] = __bfloat162float(e[i]);
+      else f[i] = e[i];
+    }
   }
 }
 
@@ -65,11 +74,17 @@ __device__ __forceinline__ void unpack(const Unit<T, N>& u, float (&f)[N]) {
 template <class T, int N>
 __device__ __forceinline__ void store_unit(T* p, const float (&f)[N]) {
   Unit<T, N> u;
-  T* e = reinterpret_cast<T*>(&u);
+  if constexpr (sizeof(T) == 2 && N >= 2) {
+    __nv_bfloat162* two = reinterpret_cast<__nv_bfloat162*>(&u);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (sizeof(T) == 2) e[i] = __float2bfloat16_rn(f[i]);
-    else e[i] = f[i];
+    for (int i = 0; i < N; i += 2) two[i / 2] = __floats2bfloat162_rn(f[i], f[i + 1]);
+  } else {
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(T) == 2) e[i] = __float2bfloat16_rn(f[i]);
+      else e[i] = f[i];
+    }
   }
   *reinterpret_cast<Unit<T, N>*>(p) = u;
 }

@@ -34,7 +34,6 @@ constexpr int kElems = 16;                  // elements a thread holds of a row
 constexpr int kWide = 1024 * kElems;        // the widest row that a block holds
 constexpr int kMid = 512 * kElems;          // and with 128 registers a thread
 constexpr int kSlowThreads = 512;           // a block of the kernels for wider rows
-constexpr int kFewWarps = 8;                // warps whose sums each thread adds up by itself
 constexpr int kFewThreads = 128;            // a block whose rows take a warp or less
 
 struct NormArgs {
@@ -63,11 +62,46 @@ __device__ __forceinline__ float element(const void* v, int f32, int64_t i) {
   return f32 ? static_cast<const float*>(v)[i] : to_float(static_cast<const bf16*>(v)[i]);
 }
 
+// Sums over the lanes of a row: a power of two below 32, or a warp.
+template <bool WARPS>
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (WARPS || o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Sums over a row's warps, in every lane: lane k holds warp k's value (zero where
+// there is none), and lanes 8 apart the same where there are at most eight.
+constexpr int kFewWarps = 8;
+__device__ __forceinline__ float warps_sum(float v, bool few) {
+  if (!few) {
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+  }
+#pragma unroll
+  for (int o = kFewWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Two sums over a whole warp in six shuffles' steps instead of ten: the halves of
+// the warp exchange what each does not go on with.  Lanes 0 to 15 return the
+// first, 16 to 31 the second.
+__device__ __forceinline__ float warp_sums(float a, float b) {
+  const bool low = (threadIdx.x & 16) == 0;
+  float v = low ? a : b;
+  v += __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// 1 / sqrt(v): the hardware's, off by two units in the last place, and a step of
+// Newton's method.  (0 gives infinity, infinity 0.)
+__device__ __forceinline__ float reciprocal_root(float v) {
+  const float r = rsqrtf(v);
+  const float better = fmaf(r * fmaf(-v * r, r, 1.0f), 0.5f, r);
+  return r > 0.0f && r < INFINITY ? better : r;
 }
 
 // A lane's elements are in pairs, for the packed fp32 instructions.
@@ -77,20 +111,57 @@ __device__ __forceinline__ void put(float2 (&f)[kElems / 2], int i, float v) {
 }
 __device__ __forceinline__ float get(const float2 (&f)[kElems / 2], int i) { return i % 2 ? f[i / 2].y : f[i / 2].x; }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// Two fp32 operations in one instruction (a sixth fewer instructions in all).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
+// (x - mean) rstd.  Of bf16 values as one multiplication and addition, whose
+// rounding is a bf16's 2^-16th unless the mean is hundreds of times the spread,
+// where bf16 holds little of the row; of fp32 values as two steps, of which the
+// first is nearly exact.
+template <class T>
+__device__ __forceinline__ float2 scaled(float2 x, float mean, float rstd) {
+  if constexpr (sizeof(T) == 2) return fma2(x, both(rstd), both(-mean * rstd));
+  else return mul2(add2(x, both(-mean)), both(rstd));
+}
 
 // A lane's units of a row, on their way from memory.  Units of 4 bytes or more
 // pass through shared memory: a lane copies its own units of DEPTH - 1 rows
 // ahead (cp.async) and reads them back itself, so nothing synchronises, no register
 // waits and far more is in flight than registers would hold.  bf16 rows off
 // 4 bytes are held in registers, one row ahead.  Forward, 10240 x 2048 bf16:
-// 23.4 us with one row ahead in registers.
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes, int have) {
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
-  else if (bytes == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+// 23.4 us with one row ahead in registers, 16.4 so, 18.7 with one bulk copy a row, whose
+// arrival and release cost more instructions than the copies of 16 bytes.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(have) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void store_shared_zero(uint32_t to) {
+  if constexpr (BYTES == 16)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+  else if constexpr (BYTES == 8)
+    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
+  else
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
+}
+template <class U>
+__device__ __forceinline__ U load_shared(uint32_t from) {
+  U u;
+  if constexpr (sizeof(U) == 16)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(from)
+                 : "memory");
+  else if constexpr (sizeof(U) == 8)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(from) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(from) : "memory");
+  return u;
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -102,37 +173,62 @@ template <class T, int VEC>
 struct RowUnits {
   static constexpr int U = kElems / VEC, kBytes = VEC * static_cast<int>(sizeof(T));
   static constexpr bool kRing = kBytes >= 4;
-  Unit<T, VEC> u[kRing ? 1 : U];
-  uint8_t* ring;  // [DEPTH][U][threads] units
+  Unit<T, VEC> held[kRing ? 1 : U];
+  const T* next;   // the lane's first unit of the row to be loaded
+  int64_t step;    // elements from one of the group's rows to its next
+  int apart;       // elements between the lane's units
+  int count;       // units that the lane has
+  uint32_t pitch;  // of a slot's units in shared memory
+  uint32_t first, in, out, end;  // of the lane's slots: the first, the one to fill, the one to read, the last's end
 
-  // The units of row `r` of a matrix into a slot; zeros past the row's end and for no row.
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t r, int64_t rows, int slot, int lane, int lanes,
-                                       int units) {
-    const T* row = base + (r < rows ? r * ld : 0);
-    units = r < rows ? units : 0;
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int at = lane + i * lanes;
-      if constexpr (kRing) {
-        copy_async(smem_u32(ring + ((slot * U + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kBytes),
-                   row + (at < units ? at * VEC : 0), kBytes, at < units ? kBytes : 0);
-      } else {
-        u[i] = at < units ? load_unit_once<T, VEC>(row + at * VEC) : Unit<T, VEC>{};
-      }
+  // ring: [depth][U][threads] units.  Units past a row's end are zeros, which no load writes.
+  __device__ __forceinline__ void begin(const T* x, int64_t ld, int64_t row, int64_t stride, int lane, int lanes,
+                                        int units, uint8_t* ring, int depth) {
+    next = x + row * ld + lane * VEC;
+    step = stride * ld;
+    apart = lanes * VEC;
+    count = lane < units ? (units - lane + lanes - 1) / lanes : 0;
+    pitch = blockDim.x * kBytes;
+    first = in = out = smem_u32(ring) + threadIdx.x * kBytes;
+    end = first + depth * U * pitch;
+    if constexpr (kRing) {
+      if (count < U)
+        for (int k = 0; k < depth; ++k) zero(first + k * U * pitch, count);
     }
   }
-  __device__ __forceinline__ void get(int slot, float2 (&f)[kElems / 2]) const {
+  __device__ __forceinline__ void zero(uint32_t slot, int from) {
+    for (int i = from; i < U; ++i) store_shared_zero<kBytes>(slot + i * pitch);
+  }
+  // The next row; zeros where it does not exist.
+  __device__ __forceinline__ void load(bool exists) {
+    if constexpr (kRing) {
+      if (exists) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (i < count) copy_async<kBytes>(in + i * pitch, next + i * apart);
+      } else {
+        zero(in, 0);
+      }
+      in += U * pitch;
+      if (in == end) in = first;
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) held[i] = exists && i < count ? load_unit_once<T, VEC>(next + i * apart) : Unit<T, VEC>{};
+    }
+    next += step;
+  }
+  __device__ __forceinline__ void get(float2 (&f)[kElems / 2]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       float e[VEC];
-      if constexpr (kRing)
-        unpack<T, VEC>(*reinterpret_cast<const Unit<T, VEC>*>(
-                           ring + ((slot * U + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kBytes),
-                       e);
-      else
-        unpack<T, VEC>(u[i], e);
+      if constexpr (kRing) unpack<T, VEC>(load_shared<Unit<T, VEC>>(out + i * pitch), e);
+      else unpack<T, VEC>(held[i], e);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) put(f, i * VEC + j, e[j]);
+    }
+    if constexpr (kRing) {
+      out += U * pitch;
+      if (out == end) out = first;
     }
   }
 };
@@ -176,24 +272,25 @@ __device__ __forceinline__ void lane_columns(const void* v, int f32, int units_f
   }
 }
 
+// row: the lane's first unit.
 template <class T, int VEC>
-__device__ __forceinline__ void store_row(T* row, int lane, int lanes, int units, const float2 (&f)[kElems / 2]) {
+__device__ __forceinline__ void store_row(T* row, int apart, int count, const float2 (&f)[kElems / 2]) {
 #pragma unroll
   for (int i = 0; i < kElems / VEC; ++i) {
-    const int at = lane + i * lanes;
-    if (at >= units) continue;
+    if (i >= count) continue;
     float e[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) e[j] = get(f, i * VEC + j);
-    store_unit<T, VEC>(row + static_cast<int64_t>(at) * VEC, e);
+    store_unit<T, VEC>(row + i * apart, e);
   }
 }
 
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
 // apart.
 // THREADS: the most in a block (1024: the weight does not fit beside a row in 64
-// registers and is read again for each row, from L1).
-template <class XT, int VEC, int THREADS>
+// registers and is read again for each row, from L1).  WARPS: a row has several
+// warps, which are the block.
+template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -201,32 +298,34 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   constexpr int DEPTH = kDepth<XT, VEC>;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
-  __shared__ float2 counts[32];  // elements of a warp, and one over that
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
-  const bool whole = lanes > 32;  // the block is one group
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (blockDim.x / lanes);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
+  // (rows fit 31 bits)
+  const int in_block = blockDim.x / lanes, groups = gridDim.x * in_block, nrows = static_cast<int>(a.rows);
+  int row = blockIdx.x * in_block + threadIdx.x / lanes;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
   const float inv_d = 1.0f / static_cast<float>(a.d);
 
-  const XT* x = static_cast<const XT*>(a.x);
+  const int count = lane < units ? (units - lane + lanes - 1) / lanes : 0, apart = lanes * VEC;
   RowUnits<XT, VEC> rows;
-  rows.ring = ring;
+  rows.begin(static_cast<const XT*>(a.x), a.ldx, row, groups, lane, lanes, units, ring, DEPTH);
+  int ahead = nrows - row;  // rows from the next to be loaded on, over all groups
 #pragma unroll
-  for (int k = 0; k < DEPTH - 1; ++k) {
-    rows.load(x, a.ldx, row + k * groups, a.rows, k, lane, lanes, units);
+  for (int k = 0; k < DEPTH - 1; ++k, ahead -= groups) {
+    rows.load(ahead > 0);
     copy_async_commit();
   }
 
-  // elements that this lane holds, its warp (or smaller group), and each warp of its block
+  // elements that the lane's warp (or smaller group) holds, and each warp of its block
   const bool full = units == lanes * (kElems / VEC);
-  int mine = 0;
-#pragma unroll
-  for (int i = 0; i < kElems / VEC; ++i) mine += lane + i * lanes < units ? VEC : 0;
-  const float held = lanes_sum(static_cast<float>(mine), lanes < 32 ? lanes : 32);
+  const float held = lanes_sum<WARPS>(static_cast<float>(count * VEC), lanes);
   const float inv_held = held > 0.0f ? 1.0f / held : 0.0f;
-  if (whole) {
-    if (in_warp == 0) counts[warp] = make_float2(held, inv_held);
+  const bool few = warps <= kFewWarps;
+  const int other = few ? in_warp % kFewWarps : in_warp;  // the warp whose sums this lane takes up
+  float2 counted = both(0.0f);  // of that warp: elements, and one over that
+  if constexpr (WARPS) {
+    if (in_warp == 0) red[0][warp] = make_float2(held, inv_held);
+    __syncthreads();
+    if (other < warps) counted = red[0][other];
     __syncthreads();
   }
 
@@ -235,69 +334,58 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
     lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
     lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
   }
+  XT* y = static_cast<XT*>(a.y) + row * a.ldy + lane * VEC;
+  const int64_t y_step = groups * a.ldy;
   // all lanes of a warp go round together: the rows of its groups may end apart
-  const int64_t turns = (a.rows + groups - 1) / groups;
-  int slot = 0;
-  for (int64_t turn = 0; turn < turns; ++turn, row += groups) {
-    const bool live = row < a.rows;
+  const int turns = (nrows + groups - 1) / groups;
+  for (int turn = 0; turn < turns; ++turn, row += groups, y += y_step) {
     float2 f[kElems / 2];
     copy_async_wait<DEPTH - 2>();
-    rows.get(slot, f);
-    const int free = slot == 0 ? DEPTH - 1 : slot - 1;
-    slot = slot == DEPTH - 1 ? 0 : slot + 1;
-    rows.load(x, a.ldx, row + (DEPTH - 1) * groups, a.rows, free, lane, lanes, units);
+    rows.get(f);
+    rows.load(ahead > 0);
+    ahead -= groups;
     copy_async_commit();
     // the warp's (or group's) mean and squares around it, then the block's
     float2 t = f[0];
 #pragma unroll
-    for (int i = 1; i < kElems / 2; ++i) t = __fadd2_rn(t, f[i]);
-    const float s = lanes_sum(t.x + t.y, lanes < 32 ? lanes : 32);
-    float mean = s * inv_held, q;
-    {
-      float2 squares = both(0.0f);
+    for (int i = 1; i < kElems / 2; ++i) t = add2(t, f[i]);
+    const float s = lanes_sum<WARPS>(t.x + t.y, lanes);
+    float mean = s * inv_held;
+    float2 squares = both(0.0f);
+    if (full) {
 #pragma unroll
       for (int i = 0; i < kElems / 2; ++i) {
-        float2 c = __fadd2_rn(f[i], both(-mean));
-        if (!full) {
-          if (lane + 2 * i / VEC * lanes >= units) c.x = 0.0f;
-          if (lane + (2 * i + 1) / VEC * lanes >= units) c.y = 0.0f;
-        }
-        squares = __ffma2_rn(c, c, squares);
+        const float2 c = add2(f[i], both(-mean));
+        squares = fma2(c, c, squares);
       }
-      q = lanes_sum(squares.x + squares.y, lanes < 32 ? lanes : 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kElems / 2; ++i) {
+        float2 c = add2(f[i], both(-mean));
+        if (2 * i / VEC >= count) c.x = 0.0f;
+        if ((2 * i + 1) / VEC >= count) c.y = 0.0f;
+        squares = fma2(c, c, squares);
+      }
     }
-    if (whole) {
+    float q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
+    if constexpr (WARPS) {
       float2* r = red[turn & 1];  // two in turn: one barrier a row
       if (in_warp == 0) r[warp] = make_float2(s, q);
       __syncthreads();
-      if (warps <= kFewWarps) {
-        // each thread by itself: fewer steps one after another than ten shuffles
-        float sum = 0.0f;
-        for (int k = 0; k < warps; ++k) sum += r[k].x;
-        mean = sum * inv_d;
-        q = 0.0f;
-        for (int k = 0; k < warps; ++k) {
-          const float c = fmaf(r[k].x, counts[k].y, -mean);
-          q += fmaf(counts[k].x * c, c, r[k].y);
-        }
-      } else {
-        const float2 o = in_warp < warps ? r[in_warp] : both(0.0f);
-        const float2 n = in_warp < warps ? counts[in_warp] : both(0.0f);
-        mean = lanes_sum(o.x, 32) * inv_d;
-        const float c = fmaf(o.x, n.y, -mean);
-        q = lanes_sum(fmaf(n.x * c, c, o.y), 32);
-      }
+      const float2 o = other < warps ? r[other] : both(0.0f);
+      mean = warps_sum(o.x, few) * inv_d;
+      const float c = fmaf(o.x, counted.y, -mean);
+      q = warps_sum(fmaf(counted.x * c, c, o.y), few);
     }
-    const float rstd = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
-    if (!live) continue;
+    const float rstd = reciprocal_root(fmaf(q, inv_d, a.eps));
+    if (row >= nrows) continue;
     if constexpr (!kKeep) {
       lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
       lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
     }
 #pragma unroll
-    for (int i = 0; i < kElems / 2; ++i)
-      f[i] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[i], both(-mean)), both(rstd)), w[i], b[i]);
-    store_row<XT, VEC>(static_cast<XT*>(a.y) + row * a.ldy, lane, lanes, units, f);
+    for (int i = 0; i < kElems / 2; ++i) f[i] = fma2(scaled<XT>(f[i], mean, rstd), w[i], b[i]);
+    store_row<XT, VEC>(y, apart, count, f);
     if (lane == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -306,7 +394,7 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
 }
 
 __device__ __forceinline__ float block_sum(float v, float* red) {
-  v = lanes_sum(v, 32);
+  v = lanes_sum<true>(v, 32);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = v;
   __syncthreads();
@@ -332,7 +420,7 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
       const float c = to_float(x[i]) - mean;
       q = fmaf(c, c, q);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(q, red) / static_cast<float>(a.d) + a.eps);
+    const float rstd = reciprocal_root(block_sum(q, red) / static_cast<float>(a.d) + a.eps);
     for (int i = threadIdx.x; i < a.d; i += kSlowThreads)
       y[i] = from_float<XT>(fmaf((to_float(x[i]) - mean) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f, a.b ? element(a.b, a.w_f32, i) : 0.0f));
     if (threadIdx.x == 0) {
@@ -350,7 +438,7 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
 // groups join theirs in shared memory.  THREADS 1024 (rows past 8192, one group): the
 // sums are in shared memory, which only the lane itself reads and writes, and
 // nothing is loaded ahead.
-template <class XT, int VEC, int THREADS>
+template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
@@ -360,34 +448,29 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
   float* sums = reinterpret_cast<float*>(ring);  // [2 kElems][threads]
   __shared__ float2 red[2][32];
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
-  const bool whole = lanes > 32;  // a group is whole warps
   const int in_block = blockDim.x / lanes, group = threadIdx.x / lanes;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * in_block;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * in_block + group;
+  const int groups = gridDim.x * in_block, nrows = static_cast<int>(a.rows);  // (rows fit 31 bits)
+  int row = blockIdx.x * in_block + group;
   const int warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
-  const int group_warps = lanes / 32, first_warp = group * group_warps;
+  const int group_warps = lanes / 32;
+  const bool few = group_warps <= kFewWarps;
+  const int other = few ? in_warp % kFewWarps : in_warp;  // the group's warp whose sums this lane takes up
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const bool want_w = a.part != nullptr;
 
-  const XT* x = static_cast<const XT*>(a.x);
-  const XT* dy = static_cast<const XT*>(a.dy);
+  const int count = lane < units ? (units - lane + lanes - 1) / lanes : 0, apart = lanes * VEC;
   RowUnits<XT, VEC> rows_x, rows_g;
-  rows_x.ring = ring;
-  rows_g.ring = ring + kRingBytes<XT, VEC> * blockDim.x;
-  auto load = [&](int64_t r, int slot) {
-    rows_x.load(x, a.ldx, r, a.rows, slot, lane, lanes, units);
-    rows_g.load(dy, a.lddy, r, a.rows, slot, lane, lanes, units);
-  };
+  rows_x.begin(static_cast<const XT*>(a.x), a.ldx, row, groups, lane, lanes, units, ring, kKeep ? DEPTH : 0);
+  rows_g.begin(static_cast<const XT*>(a.dy), a.lddy, row, groups, lane, lanes, units,
+               ring + kRingBytes<XT, VEC> * blockDim.x, kKeep ? DEPTH : 0);
+  int ahead = nrows - row;  // rows from the next to be loaded on, over all groups
   float next_mean = 0.0f, next_rstd = 0.0f;  // of the next row
-  auto load_statistics = [&](int64_t r) {
-    next_mean = r < a.rows ? a.mean[r] : 0.0f;
-    next_rstd = r < a.rows ? a.rstd[r] : 0.0f;
-  };
-  load_statistics(row);
+  if (row < nrows) next_mean = a.mean[row], next_rstd = a.rstd[row];
   if constexpr (kKeep) {
 #pragma unroll
-    for (int k = 0; k < DEPTH - 1; ++k) {
-      load(row + k * groups, k);
+    for (int k = 0; k < DEPTH - 1; ++k, ahead -= groups) {
+      rows_x.load(ahead > 0);
+      rows_g.load(ahead > 0);
       copy_async_commit();
     }
   }
@@ -402,30 +485,30 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 2 * kElems; ++i) sums[i * THREADS + threadIdx.x] = 0.0f;
   }
-  const int64_t turns = (a.rows + groups - 1) / groups;
-  int slot = 0;
-  for (int64_t turn = 0; turn < turns; ++turn, row += groups) {
+  XT* dx = static_cast<XT*>(a.dx) + row * a.lddx + lane * VEC;
+  const int64_t dx_step = groups * a.lddx;
+  const int turns = (nrows + groups - 1) / groups;
+  for (int turn = 0; turn < turns; ++turn, row += groups, dx += dx_step) {
     // (a row that does not exist, and columns past the row's, are zeros of dy and add nothing)
-    const bool live = row < a.rows;
     float2 h[kElems / 2], g[kElems / 2];
     const float mean = next_mean, rstd = next_rstd;
-    load_statistics(row + groups);
+    if (row < nrows - groups) next_mean = a.mean[row + groups], next_rstd = a.rstd[row + groups];
     if constexpr (kKeep) {
       copy_async_wait<DEPTH - 2>();
-      rows_x.get(slot, h);
-      rows_g.get(slot, g);
-      const int free = slot == 0 ? DEPTH - 1 : slot - 1;
-      slot = slot == DEPTH - 1 ? 0 : slot + 1;
-      load(row + (DEPTH - 1) * groups, free);
+      rows_x.get(h);
+      rows_g.get(g);
+      rows_x.load(ahead > 0);
+      rows_g.load(ahead > 0);
+      ahead -= groups;
       copy_async_commit();
     } else {
+      const int have = row < nrows ? count : 0;
 #pragma unroll
       for (int i = 0; i < kElems / VEC; ++i) {
-        const int at = lane + i * lanes;
         float e[2][VEC] = {};
-        if (live && at < units) {
-          unpack<XT, VEC>(load_unit_once<XT, VEC>(x + row * a.ldx + at * VEC), e[0]);
-          unpack<XT, VEC>(load_unit_once<XT, VEC>(dy + row * a.lddy + at * VEC), e[1]);
+        if (i < have) {
+          unpack<XT, VEC>(load_unit_once<XT, VEC>(rows_x.next + i * apart), e[0]);
+          unpack<XT, VEC>(load_unit_once<XT, VEC>(rows_g.next + i * apart), e[1]);
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
@@ -433,58 +516,61 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
           put(g, i * VEC + j, e[1][j]);
         }
       }
+      rows_x.next += rows_x.step;
+      rows_g.next += rows_g.step;
       lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, wv);
     }
+#pragma unroll
+    for (int i = 0; i < kElems / 2; ++i) h[i] = scaled<XT>(h[i], mean, rstd);
+    if (want_w) {
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kElems / 2; ++i) {
+          dw[i] = fma2(g[i], h[i], dw[i]);
+          db[i] = add2(db[i], g[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kElems; ++i) {
+          float* m = sums + i * THREADS + threadIdx.x;
+          *m = fmaf(get(g, i), get(h, i), *m);
+          m[kElems * THREADS] += get(g, i);
+        }
+      }
+    }
+    if (!a.dx) continue;
     float2 sum = both(0.0f), dot = both(0.0f);
 #pragma unroll
     for (int i = 0; i < kElems / 2; ++i) {
-      h[i] = __fmul2_rn(__fadd2_rn(h[i], both(-mean)), both(rstd));
-      if (want_w) {
-        if constexpr (kKeep) {
-          dw[i] = __ffma2_rn(g[i], h[i], dw[i]);
-          db[i] = __fadd2_rn(db[i], g[i]);
-        } else {
-#pragma unroll
-          for (int j = 2 * i; j < 2 * i + 2; ++j) {
-            float* m = sums + j * THREADS + threadIdx.x;
-            *m = fmaf(get(g, j), get(h, j), *m);
-            m[kElems * THREADS] += get(g, j);
-          }
-        }
-      }
-      g[i] = __fmul2_rn(g[i], wv[i]);  // u
-      sum = __fadd2_rn(sum, g[i]);
-      dot = __ffma2_rn(g[i], h[i], dot);
+      g[i] = mul2(g[i], wv[i]);  // u
+      sum = add2(sum, g[i]);
+      dot = fma2(g[i], h[i], dot);
     }
-    if (!a.dx) continue;
-    float s = lanes_sum(sum.x + sum.y, lanes < 32 ? lanes : 32);
-    float q = lanes_sum(dot.x + dot.y, lanes < 32 ? lanes : 32);
-    if (whole) {
+    float s, q;
+    if constexpr (WARPS) {
       float2* r = red[turn & 1];
-      if (in_warp == 0) r[warp] = make_float2(s, q);
+      const float v = warp_sums(sum.x + sum.y, dot.x + dot.y);
+      if (in_warp == 0) r[warp].x = v;
+      if (in_warp == 16) r[warp].y = v;
       group_sync(group, lanes, in_block);
-      if (group_warps <= kFewWarps) {
-        float2 o = both(0.0f);
-        for (int k = 0; k < group_warps; ++k) o = __fadd2_rn(o, r[first_warp + k]);
-        s = o.x;
-        q = o.y;
-      } else {
-        const float2 o = in_warp < group_warps ? r[first_warp + in_warp] : both(0.0f);
-        s = lanes_sum(o.x, 32);
-        q = lanes_sum(o.y, 32);
-      }
+      const float2 o = other < group_warps ? r[group * group_warps + other] : both(0.0f);
+      s = warps_sum(o.x, few);
+      q = warps_sum(o.y, few);
+    } else {
+      s = lanes_sum<false>(sum.x + sum.y, lanes);
+      q = lanes_sum<false>(dot.x + dot.y, lanes);
     }
-    if (!live) continue;
+    if (row >= nrows) continue;
     s *= -inv_d * rstd;
     q *= -inv_d * rstd;
 #pragma unroll
-    for (int i = 0; i < kElems / 2; ++i) g[i] = __ffma2_rn(g[i], both(rstd), __ffma2_rn(h[i], both(q), both(s)));
-    store_row<XT, VEC>(static_cast<XT*>(a.dx) + row * a.lddx, lane, lanes, units, g);
+    for (int i = 0; i < kElems / 2; ++i) g[i] = fma2(g[i], both(rstd), fma2(h[i], both(q), both(s)));
+    store_row<XT, VEC>(dx, apart, count, g);
   }
   if (!want_w) return;
   float* part = a.part + blockIdx.x * 2 * static_cast<int64_t>(a.d);
   if constexpr (kKeep) {
-    const int stride = whole ? lanes : 32;  // the block's groups, or warps of smaller ones
+    const int stride = WARPS ? lanes : 32;  // the block's groups, or warps of smaller ones
     if (static_cast<int>(blockDim.x) > stride || lanes < 32) {
       // the groups of a warp, then of the block, in a fixed order
       for (int o = lanes; o < 32; o *= 2) {
@@ -652,7 +738,8 @@ int64_t part_bytes(int64_t rows, int64_t d) {
 dgl_status check_extents(const dgl_norm_desc* n) {
   if (!n) return DGL_ERR_ARG;
   if (n->rows < 0 || n->d <= 0) return DGL_ERR_ARG;
-  if (n->rows > INT32_MAX || n->d > INT32_MAX / 8) return DGL_ERR_SHAPE;
+  // (row numbers go past the last row by less than a grid's groups)
+  if (n->rows > INT32_MAX - (1 << 20) || n->d > INT32_MAX / 8) return DGL_ERR_SHAPE;
   for (int32_t t : {n->x_dtype, n->w_dtype, n->dw_dtype})
     if (t != DGL_OUT_BF16 && t != DGL_OUT_F32) return DGL_ERR_ARG;
   return DGL_OK;
@@ -708,11 +795,11 @@ dgl_status prepare(dgl_norm_desc& n, bool backward, NormArgs& a, int64_t& vec) {
 
 // A persistent grid of as many blocks as are resident together (one more an SM
 // would run alone afterwards and double the time).
-template <class X, int VEC, int THREADS>
+template <class X, int VEC, int THREADS, bool WARPS>
 cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> resident[33] = {};  // blocks of so many warps on an SM
-  const auto kernel = norm_forward_kernel<X, VEC, THREADS>;
+  const auto kernel = norm_forward_kernel<X, VEC, THREADS, WARPS>;
   const int threads = threads_for(a.lanes), smem = kRingBytes<X, VEC> * threads;
   cudaError_t e = set_smem_attr_once(kernel, kRingBytes<X, VEC> * THREADS, done);
   if (e != cudaSuccess) return e;
@@ -726,12 +813,12 @@ cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) 
   return launch_dependent_smem(kernel, static_cast<unsigned>(grid), threads, smem, stream, a);
 }
 
-template <class X, int VEC, int THREADS>
+template <class X, int VEC, int THREADS, bool WARPS>
 cudaError_t launch_backward(const NormArgs& a, const BackwardPlan& plan, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr int kSums = 2 * kElems * static_cast<int>(sizeof(float));  // a thread
   constexpr int kEach = THREADS <= 512 ? std::max(2 * kRingBytes<X, VEC>, kSums) : kSums;
-  const auto kernel = norm_backward_kernel<X, VEC, THREADS>;
+  const auto kernel = norm_backward_kernel<X, VEC, THREADS, WARPS>;
   const cudaError_t e = set_smem_attr_once(kernel, kEach * THREADS, done);
   if (e != cudaSuccess) return e;
   // (the 1024-thread kernel's sums have a pitch of 1024)
@@ -761,8 +848,9 @@ dgl_status run_forward(dgl_norm_desc n, cudaStream_t stream) {
   const cudaError_t e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
     using X = decltype(x);
     constexpr int kVec = decltype(v)::value;
-    return n.d > kMid ? launch_forward<X, kVec, 1024>(a, ds->num_sms, stream)
-                      : launch_forward<X, kVec, 512>(a, ds->num_sms, stream);
+    return n.d > kMid      ? launch_forward<X, kVec, 1024, true>(a, ds->num_sms, stream)
+           : a.lanes > 32 ? launch_forward<X, kVec, 512, true>(a, ds->num_sms, stream)
+                          : launch_forward<X, kVec, 512, false>(a, ds->num_sms, stream);
   });
   return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
 }
@@ -800,7 +888,7 @@ dgl_status run_backward(dgl_norm_desc n, cudaStream_t stream) {
     groups = plan.groups;
     a.lanes = plan.lanes;
     a.part = part;
-    cudaError_t e = cudaSuccess;
+      cudaError_t e = cudaSuccess;
     if (n.d > kWide) {
       if (n.dx)
         e = with_types(n.x_dtype, 1, [&](auto x, auto) {
@@ -815,8 +903,9 @@ dgl_status run_backward(dgl_norm_desc n, cudaStream_t stream) {
       e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
         using X = decltype(x);
         constexpr int kVec = decltype(v)::value;
-        return n.d <= kMid ? launch_backward<X, kVec, 512>(a, plan, stream)
-                           : launch_backward<X, kVec, 1024>(a, plan, stream);
+            return n.d > kMid      ? launch_backward<X, kVec, 1024, true>(a, plan, stream)
+               : a.lanes > 32 ? launch_backward<X, kVec, 512, true>(a, plan, stream)
+                              : launch_backward<X, kVec, 512, false>(a, plan, stream);
       });
     }
     if (e != cudaSuccess) return DGL_ERR_CUDA;

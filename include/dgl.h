@@ -571,7 +571,7 @@ dgl_status dgl_layer_norm_workspace(const dgl_norm_desc* norm, int64_t* bytes);
  * may be captured into a CUDA graph.  rows == 0 does nothing.  Errors:
  * DGL_ERR_ARG (null pointers, negative extents, d of 0, a pitch below d, an eps
  * that is negative or not finite, an unknown type), DGL_ERR_ALIGN,
- * DGL_ERR_SHAPE (rows past 2^31 - 1, d past 2^28 - 1), DGL_ERR_UNSUPPORTED,
+ * DGL_ERR_SHAPE (rows past 2^31 - 2^20 - 1, d past 2^28 - 1), DGL_ERR_UNSUPPORTED,
  * DGL_ERR_CUDA.
  */
 dgl_status dgl_layer_norm(const dgl_norm_desc* norm, void* stream);
