@@ -7,12 +7,12 @@
 // of the positions, and written once: no atomics, equal calls give equal bits.
 //
 //   sort   one cluster of up to 8 CTAs sorts up to 131072 tokens in its shared
-//          memory (radix, stable).  The other CTAs of the launch write the rows
-//          of a new dW that no token reaches: HBM is busy while the sort, which
-//          latency bounds, runs.
-//   sum    the sorted positions in chunks of equal length; a token's run inside
-//          a chunk goes to dW at once, what crosses a chunk's border to fp32
-//          partial sums.  Reads dY once.
+//          memory (radix, stable).  The other CTAs of the launch keep HBM busy
+//          while the sort, which latency bounds, runs: with zeros for rows of a new dW
+//          that no token reaches, or dY's rows on their way to L2.
+//   sum    the sorted positions in chunks of equal length, a block each; a token's run
+//          inside a chunk goes to dW at once, what crosses a chunk's border to
+//          fp32 partial sums.  Reads dY once.
 //   join   the partial sums of runs over several chunks, in order.
 // More tokens are taken 131072 at a time, each adding to the sums before.
 #include <cuda_bf16.h>
@@ -45,50 +45,64 @@ struct LookupArgs {
   int64_t ldw;
   void* y;
   int64_t ldy;
-  int64_t rows;
   int64_t vocab;
-  int units;  // of a row
+  int rows;
+  int units;   // of a row
+  int lanes;   // threads of a worker
+  int slices;  // workers of a row
   float scale;
 };
 
-constexpr int kLookupThreads = 256, kLookupEach = 4;
+constexpr int kLookupThreads = 256;
 
-// Four units a thread, all loads first.  A token that is ignored gives zeros, one
-// outside the vocabulary NaN.
+// Units that a lane takes of a row: 64 bytes of W, in loads of what alignment allows.
+template <class WT, int VEC>
+constexpr int kLookupUnits = VEC == 1 ? 16 : 64 / (VEC * static_cast<int>(sizeof(WT)));
+
+// A worker (a warp, or a part of one for narrow rows) takes a slice of a row, all
+// loads first.  A token that is ignored gives zeros, one outside the vocabulary NaN.
 template <class WT, class YT, int VEC>
 __global__ void __launch_bounds__(kLookupThreads) embed_lookup_kernel(const __grid_constant__ LookupArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kLookupThreads * kLookupEach);
-  const int64_t row0 = first / a.units;
-  const uint32_t rest = static_cast<uint32_t>(first - row0 * a.units);
-  Unit<WT, VEC> u[kLookupEach];
-  YT* to[kLookupEach];
-  float fill[kLookupEach];
-  bool found[kLookupEach];
-#pragma unroll
-  for (int i = 0; i < kLookupEach; ++i) {
-    const uint32_t at = rest + i * kLookupThreads + threadIdx.x;
-    const int64_t row = row0 + at / static_cast<uint32_t>(a.units);
-    const int64_t col = static_cast<int64_t>(at % static_cast<uint32_t>(a.units)) * VEC;
-    to[i] = nullptr;
-    found[i] = false;
-    if (row >= a.rows) continue;
-    to[i] = static_cast<YT*>(a.y) + row * a.ldy + col;
-    const int64_t token = a.tokens[row];
-    found[i] = token != a.ignore_index && token >= 0 && token < a.vocab;
-    fill[i] = token == a.ignore_index ? 0.0f : NAN;
-    if (found[i]) u[i] = load_unit_once<WT, VEC>(static_cast<const WT*>(a.w) + token * a.ldw + col);
-  }
-#pragma unroll
-  for (int i = 0; i < kLookupEach; ++i) {
-    if (!to[i]) continue;
+  constexpr int U = kLookupUnits<WT, VEC>;
+  const int lane = threadIdx.x % a.lanes;
+  const int64_t worker = static_cast<int64_t>(blockIdx.x) * (kLookupThreads / a.lanes) + threadIdx.x / a.lanes;
+  const int64_t row = worker / a.slices;
+  const int first = static_cast<int>(worker % a.slices) * a.lanes * U + lane;
+  if (row >= a.rows || first >= a.units) return;
+  const int64_t token = a.tokens[row];
+  YT* y = static_cast<YT*>(a.y) + row * a.ldy;
+  if (token == a.ignore_index || token < 0 || token >= a.vocab) {
     float f[VEC];
-    if (found[i]) unpack<WT, VEC>(u[i], f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = found[i] ? f[j] * a.scale : fill[i];
-    store_unit<YT, VEC>(to[i], f);
+    for (int j = 0; j < VEC; ++j) f[j] = token == a.ignore_index ? 0.0f : NAN;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (first + i * a.lanes < a.units) store_unit<YT, VEC>(y + (first + i * a.lanes) * VEC, f);
+    return;
   }
+  const WT* w = static_cast<const WT*>(a.w) + token * a.ldw;
+  Unit<WT, VEC> u[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i)
+    if (first + i * a.lanes < a.units) u[i] = load_unit_once<WT, VEC>(w + (first + i * a.lanes) * VEC);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (first + i * a.lanes >= a.units) continue;
+    float f[VEC];
+    unpack<WT, VEC>(u[i], f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] *= a.scale;
+    store_unit<YT, VEC>(y + (first + i * a.lanes) * VEC, f);
+  }
+}
+
+// Threads of a worker: a warp, or fewer for rows of fewer units.
+int lanes_for(int64_t units) {
+  int lanes = 1;
+  while (lanes < 32 && lanes < units) lanes *= 2;
+  return lanes;
 }
 
 // ---- gradient: sort
@@ -109,10 +123,16 @@ struct SortArgs {
   int passes, digit_bits;
   int* keys;       // [n] tokens in order; `vocab`, behind them, for those without a row
   int* positions;  // [n]
-  // rows without a token are set to zero (null: not)
+  // what the other CTAs of the launch do meanwhile: a new dW's rows without a
+  // token, or (null) dY's rows on their way to L2
   void* dw;
   int64_t row_bytes, pitch_bytes;
-  int store_bytes;  // 16, 4 or 2: of a store
+  int element;        // bytes
+  uint32_t* present;  // bits of the rows of dW that a token reaches, where rows are left to the next kernel
+  int share, quota;   // rows of a CTA's range, and of those that it sets to zero now; whole words
+  const void* dy;
+  int64_t dy_bytes;   // of a row that its CTA asks for (0: nothing to prefetch)
+  int64_t dy_pitch;
 };
 
 struct SortShared {
@@ -241,19 +261,28 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, uint2* items, int
   }
 }
 
-template <class U>
-__device__ __forceinline__ void zero_row(uint8_t* row, int64_t bytes, int lane) {
-  U* to = reinterpret_cast<U*>(row);
-  for (int64_t i = lane; i < bytes / static_cast<int64_t>(sizeof(U)); i += 32) to[i] = U{};
+// Zeros in a row of any alignment: 16-byte stores, and single elements at its ends.
+__device__ __forceinline__ void zero_row(uint8_t* row, int64_t bytes, int element, int lane) {
+  const int64_t head = min(bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(row) & 15));
+  const int64_t body = (bytes - head) / 16 * 16;
+  for (int64_t i = lane * 16; i < body; i += 512) *reinterpret_cast<uint4*>(row + head + i) = make_uint4(0, 0, 0, 0);
+  const int64_t edge = bytes - body;  // bytes that are left, at both ends
+  for (int64_t i = lane * element; i < edge; i += 32 * element) {
+    uint8_t* to = row + (i < head ? i : i + body);
+    if (element == 4) *reinterpret_cast<uint32_t*>(to) = 0;
+    else *reinterpret_cast<uint16_t*>(to) = 0;
+  }
 }
 
 // Rows of dW that no token reaches: each CTA has a range of rows and looks
-// through all tokens for those in it.
-__device__ void zero_rows(const SortArgs& a, uint32_t* map, int cta, int ctas) {
-  const int64_t share = (a.vocab + ctas - 1) / ctas;
-  const int64_t end = min(a.vocab, share * (cta + 1));
+// through all tokens for those in it.  It writes zeros to the first of them, about as many as
+// the sort takes time for, and leaves the others to the next kernel, whose sums
+// wait on latency and not on HBM: 185 of 206 MB of zeros by these CTAs alone took
+// 45 us, and the sums 18 us after them.
+__device__ void zero_rows(const SortArgs& a, uint32_t* map, int cta) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t v0 = share * cta; v0 < end; v0 += kMapWords * 32) {
+  const int64_t begin = static_cast<int64_t>(a.share) * cta, end = min(a.vocab, begin + a.share);
+  for (int64_t v0 = begin; v0 < end; v0 += kMapWords * 32) {
     const int64_t rows = min(end - v0, static_cast<int64_t>(kMapWords * 32));
     for (int i = threadIdx.x; i < kMapWords; i += kSortThreads) map[i] = 0;
     __syncthreads();
@@ -264,29 +293,45 @@ __device__ void zero_rows(const SortArgs& a, uint32_t* map, int cta, int ctas) {
         atomicOr(&map[(t - v0) / 32], 1u << ((t - v0) % 32));
     }
     __syncthreads();
-    for (int r = warp; r < rows; r += kSortWarps) {
-      if (map[r / 32] >> (r % 32) & 1) continue;
-      uint8_t* row = static_cast<uint8_t*>(a.dw) + (v0 + r) * a.pitch_bytes;
-      if (a.store_bytes == 16) zero_row<uint4>(row, a.row_bytes, lane);
-      else if (a.store_bytes == 4) zero_row<uint32_t>(row, a.row_bytes, lane);
-      else zero_row<uint16_t>(row, a.row_bytes, lane);
+    if (a.quota < a.share) {
+      uint32_t* present = a.present + v0 / 32;  // (shares are whole words)
+      for (int i = threadIdx.x; i < (rows + 31) / 32; i += kSortThreads) present[i] = map[i];
     }
+    const int64_t now = min(rows, begin + a.quota - v0);
+    for (int r = warp; r < now; r += kSortWarps)
+      if (!(map[r / 32] >> (r % 32) & 1))
+        zero_row(static_cast<uint8_t*>(a.dw) + (v0 + r) * a.pitch_bytes, a.row_bytes, a.element, lane);
     __syncthreads();
   }
 }
 
-// The first `ctas` CTAs (one cluster) sort, the others write zeros.
+// dY's rows into L2, where the sums then find them: nothing else reads HBM while the
+// sort runs.
+__device__ void prefetch_rows(const SortArgs& a, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  for (int t = cta * kSortWarps + (threadIdx.x >> 5); t < a.n; t += ctas * kSortWarps) {
+    const int64_t token = a.tokens[t];
+    if (token == a.ignore_index || token < 0 || token >= a.vocab) continue;
+    const uint8_t* row = static_cast<const uint8_t*>(a.dy) + t * a.dy_pitch;
+    for (int64_t i = lane * 128; i < a.dy_bytes; i += 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + i));
+  }
+}
+
+// The first `ctas` CTAs (one cluster) sort; what the others do, see above.
 template <int EACH>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ SortArgs a, int ctas) {
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ __align__(16) uint8_t raw[];
   SortShared& sh = *reinterpret_cast<SortShared*>(raw);
-  if (static_cast<int>(blockIdx.x) < ctas)
+  const int cta = static_cast<int>(blockIdx.x) - ctas;
+  if (cta < 0)
     sort_tokens<EACH>(a, sh, reinterpret_cast<uint2*>(raw + sizeof(SortShared)), ctas, static_cast<int>(blockIdx.x));
+  else if (a.dw)
+    zero_rows(a, reinterpret_cast<uint32_t*>(raw), cta);
   else
-    zero_rows(a, reinterpret_cast<uint32_t*>(raw), static_cast<int>(blockIdx.x) - ctas,
-              static_cast<int>(gridDim.x) - ctas);
+    prefetch_rows(a, cta, static_cast<int>(gridDim.x) - ctas);
 }
 
 // ---- gradient: sums
@@ -300,128 +345,250 @@ struct SumArgs {
   int64_t lddw;
   float* part;  // [chunks][2][d]: a chunk's first run, when it began before; its last, when it goes on
   int n, vocab;
-  int chunk;    // positions of a chunk
+  int each;     // positions that a worker takes
+  int chunk;    // and a block, all its workers together
   int chunks;
-  int d, units, lanes;  // units of a row, threads on a row's (part of the) units
+  int d, units;  // units of a row
+  int lanes;    // threads of a worker
+  int slices;   // blocks that share a chunk, each with some columns
   float scale;
   int add;
+  // a new dW's rows without a token that are left to be set to zero
+  int zero_blocks;
+  int64_t words;       // of `present`, in all ranges together
+  int words_each;      // that a block takes
+  int range_words, quota_words;  // of a range, and of those that are done
+  const uint32_t* present;
 };
 
 constexpr int kSumThreads = 256;
-constexpr int kSumAhead = 8;  // rows of dY in flight
+constexpr int kMostChunk = 2048;
+// A lane's units of a row, 16 bytes of dY in all (their loads are smaller where
+// alignment says so), and the rows that a worker has in flight.
+template <class GT, int VEC>
+constexpr int kSumUnits = 16 / (VEC * static_cast<int>(sizeof(GT)));
+template <class GT, int VEC>
+constexpr int kSumAhead = kSumUnits<GT, VEC> == 1 ? 8 : 4;
 
+// sum: of a unit.  To an fp32 dW by a reduction in L2, which waits for no load;
+// each element gets one, so that its order is fixed (subnormal sums count as zero there).
 template <class DT, int VEC>
-__device__ __forceinline__ void finish_row(const SumArgs& a, int key, int64_t col, float (&sum)[VEC]) {
+__device__ __forceinline__ void finish_unit(const SumArgs& a, int key, int64_t col, const float* sum) {
   DT* to = static_cast<DT*>(a.dw) + key * a.lddw + col;
-  if (a.add) {
-    float old[VEC];
-    unpack<DT, VEC>(load_unit<DT, VEC>(to), old);
+  float f[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] = fmaf(sum[j], a.scale, old[j]);
-  } else {
+  for (int j = 0; j < VEC; ++j) f[j] = sum[j] * a.scale;
+  if constexpr (sizeof(DT) == 4) {
+    if (a.add) {
+      if constexpr (VEC >= 4) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) sum[j] *= a.scale;
+        for (int j = 0; j < VEC; j += 4)
+          asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + j), "f"(f[j]), "f"(f[j + 1]),
+                       "f"(f[j + 2]), "f"(f[j + 3])
+                       : "memory");
+      } else if constexpr (VEC == 2) {
+        asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(f[0]), "f"(f[1]) : "memory");
+      } else {
+        asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to), "f"(f[0]) : "memory");
+      }
+      return;
+    }
   }
-  store_unit<DT, VEC>(to, sum);
+  store_unit<DT, VEC>(to, f);
 }
 
-// A group of lanes takes a chunk of positions and lanes x VEC columns.
+__device__ void zero_rest(const SumArgs& a, int64_t row_bytes, int64_t pitch_bytes, int element, int block) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int left = a.range_words - a.quota_words;
+  for (int64_t k = static_cast<int64_t>(block) * a.words_each; k < min(a.words, static_cast<int64_t>(block + 1) * a.words_each); ++k) {
+    const int64_t word = k / left * a.range_words + a.quota_words + k % left;
+    if (word * 32 >= a.vocab) continue;
+    const uint32_t present = a.present[word];
+    for (int r = warp; r < 32 && word * 32 + r < a.vocab; r += kSumThreads / 32)
+      if (!(present >> r & 1))
+        zero_row(static_cast<uint8_t*>(a.dw) + (word * 32 + r) * pitch_bytes, row_bytes, element, lane);
+  }
+}
+
+// A block takes a chunk of the sorted positions and the columns of one worker.
+// Its workers (a warp, or a part of one for narrow rows) take neighbouring
+// pieces of the chunk and all the same columns.  A run of one token inside a piece goes
+// to dW; a piece's first run that began before it, and its last that goes on,
+// are left in shared memory, where the block adds up those of its workers in
+// order.  What began before the chunk, or goes on after it, goes to `part`.
+// Blocks that write the remaining zeros lie between them.
 template <class GT, class DT, int VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(kSumThreads, 3) embed_sum_kernel(const __grid_constant__ SumArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int in_block = kSumThreads / a.lanes;
-  const int chunk = blockIdx.x * in_block + threadIdx.x / a.lanes;
-  const int unit = blockIdx.y * a.lanes + threadIdx.x % a.lanes;
-  if (threadIdx.x / a.lanes >= in_block || chunk >= a.chunks || unit >= a.units) return;
-  const int64_t col = static_cast<int64_t>(unit) * VEC;
-  const GT* dy = static_cast<const GT*>(a.dy) + col;
-  const int j0 = chunk * a.chunk, j1 = min(a.n, j0 + a.chunk);
-  float* part = a.part + static_cast<int64_t>(chunk) * 2 * a.d + col;
-  int run = a.keys[j0];  // the token being summed
-  if (run >= a.vocab) return;
-  bool began = j0 > 0 && a.keys[j0 - 1] == run;
-  const int after = j1 < a.n ? a.keys[j1] : INT_MAX;
-  float sum[VEC];
+  constexpr int U = kSumUnits<GT, VEC>, E = U * VEC, AHEAD = kSumAhead<GT, VEC>;
+  __shared__ __align__(16) float open[2][kSumThreads * E];  // first runs and last runs of the pieces
+  __shared__ int keys_at[kMostChunk + 2];                   // the chunk's, one before and one behind
+  __shared__ int positions[kMostChunk];
+  // zero block `z` of all, spread evenly, or sum block `block`
+  const int64_t all = gridDim.x;
+  const int z = static_cast<int>(blockIdx.x * static_cast<int64_t>(a.zero_blocks) / all);
+  if (static_cast<int>((blockIdx.x + 1) * static_cast<int64_t>(a.zero_blocks) / all) != z) {
+    zero_rest(a, static_cast<int64_t>(a.d) * sizeof(DT), a.lddw * static_cast<int64_t>(sizeof(DT)), sizeof(DT), z);
+    return;
+  }
+  const int block = blockIdx.x - z, chunk = block / a.slices, slice = block % a.slices;
+  const int lane = threadIdx.x % a.lanes, worker = threadIdx.x / a.lanes, workers = kSumThreads / a.lanes;
+  const int first_unit = slice * a.lanes * U + lane;
+  const int c0 = chunk * a.chunk, c1 = min(a.n, c0 + a.chunk);
+  const int* keys = keys_at + 1 - c0;
+  for (int i = threadIdx.x; i < c1 - c0 + 2; i += kSumThreads) {
+    const int at = c0 - 1 + i;
+    keys_at[i] = at < 0 ? -1 : at < a.n ? a.keys[at] : INT_MAX;
+    if (at >= c0 && at < c1) positions[at - c0] = a.positions[at];
+  }
+  __syncthreads();
+  const int j0 = min(c0 + worker * a.each, c1), j1 = min(j0 + a.each, c1);
+  float* first = &open[0][threadIdx.x * E];
+  float* last = &open[1][threadIdx.x * E];
+  float sum[E];
+  auto clear = [&] {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) sum[j] = 0.0f;
-  for (int j = j0; j < j1; j += kSumAhead) {
-    int key[kSumAhead];
-    Unit<GT, VEC> u[kSumAhead];
+    for (int k = 0; k < E; ++k) sum[k] = 0.0f;
+  };
+  auto finish = [&](int key) {
 #pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      key[i] = j + i < j1 ? a.keys[j + i] : INT_MAX;
-      if (key[i] < a.vocab) u[i] = load_unit_once<GT, VEC>(dy + a.positions[j + i] * a.lddy);
+    for (int i = 0; i < U; ++i) {
+      const int unit = first_unit + i * a.lanes;
+      if (unit < a.units) finish_unit<DT, VEC>(a, key, static_cast<int64_t>(unit) * VEC, sum + i * VEC);
     }
+  };
+  auto keep = [&](float* to) {
 #pragma unroll
-    for (int i = 0; i < kSumAhead; ++i) {
-      if (key[i] != run) {
-        if (run < a.vocab && j + i <= j1) {
-          // the run ended before this position, which may be the chunk's end
-          if (j + i == j1 && after == run) {  // goes on in the next chunk
-            store_unit<float, VEC>(part + (began ? 0 : a.d), sum);
-          } else if (began) {
-            store_unit<float, VEC>(part, sum);
-          } else {
-            finish_row<DT, VEC>(a, run, col, sum);
-          }
+    for (int k = 0; k < E; ++k) to[k] = sum[k];
+  };
+  if (j0 < j1 && first_unit < a.units) {
+    const GT* dy = static_cast<const GT*>(a.dy) + static_cast<int64_t>(first_unit) * VEC;
+    int run = keys[j0];  // the token being summed
+    bool began = keys[j0 - 1] == run;
+    clear();
+    for (int j = j0; j < j1 && run < a.vocab; j += AHEAD) {
+      Unit<GT, VEC> u[AHEAD][U];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (j + i >= j1 || keys[j + i] >= a.vocab) continue;
+        const GT* row = dy + positions[j + i - c0] * a.lddy;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          if (U == 1 || first_unit + k * a.lanes < a.units) u[i][k] = load_unit_once<GT, VEC>(row + k * a.lanes * VEC);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (j + i >= j1) continue;
+        const int key = keys[j + i];
+        if (key != run) {  // the run ended before this position
+          if (began) keep(first);
+          else finish(run);
+          run = key;
+          began = false;
+          clear();
+          if (run >= a.vocab) break;  // only tokens without a row follow
         }
-        run = key[i];
-        began = false;
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum[k] = 0.0f;
-      }
-      if (key[i] < a.vocab) {
-        float f[VEC];
-        unpack<GT, VEC>(u[i], f);
+        for (int k = 0; k < U; ++k) {
+          float f[VEC];
+          unpack<GT, VEC>(u[i][k], f);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) sum[k] += f[k];
+          for (int l = 0; l < VEC; ++l) sum[k * VEC + l] += f[l];
+        }
       }
+    }
+    if (run < a.vocab) {
+      if (began) keep(first);  // (and may go on)
+      else if (keys[j1] == run) keep(last);
+      else finish(run);
     }
   }
-  if (run < a.vocab) {  // the chunk's length is a whole number of steps: its last run is open
-    if (after == run) store_unit<float, VEC>(part + (began ? 0 : a.d), sum);
-    else if (began) store_unit<float, VEC>(part, sum);
-    else finish_row<DT, VEC>(a, run, col, sum);
+  __syncthreads();
+  // the pieces' open runs, in order: a worker's threads again
+  if (worker != 0 || first_unit >= a.units) return;
+  auto leave = [&](float* part) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int unit = first_unit + i * a.lanes;
+      if (unit >= a.units) continue;
+      float f[VEC];
+#pragma unroll
+      for (int l = 0; l < VEC; ++l) f[l] = sum[i * VEC + l];
+      store_unit<float, VEC>(part + static_cast<int64_t>(unit) * VEC, f);
+    }
+  };
+  float* part = a.part + static_cast<int64_t>(chunk) * 2 * a.d;
+  bool before = true;  // the run that is open began before the chunk
+  clear();
+  int p0 = c0;
+  for (int w = 0; w < workers && p0 < c1; ++w) {
+    const int p1 = min(p0 + a.each, c1);
+    const int head = keys[p0], tail = keys[p1 - 1];
+    if (head >= a.vocab) break;
+    const bool began = keys[p0 - 1] == head, goes_on = keys[p1] == tail && tail < a.vocab;
+    const int at = (w * a.lanes + lane) * E;
+    if (began) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) sum[k] += open[0][at + k];
+      if (head != tail || !goes_on) {  // it ends here
+        if (before) leave(part);
+        else finish(head);
+        before = false;
+      }
+    }
+    if (goes_on && !(began && head == tail)) {  // a run begins that goes on
+#pragma unroll
+      for (int k = 0; k < E; ++k) sum[k] = open[1][at + k];
+      before = false;
+    } else if (!goes_on) {
+      clear();
+    }
+    if (p1 == c1 && goes_on) leave(part + (before ? 0 : a.d));
+    p0 = p1;
   }
 }
 
-// A group of lanes for each chunk in which a run begins that goes on past it.
+// Runs over several chunks: a thread a unit for each chunk in which one begins
+// that goes on past it.
 template <class DT, int VEC>
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const __grid_constant__ SumArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int in_block = kSumThreads / a.lanes;
-  const int chunk = blockIdx.x * in_block + threadIdx.x / a.lanes;
-  const int unit = blockIdx.y * a.lanes + threadIdx.x % a.lanes;
-  if (threadIdx.x / a.lanes >= in_block || chunk >= a.chunks - 1 || unit >= a.units) return;
-  const int64_t col = static_cast<int64_t>(unit) * VEC;
-  const int end = (chunk + 1) * a.chunk;  // below n: another chunk follows
-  const int run = a.keys[end];
-  if (run >= a.vocab || a.keys[end - 1] != run) return;
-  const int begin = chunk * a.chunk;
-  if (a.keys[begin] == run && begin > 0 && a.keys[begin - 1] == run) return;  // began before
-  // the run's end: the first position with another token
-  int lo = end, hi = a.n;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (a.keys[mid] > run) hi = mid;
-    else lo = mid + 1;
-  }
-  const int last = (lo - 1) / a.chunk;  // the chunk that it ends in
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x;
+  const int chunk = static_cast<int>(at / a.units);
+  if (chunk >= a.chunks - 1) return;
+  const int64_t col = at % a.units * VEC;
+  const int begin = chunk * a.chunk, end = begin + a.chunk;  // below n: another chunk follows
+  const int run = a.keys[end], tail = a.keys[end - 1], head = a.keys[begin], prior = begin > 0 ? a.keys[begin - 1] : -1;
+  if (run >= a.vocab || tail != run) return;
+  if (head == run && prior == run) return;  // began before
   const int64_t pitch = 2 * static_cast<int64_t>(a.d);
   const float* part = a.part + chunk * pitch + col;
   float sum[VEC];
   unpack<float, VEC>(load_unit<float, VEC>(part + a.d), sum);
-  part += pitch;
-#pragma unroll 8
-  for (int c = chunk + 1; c <= last; ++c, part += pitch) {
-    float f[VEC];
-    unpack<float, VEC>(load_unit<float, VEC>(part), f);
+  // each chunk whose first key is the run's adds its first run; keys and sums of eight chunks at once
+  for (int c = chunk + 1; c < a.chunks; c += 8) {
+    int key[8];
+    Unit<float, VEC> u[8];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) sum[k] += f[k];
+    for (int i = 0; i < 8; ++i) key[i] = c + i < a.chunks ? a.keys[(c + i) * a.chunk] : INT_MAX;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (key[i] == run) u[i] = load_unit<float, VEC>(part + (c + i - chunk) * pitch);
+    bool more = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      more = more && key[i] == run;
+      if (!more) continue;
+      float f[VEC];
+      unpack<float, VEC>(u[i], f);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) sum[k] += f[k];
+    }
+    if (!more) break;
   }
-  finish_row<DT, VEC>(a, run, col, sum);
+  finish_unit<DT, VEC>(a, run, col, sum);
 }
 
 // A bf16 dW from the fp32 sums of several calls' worth of tokens.
@@ -494,9 +661,13 @@ dgl_status run_lookup(dgl_embed_desc e, cudaStream_t stream) {
   const cudaError_t err = with_types(e.w_dtype, e.y_dtype, vec, [&](auto w, auto y, auto v) {
     constexpr int kVec = decltype(v)::value;
     const int64_t units = e.d / kVec;
-    const LookupArgs a{e.tokens, e.ignore_index, e.W, e.ldw, e.Y, e.ldy, e.T, e.V, static_cast<int>(units), e.scale};
-    const int64_t each = kLookupThreads * kLookupEach;
-    const int64_t blocks = (e.T * units + each - 1) / each;
+    const int lanes = lanes_for(units);
+    const int64_t slice = static_cast<int64_t>(lanes) * kLookupUnits<decltype(w), kVec>;
+    const int64_t slices = (units + slice - 1) / slice;
+    const LookupArgs a{e.tokens, e.ignore_index,         e.W,   e.ldw,
+                       e.Y,      e.ldy,                  e.V,   static_cast<int>(e.T),
+                       static_cast<int>(units), lanes, static_cast<int>(slices), e.scale};
+    const int64_t blocks = (e.T * slices + kLookupThreads / lanes - 1) / (kLookupThreads / lanes);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     return launch_dependent(embed_lookup_kernel<decltype(w), decltype(y), kVec>, static_cast<unsigned>(blocks),
                             kLookupThreads, stream, a);
@@ -504,22 +675,23 @@ dgl_status run_lookup(dgl_embed_desc e, cudaStream_t stream) {
   return err == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
 }
 
+constexpr int kMostSms = 160;  // workspaces are sized for this many
+
 struct GradLayout {
-  int64_t keys = 0, positions = 0, part = 0, sums = 0, bytes = 0;
-  int chunk = 0;  // positions that a group sums
+  int64_t keys = 0, positions = 0, part = 0, present = 0, sums = 0, bytes = 0;
+  int each = 0;  // positions that a worker sums
 };
 
-// Positions of a chunk: 16, or as many more as leave about 2048 threads an SM.
-// (units of 16 bytes; rows that are accessed in smaller ones have more threads)
-int chunk_for(int64_t n, int64_t d, int64_t size) {
+// Positions that a worker sums: 8, or as many more as leave about 1500 threads an SM.
+int each_for(int64_t n, int64_t d, int64_t size) {
   const int64_t threads = n * round_up(d * size, 16) / 16;
-  return static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(16, round_up(threads / (152 * 2048), kSumAhead))));
+  return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(8, threads / (152 * 1500) / 8 * 8)));
 }
 
 GradLayout grad_layout(const dgl_embed_desc& e) {
   GradLayout l;
   const int64_t n = std::min(e.T, kSortMost);
-  l.chunk = chunk_for(n, e.d, size_of(e.y_dtype));
+  l.each = each_for(n, e.d, size_of(e.y_dtype));
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -528,20 +700,27 @@ GradLayout grad_layout(const dgl_embed_desc& e) {
   };
   l.keys = take(n * 4);
   l.positions = take(n * 4);
-  l.part = take((n + l.chunk - 1) / l.chunk * 2 * e.d * 4);
+  // (a block has the fewest workers when they are whole warps)
+  const int64_t chunk = static_cast<int64_t>(l.each) * (kSumThreads / 32);
+  l.part = take((n + chunk - 1) / chunk * 2 * e.d * 4);
+  l.present = take((e.V + 32 * 32 * kMostSms) / 8);  // (ranges are whole words)
   if (e.T > kSortMost && e.w_dtype == DGL_OUT_BF16) l.sums = take(e.V * e.d * 4);
   l.bytes = at;
   return l;
 }
 
+constexpr int64_t kZeroBytes = int64_t(40) << 20;      // zeros written beside the sort
+constexpr int64_t kZeroBlockBytes = int64_t(64) << 10;  // and by a block beside the sums
+constexpr int64_t kPrefetchBytes = int64_t(80) << 20;  // of dY that L2 keeps until the sums
+
 template <int EACH>
-cudaError_t launch_sort(const SortArgs& a, int ctas, int zero_ctas, cudaStream_t stream) {
+cudaError_t launch_sort(const SortArgs& a, int ctas, int helpers, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr int kBytes = static_cast<int>(sizeof(SortShared)) + EACH * kSortThreads * 8;
   const cudaError_t err = set_smem_attr_once(embed_sort_kernel<EACH>, kBytes, done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas + (zero_ctas + ctas - 1) / ctas * ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas + helpers));  // (whole clusters)
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
@@ -562,7 +741,7 @@ dgl_status run_grad(dgl_embed_desc e, cudaStream_t stream) {
   if (e.accumulate != 0 && (e.accumulate != 1 || e.w_dtype != DGL_OUT_F32)) return DGL_ERR_ARG;
   if (!e.dW || (e.T > 0 && (!e.tokens || !e.dY))) return DGL_ERR_ARG;
   if (!aligned(e.tokens, 8)) return DGL_ERR_ALIGN;
-  const int64_t size = size_of(e.w_dtype);
+  const int64_t size = size_of(e.w_dtype), y_size = size_of(e.y_dtype);
   int64_t vec = 16 / static_cast<int64_t>(size_of(e.y_dtype));
   dgl_status st;
   if ((st = check_matrix(e.dY, e.ldy, e.T, e.d, size_of(e.y_dtype), vec)) != DGL_OK ||
@@ -592,9 +771,8 @@ dgl_status run_grad(dgl_embed_desc e, cudaStream_t stream) {
   sort.digit_bits = (bits + sort.passes - 1) / sort.passes;
   sort.row_bytes = e.d * dw_size;
   sort.pitch_bytes = lddw * dw_size;
-  for (sort.store_bytes = 16; sort.store_bytes > dw_size; sort.store_bytes = sort.store_bytes == 16 ? 4 : 2)
-    if (aligned(dw, sort.store_bytes) && sort.row_bytes % sort.store_bytes == 0 && sort.pitch_bytes % sort.store_bytes == 0)
-      break;
+  sort.element = static_cast<int>(dw_size);
+  sort.present = reinterpret_cast<uint32_t*>(ws + lay.present);
   int64_t t0 = 0;
   do {
     const int n = static_cast<int>(std::min(kSortMost, e.T - t0));
@@ -605,13 +783,21 @@ dgl_status run_grad(dgl_embed_desc e, cudaStream_t stream) {
     sort.positions = reinterpret_cast<int*>(ws + lay.positions);
     sort.dw = dense ? dw : nullptr;
     const int ctas = n > kSortFew ? kSortCtas : 1;
-    const int zero_ctas = dense ? std::max(1, ds->num_sms - ctas) : 0;
+    const int others = std::max(1, (ds->num_sms - ctas) / ctas) * ctas;  // CTAs that do not sort
+    sort.share = static_cast<int>(round_up((e.V + others - 1) / others, 32));
+    // zeros for the time of the sort; without a next kernel, all of them
+    const int64_t now = n > 0 ? kZeroBytes / (others * sort.row_bytes) : sort.share;
+    sort.quota = static_cast<int>(std::min<int64_t>(sort.share, round_up(now, 32)));
+    sort.dy = static_cast<const uint8_t*>(e.dY) + t0 * e.ldy * y_size;
+    sort.dy_pitch = e.ldy * y_size;
+    sort.dy_bytes = n * e.d * y_size <= kPrefetchBytes ? e.d * y_size : 0;
+    const int helpers = dense || (sort.dy_bytes > 0 && n > kSortFew) ? others : 0;
     const int each = (n + ctas * kSortThreads - 1) / (ctas * kSortThreads);
-    const cudaError_t err = each <= 1   ? launch_sort<1>(sort, ctas, zero_ctas, stream)
-                            : each <= 2 ? launch_sort<2>(sort, ctas, zero_ctas, stream)
-                            : each <= 4 ? launch_sort<4>(sort, ctas, zero_ctas, stream)
-                            : each <= 8 ? launch_sort<8>(sort, ctas, zero_ctas, stream)
-                                        : launch_sort<kSortMostEach>(sort, ctas, zero_ctas, stream);
+    const cudaError_t err = each <= 1   ? launch_sort<1>(sort, ctas, helpers, stream)
+                            : each <= 2 ? launch_sort<2>(sort, ctas, helpers, stream)
+                            : each <= 4 ? launch_sort<4>(sort, ctas, helpers, stream)
+                            : each <= 8 ? launch_sort<8>(sort, ctas, helpers, stream)
+                                        : launch_sort<kSortMostEach>(sort, ctas, helpers, stream);
     if (err != cudaSuccess) return DGL_ERR_CUDA;
     if (n > 0) {
       const cudaError_t e2 = with_types(e.y_dtype, dw_type, vec, [&](auto g, auto w, auto v) {
@@ -628,20 +814,31 @@ dgl_status run_grad(dgl_embed_desc e, cudaStream_t stream) {
         a.part = reinterpret_cast<float*>(ws + lay.part);
         a.n = n;
         a.vocab = static_cast<int>(e.V);
-        a.chunk = lay.chunk;
-        a.chunks = (n + lay.chunk - 1) / lay.chunk;
-        a.d = static_cast<int>(e.d);
         a.units = static_cast<int>(e.d / kVec);
-        a.lanes = static_cast<int>(std::min<int64_t>(kSumThreads, round_up(a.units, 32)));
+        a.lanes = lanes_for(a.units);
+        const int workers = kSumThreads / a.lanes;
+        a.each = std::min(lay.each, kMostChunk / workers);
+        a.chunk = a.each * workers;
+        a.chunks = (n + a.chunk - 1) / a.chunk;
+        a.d = static_cast<int>(e.d);
+        const int slice = a.lanes * kSumUnits<G, kVec>;
+        a.slices = (a.units + slice - 1) / slice;
         a.scale = e.scale;
         a.add = dense ? 0 : 1;
-        const int in_block = kSumThreads / a.lanes;
-        const dim3 grid(static_cast<unsigned>((a.chunks + in_block - 1) / in_block),
-                        static_cast<unsigned>((a.units + a.lanes - 1) / a.lanes));
-        if (grid.y > 65535) return cudaErrorInvalidValue;
-        const cudaError_t e3 = launch_dependent(embed_sum_kernel<G, W, kVec>, grid, kSumThreads, stream, a);
+        if (dense && sort.quota < sort.share) {
+          a.present = sort.present;
+          a.range_words = sort.share / 32;
+          a.quota_words = sort.quota / 32;
+          a.words = static_cast<int64_t>(helpers) * (a.range_words - a.quota_words);
+          a.words_each = static_cast<int>(std::max<int64_t>(1, kZeroBlockBytes / (32 * sort.row_bytes)));
+          a.zero_blocks = static_cast<int>((a.words + a.words_each - 1) / a.words_each);
+        }
+        const int64_t grid = static_cast<int64_t>(a.chunks) * a.slices + a.zero_blocks;
+        const int64_t join = (static_cast<int64_t>(a.chunks - 1) * a.units + kSumThreads - 1) / kSumThreads;
+        if (grid > INT32_MAX || join > INT32_MAX) return cudaErrorInvalidValue;
+        const cudaError_t e3 = launch_dependent(embed_sum_kernel<G, W, kVec>, static_cast<unsigned>(grid), kSumThreads, stream, a);
         if (e3 != cudaSuccess || a.chunks < 2) return e3;
-        return launch_dependent(embed_join_kernel<W, kVec>, grid, kSumThreads, stream, a);
+        return launch_dependent(embed_join_kernel<W, kVec>, static_cast<unsigned>(join), kSumThreads, stream, a);
       });
       if (e2 != cudaSuccess) return DGL_ERR_CUDA;
     }
