@@ -100,8 +100,19 @@ __device__ __forceinline__ uint64_t split_mix(uint64_t z) {
   return z ^ (z >> 31);
 }
 
-// Eight elements from p on, as far as they exist; 0 past them.
-__device__ __forceinline__ void load8(const float* p, int have, uint32_t kind, float (&f)[kEach]) {
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Products in pairs, and their sum one by one: fused into one rounding, as packed
+// additions were, they would not give the bits that an 8-bit state depends on.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add_apart(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
+// Eight elements from p on, as far as they exist; 0 past them.  (Elements are in
+// pairs, for the packed fp32 instructions.)
+__device__ __forceinline__ void load8(const float* p, int have, uint32_t kind, float2 (&pairs)[kEach / 2]) {
+  float(&f)[kEach] = reinterpret_cast<float(&)[kEach]>(pairs);
   if (have == kEach && (kind & UNITS_32)) {
     asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
@@ -114,7 +125,8 @@ __device__ __forceinline__ void load8(const float* p, int have, uint32_t kind, f
     for (int i = 0; i < kEach; ++i) f[i] = i < have ? p[i] : 0.0f;
   }
 }
-__device__ __forceinline__ void load8(const bf16* p, int have, uint32_t kind, float (&f)[kEach]) {
+__device__ __forceinline__ void load8(const bf16* p, int have, uint32_t kind, float2 (&pairs)[kEach / 2]) {
+  float(&f)[kEach] = reinterpret_cast<float(&)[kEach]>(pairs);
   if (have == kEach && (kind & (UNITS_32 | UNITS_16))) {
     unpack<bf16, kEach>(load_unit<bf16, kEach>(p), f);
   } else {
@@ -131,7 +143,8 @@ __device__ __forceinline__ uint2 load8(const uint8_t* p, int have, uint32_t kind
   return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ void store8(float* p, int have, uint32_t kind, const float (&f)[kEach]) {
+__device__ __forceinline__ void store8(float* p, int have, uint32_t kind, const float2 (&pairs)[kEach / 2]) {
+  const float(&f)[kEach] = reinterpret_cast<const float(&)[kEach]>(pairs);
   if (have == kEach && (kind & UNITS_32)) {
     asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
                  "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
@@ -145,7 +158,8 @@ __device__ __forceinline__ void store8(float* p, int have, uint32_t kind, const 
       if (i < have) p[i] = f[i];
   }
 }
-__device__ __forceinline__ void store8(bf16* p, int have, uint32_t kind, const float (&f)[kEach]) {
+__device__ __forceinline__ void store8(bf16* p, int have, uint32_t kind, const float2 (&pairs)[kEach / 2]) {
+  const float(&f)[kEach] = reinterpret_cast<const float(&)[kEach]>(pairs);
   if (have == kEach && (kind & (UNITS_32 | UNITS_16))) {
     store_unit<bf16, kEach>(p, f);
   } else {
@@ -166,20 +180,31 @@ __device__ __forceinline__ void store8(uint8_t* p, int have, uint32_t kind, uint
 
 // The values of eight E4M3 or E5M2 codes (E5M2 is the upper half of an fp16).
 template <bool E4M3>
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kEach]) {
+__device__ __forceinline__ void decode8(uint2 c, float scale, float2 (&f)[kEach / 2]) {
 #pragma unroll
-  for (int i = 0; i < kEach; i += 2) {
-    const uint32_t two = (i < 4 ? c.x : c.y) >> (8 * (i % 4)) & 0xffffu;
+  for (int i = 0; i < kEach / 2; ++i) {
+    const uint32_t word = i < 2 ? c.x : c.y;
     float2 v;
     if constexpr (E4M3) {
+      const uint32_t two = i % 2 ? word >> 16 : word & 0xffffu;
       v = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3)));
     } else {
-      v.x = __half2float(__ushort_as_half(static_cast<uint16_t>(two << 8)));
-      v.y = __half2float(__ushort_as_half(static_cast<uint16_t>(two & 0xff00u)));
+      const uint32_t two = __byte_perm(word, 0, i % 2 ? 0x3424 : 0x1404);
+      v = __half22float2(*reinterpret_cast<const __half2*>(&two));
     }
-    f[i] = v.x * scale;
-    f[i + 1] = v.y * scale;
+    f[i] = mul2(v, both(scale));
   }
+}
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The upper bytes of four words.
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 // Codes of eight values and their block's scale.  The block's largest finite
@@ -189,34 +214,72 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kEach])
 // subnormals begin where the format's do): a random number below the
 // last of them carries into the code as often as the rest of the fraction asks.
 // A v above zero never becomes zero, which the update divides by; what is not
-// finite becomes NaN.
+// finite becomes NaN, in a pass of its own that blocks without such a value
+// need not pay for.
 template <bool E4M3>
-__device__ __forceinline__ uint2 encode8(const float (&f)[kEach], const uint32_t (&random)[kEach], float& scale) {
+__device__ __forceinline__ uint2 encode8(const float2 (&f)[kEach / 2], const uint32_t (&random)[kEach], float& scale) {
   constexpr int kTop = E4M3 ? 7 : 14, kShift = E4M3 ? 20 : 21;
-  float top = 0.0f;
+  float x[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const float a = fabsf(f[i]);
-    top = fmaxf(top, a < INFINITY ? a : 0.0f);
+  for (int i = 0; i < kEach; ++i) x[i] = i % 2 ? f[i / 2].y : f[i / 2].x;
+  float top = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < kEach; ++i) top = max_or_nan(top, fabsf(x[i]));
+#pragma unroll
+  for (int o = 1; o < kBlock / kEach; o *= 2) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool finite = top < INFINITY;  // the same in all threads of the block
+  if (__any_sync(0xffffffffu, !finite)) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) most = fmaxf(most, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.0f);
+#pragma unroll
+    for (int o = 1; o < kBlock / kEach; o *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    top = most;
   }
-#pragma unroll
-  for (int o = 1; o < kBlock / kEach; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   // the scale and its reciprocal are normal numbers
   const uint32_t exponent = max(__float_as_uint(top) >> 23, 16u);
   scale = __uint_as_float((exponent - kTop) << 23);
-  const float up = __uint_as_float((254 + kTop - exponent) << 23);
-  const float down = E4M3 ? 7.52316384526264e-37f : 1.92592994438724e-34f;  // 2^-120, 2^-112
-  uint32_t code[kEach];
+  // 2^TOP over the largest's power of two, times 2^-120 or 2^-112: one factor
+  // where that is a normal number, else two
+  constexpr uint32_t kDown = E4M3 ? 120 : 112;
+  const bool one = exponent + kDown < 254 + kTop;
+  const float up = __uint_as_float((254 + kTop - exponent - (one ? kDown : 0)) << 23);
+  const float down = one ? 1.0f : __uint_as_float((127 - kDown) << 23);
+  uint32_t code[kEach];  // in the upper byte
+  auto round = [&](int i, float scaled) {
+    const uint32_t r = E4M3 ? (random[i] << 4 & 0xffff0u) | 8u : (random[i] >> 11 & 0x1fffe0u) | 16u;
+    code[i] = __float_as_uint(scaled) + r;
+    if constexpr (!E4M3) code[i] = max(code[i], x[i] > 0.0f ? 1u << kShift : 0u);
+    code[i] <<= 24 - kShift;
+  };
+  if (__all_sync(0xffffffffu, one)) {
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const uint32_t r = E4M3 ? (random[i] & 0xffffu) << 4 | 8u : (random[i] >> 16) << 5 | 16u;
-    const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(fabsf(f[i]), up), down));
-    code[i] = min((bits + r) >> kShift, 0x7fu);
-    if constexpr (E4M3) code[i] |= __float_as_uint(f[i]) >> 31 << 7;
-    else if (f[i] > 0.0f) code[i] = max(code[i], 1u);
+    for (int i = 0; i < kEach; ++i) round(i, __fmul_rn(fabsf(x[i]), up));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) round(i, __fmul_rn(__fmul_rn(fabsf(x[i]), up), down));
   }
-  return make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                    code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
+  if (!finite) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (!(fabsf(x[i]) < INFINITY)) code[i] = 0x7f000000u;
+  }
+  uint2 c = make_uint2(upper_bytes(code[0], code[1], code[2], code[3]), upper_bytes(code[4], code[5], code[6], code[7]));
+  if constexpr (E4M3) {
+    c.x |= 0x80808080u & upper_bytes(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    c.y |= 0x80808080u & upper_bytes(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+  }
+  return c;
+}
+
+// m / (sqrt(v) root + eps) by the hardware's approximations, off by a few units
+// in the last place.  They take subnormal numbers for zero: a v below 2^-126
+// is nothing beside an eps past 1e-18; without one its root is taken in full.
+__device__ __forceinline__ float quotient(float m, float v, float root, float eps) {
+  float r, q;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(fmaf(r, root, eps)));
+  return m * q;
 }
 
 template <bool EIGHT, int CAP>
@@ -232,14 +295,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
   const float root = 1.0f / sqrtf(-expm1f(static_cast<float>(static_cast<double>(steps) * s.log_beta2)));
   const uint64_t key = EIGHT ? split_mix(s.seed + static_cast<uint64_t>(steps) * kGolden) : 0;
 
+  // a range of chunks, and the tensor that its first lies in
+  const uint32_t begin = static_cast<uint32_t>(static_cast<uint64_t>(s.chunks) * blockIdx.x / gridDim.x);
+  const uint32_t end = static_cast<uint32_t>(static_cast<uint64_t>(s.chunks) * (blockIdx.x + 1) / gridDim.x);
   int at = 0;
-  for (uint32_t chunk = blockIdx.x; chunk < s.chunks; chunk += gridDim.x) {
+  for (int step = CAP; step > 0; step /= 2)
+    while (at + step < s.count && a.t[at + step].first_chunk <= begin) at += step;
+  for (uint32_t chunk = begin; chunk < end; ++chunk) {
     while (at + 1 < s.count && a.t[at + 1].first_chunk <= chunk) ++at;
     const AdamTensor& t = a.t[at];
     const uint32_t kind = t.kind;
     const int64_t e = static_cast<int64_t>(chunk - t.first_chunk) * kChunk + threadIdx.x * kEach;
     const int have = static_cast<int>(min(max(t.n - e, int64_t(0)), int64_t(kEach)));
-    float p[kEach], g[kEach], m[kEach], v[kEach];
+    float2 p[kEach / 2], g[kEach / 2], m[kEach / 2], v[kEach / 2];
     if (kind & GRAD_F32) load8(static_cast<const float*>(t.g) + e, have, kind, g);
     else load8(static_cast<const bf16*>(t.g) + e, have, kind, g);
     if (t.master) load8(t.master + e, have, kind, p);
@@ -257,15 +325,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
     }
     const float fade = -lr * t.decay;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      // single roundings, not fused: an 8-bit state depends on these bits alone
-      g[i] = __fmul_rn(g[i], grad_scale);
-      m[i] = __fadd_rn(__fmul_rn(s.beta1, m[i]), __fmul_rn(s.rest1, g[i]));
-      v[i] = __fadd_rn(__fmul_rn(s.beta2, v[i]), __fmul_rn(s.rest2, __fmul_rn(g[i], g[i])));
-      float r;
-      asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v[i]));
-      const float u = __fdividef(m[i], fmaf(r, root, s.eps));
-      p[i] = fmaf(-size, u, fmaf(fade, p[i], p[i]));
+    for (int i = 0; i < kEach / 2; ++i) {
+      g[i] = mul2(g[i], both(grad_scale));
+      m[i] = add_apart(mul2(both(s.beta1), m[i]), mul2(both(s.rest1), g[i]));
+      v[i] = add_apart(mul2(both(s.beta2), v[i]), mul2(both(s.rest2), mul2(g[i], g[i])));
+    }
+    if (s.eps > 1e-18f) {
+#pragma unroll
+      for (int i = 0; i < kEach / 2; ++i) {
+        const float2 u = make_float2(quotient(m[i].x, v[i].x, root, s.eps), quotient(m[i].y, v[i].y, root, s.eps));
+        p[i] = __ffma2_rn(both(-size), u, __ffma2_rn(both(fade), p[i], p[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach / 2; ++i) {
+        const float2 u = make_float2(m[i].x / fmaf(sqrtf(v[i].x), root, s.eps), m[i].y / fmaf(sqrtf(v[i].y), root, s.eps));
+        p[i] = __ffma2_rn(both(-size), u, __ffma2_rn(both(fade), p[i], p[i]));
+      }
     }
     if (t.master) store8(t.master + e, have, kind, p);
     if (kind & PARAM_F32) store8(static_cast<float*>(t.p) + e, have, kind, p);

@@ -136,7 +136,8 @@ struct SortArgs {
 };
 
 struct SortShared {
-  uint16_t hist[kSortWarps][kBins];  // tokens of a warp with a digit, then those of the warps before
+  uint16_t hist[kSortWarps][kBins];  // tokens of a warp with a digit, then those of its half's warps before
+  uint32_t half[2][kBins];           // of the CTA's lower and upper half of warps
   uint32_t total[kBins];             // of the CTA; other CTAs read it
   uint32_t base[kBins];              // where the CTA's tokens with a digit go
   uint32_t warp_sum[kSortWarps];
@@ -196,25 +197,33 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, uint2* items, int
       __syncwarp();
     }
     __syncthreads();
+    // a digit's tokens in the warps before: two threads a digit, half of the warps each
+    constexpr int kHalf = kSortWarps / 2;
+    static_assert(kSortThreads == 2 * kBins, "two threads a digit");
+    const int bin = threadIdx.x % kBins, half = threadIdx.x / kBins;
     uint32_t all = 0;
-    if (threadIdx.x < kBins) {
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = sh.hist[w][threadIdx.x];
-        sh.hist[w][threadIdx.x] = static_cast<uint16_t>(all);
-        all += c;
-      }
-      sh.total[threadIdx.x] = all;
+#pragma unroll
+    for (int w = half * kHalf; w < (half + 1) * kHalf; ++w) {
+      const uint32_t c = sh.hist[w][bin];
+      sh.hist[w][bin] = static_cast<uint16_t>(all);
+      all += c;
     }
+    sh.half[half][bin] = all;
+    __syncthreads();
+    all = sh.half[0][bin] + sh.half[1][bin];
+    if (half == 0) sh.total[bin] = all;
     uint32_t earlier = 0;  // with this thread's digit, in CTAs before this one
     if (ctas > 1) {
       cluster_sync();  // also: every CTA has taken its items of the last pass
-      if (threadIdx.x < kBins) {
+      if (half == 0) {
+        uint32_t c[kSortCtas];
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) c[r] = load_cluster(mapa_shared(smem_u32(&sh.total[bin]), r));
         all = 0;
-        for (int r = 0; r < ctas; ++r) {
-          const uint32_t c = load_cluster(mapa_shared(smem_u32(&sh.total[threadIdx.x]), r));
-          if (r < rank) earlier += c;
-          all += c;
+#pragma unroll
+        for (int r = 0; r < kSortCtas; ++r) {
+          if (r < rank) earlier += c[r];
+          all += c[r];
         }
       }
     }
@@ -225,19 +234,20 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, uint2* items, int
       const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (lane == 31) sh.warp_sum[warp] = sum;
+    if (half == 0 && lane == 31) sh.warp_sum[warp] = sum;
     __syncthreads();
-    if (threadIdx.x < kBins) {
-      uint32_t lower = sum - all + earlier;
-      for (int w = 0; w < warp; ++w) lower += sh.warp_sum[w];
-      sh.base[threadIdx.x] = lower;
+    if (half == 0) {
+      uint32_t before_warp = lane < warp ? sh.warp_sum[lane] : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) before_warp += __shfl_xor_sync(0xffffffffu, before_warp, o);
+      sh.base[bin] = sum - all + earlier + before_warp;
     }
     __syncthreads();
     const bool last = pass == a.passes - 1;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const uint32_t digit = key[i] >> shift & mask;
-      const uint32_t to = sh.base[digit] + sh.hist[warp][digit] + before[i];
+      const uint32_t to = sh.base[digit] + (warp < kHalf ? 0 : sh.half[0][digit]) + sh.hist[warp][digit] + before[i];
       if (last) {
         if (to < static_cast<uint32_t>(a.n)) {
           a.keys[to] = static_cast<int>(key[i]);
