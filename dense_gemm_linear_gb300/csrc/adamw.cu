@@ -5,8 +5,8 @@
 //
 // One launch takes hundreds of tensors: their addresses travel in the kernel's
 // parameters, so a call uploads nothing and a captured one stays valid.  The
-// tensors are cut into chunks of 2048 elements that a persistent grid walks in
-// order, 8 neighbouring elements a thread.  Every element is read and written
+// tensors are cut into chunks of 2048 elements, of which a block takes a
+// few, 8 neighbouring elements a thread.  Every element is read and written
 // once: the kernel is bound by HBM (28 bytes an element with fp32 weights,
 // gradients and states, 14 with 8-bit states and bf16 gradients), and with 8-bit states nearly as
 // much by its arithmetic.
@@ -42,16 +42,25 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kBlock = DGL_ADAMW_BLOCK;  // elements of an 8-bit state that share a scale
-constexpr int kEach = 8;                 // elements a thread takes of a chunk
+constexpr int kEach = 8;  // neighbouring elements that a thread takes
 constexpr int kThreads = 256;
 constexpr int kChunk = kEach * kThreads;
-constexpr int kBlocksPerSm = 4;
+// With 8-bit states the arithmetic bounds the kernel and its latency asks for
+// warps: five blocks an SM, at 48 registers (304 M elements: 793 us; four blocks 821, three with the loads of two chunks under way 809).
+template <bool EIGHT>
+constexpr int kBlocksPerSm = EIGHT ? 5 : 4;
+// Chunks that a block takes, where there are enough for many blocks: blocks that end and
+// make room spread the work better over SMs of unequal speed than ones that stay (304 M
+// elements, 32 bits: 1418 us with a resident grid, 1318 so), but each begins
+// with what its elements share.
+template <bool EIGHT>
+constexpr uint32_t kBlockChunks = EIGHT ? 32 : 8;
 
-enum : uint32_t {
+enum : int {
   PARAM_F32 = 1,
   GRAD_F32 = 2,
-  UNITS_32 = 4,  // every address allows units of 8 elements: 32 bytes of fp32, 16 of bf16, 8 of 8-bit states
-  UNITS_16 = 8,  // units of at most 16 bytes
+  MASTER = 4,
+  ANY_TYPES = 8,
 };
 
 struct AdamTensor {
@@ -65,7 +74,7 @@ struct AdamTensor {
   int64_t n;
   int64_t first_block;   // blocks of 128 in the call's tensors before this one
   uint32_t first_chunk;  // chunks in the launch's tensors before this one
-  uint32_t kind;
+  int types;
   float decay;
 };
 
@@ -105,77 +114,82 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // Products in pairs, and their sum one by one: fused into one rounding, as packed
 // additions were, they would not give the bits that an 8-bit state depends on.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 add_apart(float2 a, float2 b) {
   return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 
-// Eight elements from p on, as far as they exist; 0 past them.  (Elements are in
-// pairs, for the packed fp32 instructions.)
-__device__ __forceinline__ void load8(const float* p, int have, uint32_t kind, float2 (&pairs)[kEach / 2]) {
-  float(&f)[kEach] = reinterpret_cast<float(&)[kEach]>(pairs);
-  if (have == kEach && (kind & UNITS_32)) {
-    asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                 : "l"(p));
-  } else if (have == kEach && (kind & UNITS_16)) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+// Eight elements on their way: fp32 in eight words, bf16 in four.
+struct Eight {
+  uint32_t w[kEach];
+};
+
+// Eight elements from element e of p on: as units, or one by one as far as they
+// exist (0 past them).
+__device__ __forceinline__ void load8(const void* p, int64_t e, bool f32, Eight& x) {
+  if (f32) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
+                   "=r"(x.w[7])
+                 : "l"(static_cast<const float*>(p) + e));
   } else {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) f[i] = i < have ? p[i] : 0.0f;
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
   }
 }
-__device__ __forceinline__ void load8(const bf16* p, int have, uint32_t kind, float2 (&pairs)[kEach / 2]) {
-  float(&f)[kEach] = reinterpret_cast<float(&)[kEach]>(pairs);
-  if (have == kEach && (kind & (UNITS_32 | UNITS_16))) {
-    unpack<bf16, kEach>(load_unit<bf16, kEach>(p), f);
-  } else {
+__device__ __forceinline__ void load8_guarded(const void* p, int64_t e, bool f32, int have, Eight& x) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) f[i] = i < have ? __bfloat162float(p[i]) : 0.0f;
+  for (int i = 0; i < kEach; ++i) x.w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i >= have) continue;
+    if (f32) x.w[i] = static_cast<const uint32_t*>(p)[e + i];
+    else x.w[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[e + i]) << (16 * (i % 2));
   }
 }
-__device__ __forceinline__ uint2 load8(const uint8_t* p, int have, uint32_t kind) {
-  if (have == kEach && (kind & (UNITS_32 | UNITS_16))) return *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ uint2 load8_guarded(const uint8_t* p, int have) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
     if (i < have) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
   return make_uint2(w[0], w[1]);
 }
-
-__device__ __forceinline__ void store8(float* p, int have, uint32_t kind, const float2 (&pairs)[kEach / 2]) {
-  const float(&f)[kEach] = reinterpret_cast<const float(&)[kEach]>(pairs);
-  if (have == kEach && (kind & UNITS_32)) {
-    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
-                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+// (elements are in pairs, for the packed fp32 instructions)
+__device__ __forceinline__ void values(const Eight& x, bool f32, float2 (&f)[kEach / 2]) {
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < kEach / 2; ++i) f[i] = make_float2(__uint_as_float(x.w[2 * i]), __uint_as_float(x.w[2 * i + 1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach / 2; ++i)
+      f[i] = make_float2(__uint_as_float(x.w[i] << 16), __uint_as_float(x.w[i] & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void store8(void* p, int64_t e, bool f32, const float2 (&f)[kEach / 2]) {
+  if (f32) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(static_cast<float*>(p) + e), "f"(f[0].x),
+                 "f"(f[0].y), "f"(f[1].x), "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y)
                  : "memory");
-  } else if (have == kEach && (kind & UNITS_16)) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
   } else {
+    __nv_bfloat162 two[kEach / 2];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i < have) p[i] = f[i];
+    for (int i = 0; i < kEach / 2; ++i) two[i] = __floats2bfloat162_rn(f[i].x, f[i].y);
+    *reinterpret_cast<uint4*>(static_cast<bf16*>(p) + e) = *reinterpret_cast<uint4*>(two);
   }
 }
-__device__ __forceinline__ void store8(bf16* p, int have, uint32_t kind, const float2 (&pairs)[kEach / 2]) {
-  const float(&f)[kEach] = reinterpret_cast<const float(&)[kEach]>(pairs);
-  if (have == kEach && (kind & (UNITS_32 | UNITS_16))) {
-    store_unit<bf16, kEach>(p, f);
-  } else {
+__device__ __forceinline__ void store8_guarded(void* p, int64_t e, bool f32, int have, const float2 (&f)[kEach / 2]) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i < have) p[i] = __float2bfloat16_rn(f[i]);
+  for (int i = 0; i < kEach; ++i) {
+    const float v = i % 2 ? f[i / 2].y : f[i / 2].x;
+    if (i >= have) continue;
+    if (f32) static_cast<float*>(p)[e + i] = v;
+    else static_cast<bf16*>(p)[e + i] = __float2bfloat16_rn(v);
   }
 }
-__device__ __forceinline__ void store8(uint8_t* p, int have, uint32_t kind, uint2 c) {
-  if (have == kEach && (kind & (UNITS_32 | UNITS_16))) {
-    *reinterpret_cast<uint2*>(p) = c;
-  } else {
+__device__ __forceinline__ void store8_guarded(uint8_t* p, int have, uint2 c) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (i < have) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
-  }
+  for (int i = 0; i < kEach; ++i)
+    if (i < have) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
 }
 
 // The values of eight E4M3 or E5M2 codes (E5M2 is the upper half of an fp16).
@@ -282,17 +296,21 @@ __device__ __forceinline__ float quotient(float m, float v, float root, float ep
   return m * q;
 }
 
-template <bool EIGHT, int CAP>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __grid_constant__ AdamTable<CAP> a) {
+// TYPES: the tensors' PARAM_F32, GRAD_F32 and MASTER, which are the same for all of a
+// launch and whose addresses all allow units of 8 elements; or ANY_TYPES: each its own.
+template <bool EIGHT, int TYPES, int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<EIGHT>) adamw_kernel(const __grid_constant__ AdamTable<CAP> a) {
   griddep_wait();
   griddep_launch_dependents();
   const AdamScalars& s = a.s;
+  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  // (By each thread: by one for its block the others waited longer than this
+  // takes, 816 -> 934 us.)
   const int64_t steps = *s.steps + 1;
   const float grad_scale = s.grad_scale ? *s.grad_scale : 1.0f;
   const float lr = s.lr_at ? *s.lr_at : s.lr;
-  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   const float size = lr / -expm1f(static_cast<float>(static_cast<double>(steps) * s.log_beta1));
-  const float root = 1.0f / sqrtf(-expm1f(static_cast<float>(static_cast<double>(steps) * s.log_beta2)));
+  const float root = rsqrtf(-expm1f(static_cast<float>(static_cast<double>(steps) * s.log_beta2)));
   const uint64_t key = EIGHT ? split_mix(s.seed + static_cast<uint64_t>(steps) * kGolden) : 0;
 
   // a range of chunks, and the tensor that its first lies in
@@ -304,25 +322,49 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
   for (uint32_t chunk = begin; chunk < end; ++chunk) {
     while (at + 1 < s.count && a.t[at + 1].first_chunk <= chunk) ++at;
     const AdamTensor& t = a.t[at];
-    const uint32_t kind = t.kind;
+    constexpr bool kAny = TYPES == ANY_TYPES;
+    const int types = kAny ? t.types : TYPES;
     const int64_t e = static_cast<int64_t>(chunk - t.first_chunk) * kChunk + threadIdx.x * kEach;
+    void* const param = t.p;
+    float* const master = t.master;
+    const bool param_f32 = types & PARAM_F32, grad_f32 = types & GRAD_F32, mastered = types & MASTER;
     const int have = static_cast<int>(min(max(t.n - e, int64_t(0)), int64_t(kEach)));
-    float2 p[kEach / 2], g[kEach / 2], m[kEach / 2], v[kEach / 2];
-    if (kind & GRAD_F32) load8(static_cast<const float*>(t.g) + e, have, kind, g);
-    else load8(static_cast<const bf16*>(t.g) + e, have, kind, g);
-    if (t.master) load8(t.master + e, have, kind, p);
-    else if (kind & PARAM_F32) load8(static_cast<const float*>(t.p) + e, have, kind, p);
-    else load8(static_cast<const bf16*>(t.p) + e, have, kind, p);
-    if constexpr (EIGHT) {
-      const uint2 cm = load8(static_cast<const uint8_t*>(t.m) + e, have, kind);
-      const uint2 cv = load8(static_cast<const uint8_t*>(t.v) + e, have, kind);
-      const float ms = have > 0 ? t.m_scale[e / kBlock] : 0.0f, vs = have > 0 ? t.v_scale[e / kBlock] : 0.0f;
-      decode8<true>(cm, ms, m);
-      decode8<false>(cv, vs, v);
+    const bool whole = !kAny && have == kEach;
+    Eight in_p, in_g, in_m, in_v;  // (of 8-bit states the first two words)
+    if (whole) {
+      load8(t.g, e, grad_f32, in_g);
+      load8(mastered ? master : param, e, mastered || param_f32, in_p);
+      if constexpr (EIGHT) {
+        const uint2 cm = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + e);
+        const uint2 cv = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + e);
+        in_m.w[0] = cm.x, in_m.w[1] = cm.y, in_v.w[0] = cv.x, in_v.w[1] = cv.y;
+      } else {
+        load8(t.m, e, true, in_m);
+        load8(t.v, e, true, in_v);
+      }
     } else {
-      load8(static_cast<const float*>(t.m) + e, have, kind, m);
-      load8(static_cast<const float*>(t.v) + e, have, kind, v);
+      load8_guarded(t.g, e, grad_f32, have, in_g);
+      load8_guarded(mastered ? master : param, e, mastered || param_f32, have, in_p);
+      if constexpr (EIGHT) {
+        const uint2 cm = load8_guarded(static_cast<const uint8_t*>(t.m) + e, have);
+        const uint2 cv = load8_guarded(static_cast<const uint8_t*>(t.v) + e, have);
+        in_m.w[0] = cm.x, in_m.w[1] = cm.y, in_v.w[0] = cv.x, in_v.w[1] = cv.y;
+      } else {
+        load8_guarded(t.m, e, true, have, in_m);
+        load8_guarded(t.v, e, true, have, in_v);
+      }
     }
+    float2 p[kEach / 2], g[kEach / 2], m[kEach / 2], v[kEach / 2];
+    if constexpr (EIGHT) {
+      const float m_scale = have > 0 ? t.m_scale[e / kBlock] : 0.0f, v_scale = have > 0 ? t.v_scale[e / kBlock] : 0.0f;
+      decode8<true>(make_uint2(in_m.w[0], in_m.w[1]), m_scale, m);
+      decode8<false>(make_uint2(in_v.w[0], in_v.w[1]), v_scale, v);
+    } else {
+      values(in_m, true, m);
+      values(in_v, true, v);
+    }
+    values(in_g, grad_f32, g);
+    values(in_p, mastered || param_f32, p);
     const float fade = -lr * t.decay;
 #pragma unroll
     for (int i = 0; i < kEach / 2; ++i) {
@@ -334,21 +376,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
 #pragma unroll
       for (int i = 0; i < kEach / 2; ++i) {
         const float2 u = make_float2(quotient(m[i].x, v[i].x, root, s.eps), quotient(m[i].y, v[i].y, root, s.eps));
-        p[i] = __ffma2_rn(both(-size), u, __ffma2_rn(both(fade), p[i], p[i]));
+        p[i] = fma2(both(-size), u, fma2(both(fade), p[i], p[i]));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < kEach / 2; ++i) {
         const float2 u = make_float2(m[i].x / fmaf(sqrtf(v[i].x), root, s.eps), m[i].y / fmaf(sqrtf(v[i].y), root, s.eps));
-        p[i] = __ffma2_rn(both(-size), u, __ffma2_rn(both(fade), p[i], p[i]));
+        p[i] = fma2(both(-size), u, fma2(both(fade), p[i], p[i]));
       }
     }
-    if (t.master) store8(t.master + e, have, kind, p);
-    if (kind & PARAM_F32) store8(static_cast<float*>(t.p) + e, have, kind, p);
-    else store8(static_cast<bf16*>(t.p) + e, have, kind, p);
+    if (whole) {
+      if (mastered) store8(master, e, true, p);
+      store8(param, e, param_f32, p);
+    } else {
+      if (mastered) store8_guarded(master, e, true, have, p);
+      store8_guarded(param, e, param_f32, have, p);
+    }
     if constexpr (EIGHT) {
       uint32_t random[kEach];
-      uint64_t x = key + static_cast<uint64_t>((t.first_block * kBlock + e) / 2) * kGolden;
+      uint64_t x = key + static_cast<uint64_t>(t.first_block * kBlock + e) / 2 * kGolden;
 #pragma unroll
       for (int i = 0; i < kEach; i += 2) {
         x += kGolden;
@@ -356,17 +402,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) adamw_kernel(const __g
         random[i] = static_cast<uint32_t>(z);
         random[i + 1] = static_cast<uint32_t>(z >> 32);
       }
-      float scale;
-      const uint2 cm = encode8<true>(m, random, scale);
-      const bool leads = threadIdx.x % (kBlock / kEach) == 0 && have > 0;
-      if (leads) t.m_scale[e / kBlock] = scale;
-      store8(static_cast<uint8_t*>(t.m) + e, have, kind, cm);
-      const uint2 cv = encode8<false>(v, random, scale);
-      if (leads) t.v_scale[e / kBlock] = scale;
-      store8(static_cast<uint8_t*>(t.v) + e, have, kind, cv);
+      float m_scale, v_scale;
+      const uint2 cm = encode8<true>(m, random, m_scale);
+      const uint2 cv = encode8<false>(v, random, v_scale);
+      if (threadIdx.x % (kBlock / kEach) == 0 && have > 0) {
+        t.m_scale[e / kBlock] = m_scale;
+        t.v_scale[e / kBlock] = v_scale;
+      }
+      if (whole) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + e) = cm;
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + e) = cv;
+      } else {
+        store8_guarded(static_cast<uint8_t*>(t.m) + e, have, cm);
+        store8_guarded(static_cast<uint8_t*>(t.v) + e, have, cv);
+      }
+    } else if (whole) {
+      store8(t.m, e, true, m);
+      store8(t.v, e, true, v);
     } else {
-      store8(static_cast<float*>(t.m) + e, have, kind, m);
-      store8(static_cast<float*>(t.v) + e, have, kind, v);
+      store8_guarded(t.m, e, true, have, m);
+      store8_guarded(t.v, e, true, have, v);
     }
   }
   // the last block counts the step: every block has read it by then.  The
@@ -394,23 +449,46 @@ dgl_status check_tensor(const dgl_adamw_tensor& t, int bits) {
   return DGL_OK;
 }
 
-// Whether every address of a tensor allows units of eight elements, of up to `most` bytes.
-bool takes_units(const dgl_adamw_tensor& t, int bits, uintptr_t most) {
-  const uintptr_t f32 = most, state = bits == 8 ? 8 : f32;
-  return aligned(t.param, t.param_dtype == DGL_OUT_F32 ? f32 : 16) && aligned(t.grad, t.grad_dtype == DGL_OUT_F32 ? f32 : 16) &&
-         aligned(t.master, f32) && aligned(t.exp_avg, state) && aligned(t.exp_avg_sq, state);
+// A tensor's types, if every address allows units of eight elements: 32 bytes of
+// fp32, 16 of bf16, 8 of 8-bit states.
+int types_of(const dgl_adamw_tensor& t) {
+  return (t.param_dtype == DGL_OUT_F32 ? PARAM_F32 : 0) | (t.grad_dtype == DGL_OUT_F32 ? GRAD_F32 : 0) |
+         (t.master ? MASTER : 0);
+}
+bool takes_units(const dgl_adamw_tensor& t, int bits) {
+  const uintptr_t state = bits == 8 ? 8 : 32;
+  return aligned(t.param, t.param_dtype == DGL_OUT_F32 ? 32 : 16) && aligned(t.grad, t.grad_dtype == DGL_OUT_F32 ? 32 : 16) &&
+         aligned(t.master, 32) && aligned(t.exp_avg, state) && aligned(t.exp_avg_sq, state);
 }
 
-template <int CAP>
-dgl_status launch(const AdamScalars& s, const AdamTensor* t, int bits, int num_sms, cudaStream_t stream) {
+template <bool EIGHT, int TYPES, int CAP>
+dgl_status launch(const AdamScalars& s, const AdamTensor* t, int num_sms, cudaStream_t stream) {
   AdamTable<CAP> a;
   a.s = s;
   std::copy(t, t + s.count, a.t);
-  const unsigned grid =
-      std::max(1u, std::min(s.chunks, static_cast<uint32_t>(num_sms) * static_cast<uint32_t>(kBlocksPerSm)));
-  const cudaError_t e = bits == 8 ? launch_dependent(adamw_kernel<true, CAP>, grid, kThreads, stream, a)
-                                  : launch_dependent(adamw_kernel<false, CAP>, grid, kThreads, stream, a);
+  const uint32_t resident = static_cast<uint32_t>(num_sms * kBlocksPerSm<EIGHT>);
+  const unsigned grid = std::max(1u, std::min(s.chunks, std::max(resident, s.chunks / kBlockChunks<EIGHT>)));
+  const cudaError_t e = launch_dependent(adamw_kernel<EIGHT, TYPES, CAP>, grid, kThreads, stream, a);
   return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
+}
+
+template <bool EIGHT, int TYPES>
+dgl_status launch(const AdamScalars& s, const AdamTensor* t, int num_sms, cudaStream_t stream) {
+  return s.count <= kFewTensors ? launch<EIGHT, TYPES, kFewTensors>(s, t, num_sms, stream)
+                                : launch<EIGHT, TYPES, kManyTensors>(s, t, num_sms, stream);
+}
+
+template <bool EIGHT>
+dgl_status launch(int types, const AdamScalars& s, const AdamTensor* t, int num_sms, cudaStream_t stream) {
+  switch (types) {
+    case 0: return launch<EIGHT, 0>(s, t, num_sms, stream);
+    case PARAM_F32: return launch<EIGHT, PARAM_F32>(s, t, num_sms, stream);
+    case GRAD_F32: return launch<EIGHT, GRAD_F32>(s, t, num_sms, stream);
+    case PARAM_F32 | GRAD_F32: return launch<EIGHT, PARAM_F32 | GRAD_F32>(s, t, num_sms, stream);
+    case MASTER: return launch<EIGHT, MASTER>(s, t, num_sms, stream);
+    case MASTER | GRAD_F32: return launch<EIGHT, MASTER | GRAD_F32>(s, t, num_sms, stream);
+    default: return launch<EIGHT, ANY_TYPES>(s, t, num_sms, stream);
+  }
 }
 
 dgl_status run_adamw(const dgl_adamw_desc& d, const dgl_adamw_tensor* tensors, int count, cudaStream_t stream) {
@@ -421,9 +499,11 @@ dgl_status run_adamw(const dgl_adamw_desc& d, const dgl_adamw_tensor* tensors, i
   if (!std::isfinite(d.lr) || !(d.eps >= 0.0) || !std::isfinite(d.eps)) return DGL_ERR_ARG;
   if (!aligned(d.steps, 8) || !aligned(d.ticket, 4) || !aligned(d.grad_scale, 4) || !aligned(d.lr_at, 4))
     return DGL_ERR_ALIGN;
+  uint32_t kinds = 0;  // of tensors that there are: bit `types`, or ANY_TYPES where units do not fit
   for (int i = 0; i < count; ++i) {
     const dgl_status st = check_tensor(tensors[i], d.state_bits);
     if (st != DGL_OK) return st;
+    if (tensors[i].n > 0) kinds |= 1u << (takes_units(tensors[i], d.state_bits) ? types_of(tensors[i]) : ANY_TYPES);
   }
   int dev = 0;
   DeviceState* ds = nullptr;
@@ -443,41 +523,36 @@ dgl_status run_adamw(const dgl_adamw_desc& d, const dgl_adamw_tensor* tensors, i
   s.rest2 = static_cast<float>(1.0 - d.beta2);
   s.eps = static_cast<float>(d.eps);
   s.seed = d.seed;
+  const bool eight = d.state_bits == 8;
   AdamTensor table[kManyTensors];
-  int64_t block = 0;
-  int i = 0;
-  do {
-    int64_t chunk = 0;
+  if (kinds == 0) kinds = 1u << ANY_TYPES;  // nothing but a step to count
+  // a launch for each kind, and for each table full; the last counts the step
+  for (int types = 0; kinds != 0 && st == DGL_OK; ++types) {
+    if (!(kinds >> types & 1)) continue;
+    kinds &= ~(1u << types);
+    int64_t block = 0, chunk = 0;
     s.count = 0;
-    for (; i < count && s.count < kManyTensors; ++i) {
+    auto flush = [&](bool last) {
+      s.chunks = static_cast<uint32_t>(chunk);
+      s.ticket = last ? d.ticket : nullptr;
+      st = eight ? launch<true>(types, s, table, ds->num_sms, stream) : launch<false>(types, s, table, ds->num_sms, stream);
+      s.count = 0;
+      chunk = 0;
+    };
+    for (int i = 0; i < count && st == DGL_OK; ++i) {
       const dgl_adamw_tensor& t = tensors[i];
-      const int64_t chunks = (t.n + kChunk - 1) / kChunk;
-      if (chunk + chunks > UINT32_MAX / 2) break;  // (2^40 elements are 2^29 chunks: the first always fits)
-      if (t.n > 0)
-        table[s.count++] = AdamTensor{t.param,
-                                      t.grad,
-                                      t.master,
-                                      t.exp_avg,
-                                      t.exp_avg_sq,
-                                      t.exp_avg_scale,
-                                      t.exp_avg_sq_scale,
-                                      t.n,
-                                      block,
-                                      static_cast<uint32_t>(chunk),
-                                      (t.param_dtype == DGL_OUT_F32 ? PARAM_F32 : 0u) |
-                                          (t.grad_dtype == DGL_OUT_F32 ? GRAD_F32 : 0u) |
-                                          (takes_units(t, d.state_bits, 32)   ? UNITS_32
-                                           : takes_units(t, d.state_bits, 16) ? UNITS_16
-                                                                              : 0u),
-                                      t.weight_decay};
-      chunk += chunks;
+      const int64_t first = block, chunks = (t.n + kChunk - 1) / kChunk;
       block += (t.n + kBlock - 1) / kBlock;
+      if (t.n == 0 || (takes_units(t, d.state_bits) ? types_of(t) : ANY_TYPES) != types) continue;
+      // (a tensor's 2^40 elements are 2^29 chunks)
+      if (s.count == kManyTensors || chunk + chunks > UINT32_MAX / 2) flush(false);
+      table[s.count++] =
+          AdamTensor{t.param,          t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
+                     first, static_cast<uint32_t>(chunk), types_of(t), t.weight_decay};
+      chunk += chunks;
     }
-    s.chunks = static_cast<uint32_t>(chunk);
-    s.ticket = i == count ? d.ticket : nullptr;
-    st = s.count <= kFewTensors ? launch<kFewTensors>(s, table, d.state_bits, ds->num_sms, stream)
-                                : launch<kManyTensors>(s, table, d.state_bits, ds->num_sms, stream);
-  } while (st == DGL_OK && i < count);
+    if (st == DGL_OK) flush(kinds == 0);
+  }
   return st;
 }
 
