@@ -399,7 +399,7 @@ constexpr int kMostChunk = 2048;
 template <class GT, int VEC>
 constexpr int kSumUnits = 16 / (VEC * static_cast<int>(sizeof(GT)));
 template <class GT, int VEC>
-constexpr int kSumAhead = kSumUnits<GT, VEC> == 1 ? 8 : 4;
+constexpr int kSumAhead = kSumUnits<GT, VEC> == 1 ? 8 : kSumUnits<GT, VEC> == 8 ? 2 : 4;
 
 // sum: of a unit.  To an fp32 dW by a reduction in L2, which waits for no load;
 // each element gets one, so that its order is fixed (subnormal sums count as zero there).
