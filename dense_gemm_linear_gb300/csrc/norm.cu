@@ -169,10 +169,10 @@ __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-template <class T, int VEC>
+template <class T, int VEC, bool RING>
 struct RowUnits {
   static constexpr int U = kElems / VEC, kBytes = VEC * static_cast<int>(sizeof(T));
-  static constexpr bool kRing = kBytes >= 4;
+  static constexpr bool kRing = RING && kBytes >= 4;
   Unit<T, VEC> held[kRing ? 1 : U];
   const T* next;   // the lane's first unit of the row to be loaded
   int64_t step;    // elements from one of the group's rows to its next
@@ -236,9 +236,9 @@ struct RowUnits {
 // Rows that a lane has under way and at hand: 160 KB of an SM's shared memory
 // at the residencies below.
 template <class T, int VEC>
-constexpr int kDepth = !RowUnits<T, VEC>::kRing ? 2 : sizeof(T) == 2 ? 4 : 3;
+constexpr int kDepth = VEC * sizeof(T) < 4 ? 2 : sizeof(T) == 2 ? 4 : 3;
 template <class T, int VEC>
-constexpr int kRingBytes = RowUnits<T, VEC>::kRing ? kDepth<T, VEC> * kElems * static_cast<int>(sizeof(T)) : 0;  // a thread
+constexpr int kRingBytes = VEC * sizeof(T) < 4 ? 0 : kDepth<T, VEC> * kElems * static_cast<int>(sizeof(T));  // a thread
 
 // The lanes of a group that is whole warps; `groups` in the block.
 __device__ __forceinline__ void group_sync(int group, int lanes, int groups) {
@@ -250,6 +250,19 @@ __device__ __forceinline__ void group_sync(int group, int lanes, int groups) {
 // none.  In units where its address allows: read element by element, a warp's 32 lanes touch 32
 // sectors for each of 32 loads, and a grid's blocks spent half their time on that.
 template <int VEC>
+__device__ __forceinline__ void unit_columns(const void* v, int f32, int units_fit, float fill, int at, float (&e)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) e[j] = fill;
+  if (!v) return;
+  if (units_fit) {
+    if (f32) unpack<float, VEC>(load_unit<float, VEC>(static_cast<const float*>(v) + at), e);
+    else unpack<bf16, VEC>(load_unit<bf16, VEC>(static_cast<const bf16*>(v) + at), e);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) e[j] = element(v, f32, at + j);
+  }
+}
+template <int VEC>
 __device__ __forceinline__ void lane_columns(const void* v, int f32, int units_fit, float fill, int lane, int lanes,
                                              int units, float2 (&f)[kElems / 2]) {
 #pragma unroll
@@ -258,15 +271,7 @@ __device__ __forceinline__ void lane_columns(const void* v, int f32, int units_f
     float e[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) e[j] = fill;
-    if (v && at < units) {
-      if (units_fit) {
-        if (f32) unpack<float, VEC>(load_unit<float, VEC>(static_cast<const float*>(v) + at * VEC), e);
-        else unpack<bf16, VEC>(load_unit<bf16, VEC>(static_cast<const bf16*>(v) + at * VEC), e);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) e[j] = element(v, f32, at * VEC + j);
-      }
-    }
+    if (at < units) unit_columns<VEC>(v, f32, units_fit, fill, at * VEC, e);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) put(f, i * VEC + j, e[j]);
   }
@@ -287,15 +292,16 @@ __device__ __forceinline__ void store_row(T* row, int apart, int count, const fl
 
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
 // apart.
-// THREADS: the most in a block (1024: the weight does not fit beside a row in 64
-// registers and is read again for each row, from L1).  WARPS: a row has several
-// warps, which are the block.
+// THREADS: the most in a block.  1024, of rows past 8192: the weight does not fit
+// beside a row in 64 registers and is read again for each row, from L1, which it
+// has to itself: the next row waits in registers and not in shared memory.
+// WARPS: a row has several warps, which are the block.
 template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr bool kKeep = THREADS <= 512;
-  constexpr int DEPTH = kDepth<XT, VEC>;
+  constexpr int DEPTH = kKeep ? kDepth<XT, VEC> : 2;
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float2 red[2][32];
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   const float inv_d = 1.0f / static_cast<float>(a.d);
 
   const int count = lane < units ? (units - lane + lanes - 1) / lanes : 0, apart = lanes * VEC;
-  RowUnits<XT, VEC> rows;
+  RowUnits<XT, VEC, kKeep> rows;
   rows.begin(static_cast<const XT*>(a.x), a.ldx, row, groups, lane, lanes, units, ring, DEPTH);
   int ahead = nrows - row;  // rows from the next to be loaded on, over all groups
 #pragma unroll
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
     __syncthreads();
   }
 
-  float2 w[kElems / 2], b[kElems / 2];
+  float2 w[kKeep ? kElems / 2 : 1], b[kKeep ? kElems / 2 : 1];
   if constexpr (kKeep) {
     lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
     lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
@@ -379,13 +385,23 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
     }
     const float rstd = reciprocal_root(fmaf(q, inv_d, a.eps));
     if (row >= nrows) continue;
-    if constexpr (!kKeep) {
-      lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, w);
-      lane_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, lane, lanes, units, b);
-    }
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < kElems / 2; ++i) f[i] = fma2(scaled<XT>(f[i], mean, rstd), w[i], b[i]);
-    store_row<XT, VEC>(y, apart, count, f);
+      for (int i = 0; i < kElems / 2; ++i) f[i] = fma2(scaled<XT>(f[i], mean, rstd), w[i], b[i]);
+      store_row<XT, VEC>(y, apart, count, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kElems / VEC; ++i) {
+        if (i >= count) continue;
+        const int at = (lane + i * lanes) * VEC;
+        float e[VEC], w_unit[VEC], b_unit[VEC];
+        unit_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, at, w_unit);
+        unit_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, at, b_unit);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) e[j] = fmaf((get(f, i * VEC + j) - mean) * rstd, w_unit[j], b_unit[j]);
+        store_unit<XT, VEC>(y + i * apart, e);
+      }
+    }
     if (lane == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -459,7 +475,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
   const bool want_w = a.part != nullptr;
 
   const int count = lane < units ? (units - lane + lanes - 1) / lanes : 0, apart = lanes * VEC;
-  RowUnits<XT, VEC> rows_x, rows_g;
+  RowUnits<XT, VEC, true> rows_x, rows_g;
   rows_x.begin(static_cast<const XT*>(a.x), a.ldx, row, groups, lane, lanes, units, ring, kKeep ? DEPTH : 0);
   rows_g.begin(static_cast<const XT*>(a.dy), a.lddy, row, groups, lane, lanes, units,
                ring + kRingBytes<XT, VEC> * blockDim.x, kKeep ? DEPTH : 0);
@@ -800,9 +816,10 @@ cudaError_t launch_forward(const NormArgs& a, int num_sms, cudaStream_t stream) 
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> resident[33] = {};  // blocks of so many warps on an SM
   const auto kernel = norm_forward_kernel<X, VEC, THREADS, WARPS>;
-  const int threads = threads_for(a.lanes), smem = kRingBytes<X, VEC> * threads;
-  cudaError_t e = set_smem_attr_once(kernel, kRingBytes<X, VEC> * THREADS, done);
-  if (e != cudaSuccess) return e;
+  constexpr int kRing = THREADS <= 512 ? kRingBytes<X, VEC> : 0;
+  const int threads = threads_for(a.lanes), smem = kRing * threads;
+  cudaError_t e = cudaSuccess;
+  if (kRing > 0 && (e = set_smem_attr_once(kernel, kRing * THREADS, done)) != cudaSuccess) return e;
   int fit = resident[threads / 32].load(std::memory_order_relaxed);
   if (fit == 0) {
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem)) != cudaSuccess) return e;
