@@ -2,7 +2,8 @@
 
 The helpers check their arguments, allocate what is not passed in with torch,
 and make one call of the library on torch's current stream.  The tensors are on
-the current device, where the library launches.
+the current device, where the library launches.  What a call checks of its tensors'
+types, extents and strides is kept for the next call with the same.
 """
 from __future__ import annotations
 
@@ -10,22 +11,31 @@ import functools
 
 import torch
 
-from . import OUT_BF16, OUT_F32, EmbedDesc, _check, dgl_embedding_workspace, load_library
-from .head import _byref, _not_here, _on_stream, _packed, _rows
-from .norm import _matrix
-
-_TYPES = {OUT_BF16: torch.bfloat16, OUT_F32: torch.float32}
+from . import OUT_BF16, EmbedDesc, _check, dgl_embedding_workspace, load_library
+from .head import _byref, _on_stream
+from .norm import _TYPES, _buffer, _matrix, _meta, _vector
 
 
-def _count(tokens):
-    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 1:
+def _count(tokens, device):
+    if tokens is None or len(tokens[2]) != 1:
         raise TypeError("tokens must be a 1-D int64 CUDA tensor")
-    return tokens.shape[0]
+    _vector(tokens, "tokens", device, tokens[2][0], torch.int64)
+    return tokens[2][0]
 
 
-@functools.lru_cache(maxsize=256)
-def _workspace_bytes(T, V, d, w_dtype, y_dtype):
-    return dgl_embedding_workspace(EmbedDesc(T=T, V=V, d=d, w_dtype=w_dtype, y_dtype=y_dtype))
+@functools.lru_cache(maxsize=1024)
+def _lookup(device, tokens, W, out_dtype, out):
+    w_code, ldw = _matrix(W, "W", device)
+    T, d = _count(tokens, device), W[2][1]
+    if out is None:
+        y_code = w_code if out_dtype is None else out_dtype
+        if y_code not in _TYPES:
+            raise ValueError("out_dtype must be OUT_BF16 or OUT_F32")
+        return w_code, ldw, y_code, d
+    y_code, ldy = _matrix(out, "out", device, (T, d))
+    if out_dtype is not None and out_dtype != y_code:
+        raise TypeError("out is not of out_dtype")
+    return w_code, ldw, y_code, ldy
 
 
 def embedding(tokens, W, *, scale=1.0, ignore_index=-100, out_dtype=None, out=None, stream=None):
@@ -39,28 +49,35 @@ def embedding(tokens, W, *, scale=1.0, ignore_index=-100, out_dtype=None, out=No
     if stream is not None:
         return _on_stream(stream, lambda: embedding(tokens, W, scale=scale, ignore_index=ignore_index,
                                                     out_dtype=out_dtype, out=out), tokens, W, out)
-    T = _count(tokens)
-    w_code, V, d = _matrix(W, "W")
     device = torch.cuda.current_device()
-    at = _packed(tokens, "tokens", torch.int64, (T,), device)
-    ldw = _rows(W, "W", W.dtype, (V, d), device)
+    w_code, ldw, y_code, ldy = _lookup(device, _meta(tokens), _meta(W), out_dtype, _meta(out))
+    (T,), (V, d) = tokens.shape, W.shape
     if out is None:
-        y_code = w_code if out_dtype is None else out_dtype
-        if y_code not in _TYPES:
-            raise ValueError("out_dtype must be OUT_BF16 or OUT_F32")
         out = torch.empty((T, d), dtype=_TYPES[y_code], device=device)
-        ldy = d
-    else:
-        y_code = _matrix(out, "out")[0]
-        if out_dtype is not None and out_dtype != y_code:
-            raise TypeError("out is not of out_dtype")
-        ldy = _rows(out, "out", out.dtype, (T, d), device)
-    e = EmbedDesc(T, V, d, at, ignore_index, W.data_ptr(), None, ldw, out.data_ptr(), None, ldy, scale=scale,
+    e = EmbedDesc(T, V, d, tokens.data_ptr(), ignore_index, W.data_ptr(), None, ldw, out.data_ptr(), None, ldy, scale=scale,
                   w_dtype=w_code, y_dtype=y_code)
     st = load_library().dgl_embedding(_byref(e), torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_embedding")
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _gradient(device, tokens, dY, V, dW, dw_dtype, accumulate):
+    y_code, ldy = _matrix(dY, "dY", device)
+    T, d = _count(tokens, device), dY[2][1]
+    if dY[2][0] != T:
+        raise ValueError(f"dY must have shape {(T, d)}")
+    if dw_dtype not in _TYPES:
+        raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate adds to the fp32 dW that is passed in")
+        ldw = d
+    else:
+        dw_dtype, ldw = _matrix(dW, "dW", device, (V, d))
+    size = dgl_embedding_workspace(EmbedDesc(T=T, V=V, d=d, w_dtype=dw_dtype, y_dtype=y_code))
+    return y_code, ldy, dw_dtype, ldw, max(1, size)
 
 
 def embedding_grad(tokens, dY, V, *, scale=1.0, ignore_index=-100, dW=None, dw_dtype=OUT_BF16, accumulate=False,
@@ -78,30 +95,18 @@ def embedding_grad(tokens, dY, V, *, scale=1.0, ignore_index=-100, dW=None, dw_d
         return _on_stream(stream, lambda: embedding_grad(
             tokens, dY, V, scale=scale, ignore_index=ignore_index, dW=dW, dw_dtype=dw_dtype, accumulate=accumulate,
             workspace=workspace), tokens, dY, dW, workspace)
-    T = _count(tokens)
-    y_code, _, d = _matrix(dY, "dY")
     device = torch.cuda.current_device()
-    at = _packed(tokens, "tokens", torch.int64, (T,), device)
-    ldy = _rows(dY, "dY", dY.dtype, (T, d), device)
-    if dw_dtype not in _TYPES:
-        raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
+    y_code, ldy, dw_dtype, ldw, size = _gradient(device, _meta(tokens), _meta(dY), V, _meta(dW), dw_dtype, accumulate)
+    T, d = dY.shape
     if dW is None:
-        if accumulate:
-            raise ValueError("accumulate adds to the fp32 dW that is passed in")
         dW = torch.empty((V, d), dtype=_TYPES[dw_dtype], device=device)
-        ldw = d
-    else:
-        dw_dtype = _matrix(dW, "dW")[0]
-        ldw = _rows(dW, "dW", dW.dtype, (V, d), device)
     if workspace is None:
-        workspace = torch.empty(max(1, _workspace_bytes(T, V, d, dw_dtype, y_code)), dtype=torch.uint8, device=device)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
-        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device:
-            _not_here(workspace, "workspace", device)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-    e = EmbedDesc(T, V, d, at, ignore_index, None, dW.data_ptr(), ldw, None, dY.data_ptr(), ldy, workspace.data_ptr(),
-                  workspace.nbytes, scale, dw_dtype, y_code, 1 if accumulate else 0)
+        _buffer(workspace, device)
+        size = workspace.nbytes
+    e = EmbedDesc(T, V, d, tokens.data_ptr(), ignore_index, None, dW.data_ptr(), ldw, None, dY.data_ptr(), ldy,
+                  workspace.data_ptr(), size, scale, dw_dtype, y_code, 1 if accumulate else 0)
     st = load_library().dgl_embedding_grad(_byref(e), torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_embedding_grad")

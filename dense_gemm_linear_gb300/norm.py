@@ -2,7 +2,9 @@
 
 The helpers check their arguments, allocate what is not passed in with torch,
 and make one call of the library on torch's current stream.  The tensors are on
-the current device, where the library launches.
+the current device, where the library launches.  On a few rows the kernels take
+less time than this module does, so what a call checks of its tensors' types,
+extents and strides is kept for the next call with the same.
 """
 from __future__ import annotations
 
@@ -11,46 +13,92 @@ import functools
 import torch
 
 from . import OUT_BF16, OUT_F32, NormDesc, _check, dgl_layer_norm_workspace, load_library
-from .head import _byref, _not_here, _on_stream, _packed, _rows
+from .head import _byref, _on_stream
 
 _F32 = torch.float32
 _CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+_TYPES = {OUT_BF16: torch.bfloat16, OUT_F32: torch.float32}
 
 
-def _code(t, name):
-    code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+def _meta(t):
+    """What is checked of a tensor (None: not given)."""
+    if t is None:
+        return None
+    try:
+        return t.get_device(), t.dtype, t.shape, t.stride()
+    except AttributeError:
+        raise TypeError(f"a CUDA tensor is expected, got {type(t).__name__}") from None
+
+
+def _here(meta, name, device):
+    if meta is None or meta[0] < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if meta[0] != device:
+        raise ValueError(f"{name} is on cuda:{meta[0]}, but the current device is cuda:{device}")
+
+
+def _type(meta, name):
+    code = _CODES.get(meta[1])
     if code is None:
-        raise TypeError(f"{name} must be a bf16 or fp32 CUDA tensor")
+        raise TypeError(f"{name} must be bf16 or fp32, got {meta[1]}")
     return code
 
 
-def _matrix(t, name):
-    """The type code and the extents of a matrix."""
-    code = _code(t, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    return code, *t.shape
+def _matrix(meta, name, device, shape=None, dtype=None):
+    """Checks a matrix whose rows are contiguous; returns its type code and row pitch in elements."""
+    _here(meta, name, device)
+    code = _type(meta, name)
+    if dtype is not None and meta[1] != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {meta[1]}")
+    if len(meta[2]) != 2 or (shape is not None and meta[2] != shape):
+        raise ValueError(f"{name} must have " + ("two dimensions" if shape is None else f"shape {tuple(shape)}"))
+    (rows, cols), (pitch, step) = meta[2], meta[3]
+    if step != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows <= 1:
+        return code, cols
+    if pitch < cols:  # a row repeated by expand() has pitch 0, which the C call reads as packed rows
+        raise ValueError(f"the rows of {name} must not overlap")
+    return code, pitch
 
 
-def _vectors(d, device, **vectors):
-    """Addresses of the weight and the bias (None where there is none), and their type."""
-    at, code = [], OUT_F32
-    first = None
-    for name, t in vectors.items():
-        if t is None:
-            at.append(None)
+def _vector(meta, name, device, length, dtype):
+    """Checks a contiguous vector."""
+    _here(meta, name, device)
+    if meta[1] != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {meta[1]}")
+    if tuple(meta[2]) != (length,) or (length > 1 and meta[3] != (1,)):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {(length,)}")
+
+
+def _buffer(workspace, device):
+    """Checks a scratch buffer."""
+    meta = _meta(workspace)
+    _here(meta, "workspace", device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+
+
+def _columns(device, d, weight, bias):
+    """The type code of the weight and the bias."""
+    code = OUT_F32
+    for meta, name in ((weight, "weight"), (bias, "bias")):
+        if meta is None:
             continue
-        code = _code(t, name)
-        if first is not None and first.dtype != t.dtype:
-            raise TypeError("weight and bias must have the same type")
-        first = t
-        at.append(_packed(t, name, t.dtype, (d,), device))
-    return at, code
+        _here(meta, name, device)
+        code = _type(meta, name)
+        _vector(meta, name, device, d, meta[1])
+    if weight is not None and bias is not None and weight[1] != bias[1]:
+        raise TypeError("weight and bias must have the same type")
+    return code
 
 
-@functools.lru_cache(maxsize=256)
-def _workspace_bytes(rows, d):
-    return dgl_layer_norm_workspace(NormDesc(rows=rows, d=d))
+@functools.lru_cache(maxsize=1024)
+def _forward(device, x, weight, bias, out):
+    code, ldx = _matrix(x, "x", device)
+    w_code = _columns(device, x[2][1], weight, bias)
+    ldy = x[2][1] if out is None else _matrix(out, "out", device, x[2], x[1])[1]
+    return code, ldx, w_code, ldy
 
 
 def layer_norm(x, weight=None, bias=None, *, eps=1e-5, out=None, stream=None):
@@ -63,37 +111,52 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, out=None, stream=None):
     """
     if stream is not None:
         return _on_stream(stream, lambda: layer_norm(x, weight, bias, eps=eps, out=out), x, weight, bias, out)
-    code, rows, d = _matrix(x, "x")
     device = torch.cuda.current_device()
-    ldx = _rows(x, "x", x.dtype, (rows, d), device)
-    (at_w, at_b), w_code = _vectors(d, device, weight=weight, bias=bias)
+    code, ldx, w_code, ldy = _forward(device, _meta(x), _meta(weight), _meta(bias), _meta(out))
+    rows, d = x.shape
     if out is None:
         out = torch.empty((rows, d), dtype=x.dtype, device=device)
-        ldy = d
-    else:
-        ldy = _rows(out, "out", x.dtype, (rows, d), device)
     mean = torch.empty(rows, dtype=_F32, device=device)
     rstd = torch.empty(rows, dtype=_F32, device=device)
-    n = NormDesc(rows, d, x.data_ptr(), ldx, at_w, at_b, out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(),
-                 eps=eps, x_dtype=code, w_dtype=w_code)
+    n = NormDesc(rows, d, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(),
+                 None if bias is None else bias.data_ptr(), out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), eps=eps,
+                 x_dtype=code, w_dtype=w_code)
     st = load_library().dgl_layer_norm(_byref(n), torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_layer_norm")
     return out, mean, rstd
 
 
-def _sums(given, name, d, want, dw_dtype, accumulate, device):
-    """dweight or dbias: the tensor, made when it is None, or None when it is not wanted."""
-    if not want:
-        if given is not None:
+@functools.lru_cache(maxsize=1024)
+def _gradient(device, dy, x, mean, rstd, weight, need_dx, need_dw, need_db, dweight, dbias, dw_dtype, accumulate):
+    code, ldx = _matrix(x, "x", device)
+    rows, d = x[2]
+    lddy = _matrix(dy, "dy", device, x[2], x[1])[1]
+    _vector(mean, "mean", device, rows, _F32)
+    _vector(rstd, "rstd", device, rows, _F32)
+    w_code = _columns(device, d, weight, None)
+    if not (need_dx or need_dw or need_db):
+        raise ValueError("a call computes dx, dweight, dbias or some of them")
+    if accumulate and not (need_dw or need_db):
+        raise ValueError("accumulate adds to dweight and dbias, which are not asked for")
+    if dw_dtype not in _TYPES:
+        raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
+    given = [(m, name) for m, name in ((dweight, "dweight"), (dbias, "dbias")) if m is not None]
+    for meta, name in given:
+        _here(meta, name, device)
+        dw_dtype = _type(meta, name)
+    for meta, name, need in ((dweight, "dweight", need_dw), (dbias, "dbias", need_db)):
+        if meta is None:
+            if need and accumulate:
+                raise ValueError(f"accumulate adds to the fp32 {name} that is passed in")
+            continue
+        if not need:
             raise ValueError(f"{name} is given but not asked for")
-        return None
-    if given is None:
-        if accumulate:
-            raise ValueError(f"accumulate adds to the fp32 {name} that is passed in")
-        return torch.empty(d, dtype=_F32 if dw_dtype == OUT_F32 else torch.bfloat16, device=device)
-    _packed(given, name, given.dtype, (d,), device)
-    return given
+        if meta[1] != _TYPES[dw_dtype]:
+            raise TypeError("dweight and dbias must have the same type")
+        _vector(meta, name, device, d, meta[1])
+    size = max(1, dgl_layer_norm_workspace(NormDesc(rows=rows, d=d))) if need_dw or need_db else 0
+    return code, ldx, lddy, w_code, dw_dtype, size
 
 
 def layer_norm_grad(dy, x, mean, rstd, weight=None, *, need_dx=True, need_dw=True, need_db=True, dweight=None,
@@ -110,40 +173,27 @@ def layer_norm_grad(dy, x, mean, rstd, weight=None, *, need_dx=True, need_dw=Tru
             dy, x, mean, rstd, weight, need_dx=need_dx, need_dw=need_dw, need_db=need_db, dweight=dweight, dbias=dbias,
             dw_dtype=dw_dtype, accumulate=accumulate, workspace=workspace),
             dy, x, mean, rstd, weight, dweight, dbias, workspace)
-    code, rows, d = _matrix(x, "x")
     device = torch.cuda.current_device()
-    ldx = _rows(x, "x", x.dtype, (rows, d), device)
-    lddy = _rows(dy, "dy", x.dtype, (rows, d), device)
-    at_mean = _packed(mean, "mean", _F32, (rows,), device)
-    at_rstd = _packed(rstd, "rstd", _F32, (rows,), device)
-    (at_w,), w_code = _vectors(d, device, weight=weight)
-    if not (need_dx or need_dw or need_db):
-        raise ValueError("a call computes dx, dweight, dbias or some of them")
-    if dw_dtype not in (OUT_BF16, OUT_F32):
-        raise ValueError("dw_dtype must be OUT_BF16 or OUT_F32")
-    if accumulate and not (need_dw or need_db):
-        raise ValueError("accumulate adds to dweight and dbias, which are not asked for")
-    for name, t in (("dweight", dweight), ("dbias", dbias)):
-        if t is not None:
-            dw_dtype = _code(t, name)
-    dweight = _sums(dweight, "dweight", d, need_dw, dw_dtype, accumulate, device)
-    dbias = _sums(dbias, "dbias", d, need_db, dw_dtype, accumulate, device)
-    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
-        raise TypeError("dweight and dbias must have the same type")
+    code, ldx, lddy, w_code, dw_dtype, size = _gradient(
+        device, _meta(dy), _meta(x), _meta(mean), _meta(rstd), _meta(weight), need_dx, need_dw, need_db, _meta(dweight),
+        _meta(dbias), dw_dtype, accumulate)
+    rows, d = x.shape
     dx = torch.empty((rows, d), dtype=x.dtype, device=device) if need_dx else None
-    size = 0
-    if need_dw or need_db:
+    if need_dw and dweight is None:
+        dweight = torch.empty(d, dtype=_TYPES[dw_dtype], device=device)
+    if need_db and dbias is None:
+        dbias = torch.empty(d, dtype=_TYPES[dw_dtype], device=device)
+    at = None
+    if size:
         if workspace is None:
-            workspace = torch.empty(max(1, _workspace_bytes(rows, d)), dtype=torch.uint8, device=device)
+            workspace = torch.empty(size, dtype=torch.uint8, device=device)
         else:
-            if not isinstance(workspace, torch.Tensor) or workspace.get_device() != device:
-                _not_here(workspace, "workspace", device)
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous CUDA tensor")
-        size = workspace.nbytes
-    n = NormDesc(rows, d, x.data_ptr(), ldx, at_w, None, None, 0, at_mean, at_rstd, dy.data_ptr(), lddy,
-                 dx.data_ptr() if need_dx else None, d, dweight.data_ptr() if need_dw else None,
-                 dbias.data_ptr() if need_db else None, workspace.data_ptr() if size else None, size, 0.0, code, w_code,
+            _buffer(workspace, device)
+            size = workspace.nbytes
+        at = workspace.data_ptr()
+    n = NormDesc(rows, d, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(), None, None, 0, mean.data_ptr(),
+                 rstd.data_ptr(), dy.data_ptr(), lddy, dx.data_ptr() if need_dx else None, d,
+                 dweight.data_ptr() if need_dw else None, dbias.data_ptr() if need_db else None, at, size, 0.0, code, w_code,
                  dw_dtype, 1 if accumulate else 0)
     st = load_library().dgl_layer_norm_grad(_byref(n), torch._C._cuda_getCurrentRawStream(device))
     if st:

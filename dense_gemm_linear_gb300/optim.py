@@ -7,10 +7,17 @@ import torch
 
 from . import ADAMW_BLOCK, AdamWDesc, AdamWTensor, _check, load_library
 from .head import _not_here, _packed
-from .norm import _code
+from .norm import _CODES
 
 _F32 = torch.float32
 _STATES = {32: (_F32, _F32), 8: (torch.float8_e4m3fn, torch.float8_e5m2)}
+
+
+def _code(t, name):
+    code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError(f"{name} must be a bf16 or fp32 CUDA tensor")
+    return code
 
 
 def _flat(t, name, device):
