@@ -5,20 +5,20 @@
 //
 // One launch takes hundreds of tensors: their addresses travel in the kernel's
 // parameters, so a call uploads nothing and a captured one stays valid.  The
-// tensors are cut into chunks of 2048 elements, of which a block takes a
-// few, 8 neighbouring elements a thread.  Every element is read and written
-// once: the kernel is bound by HBM (28 bytes an element with fp32 weights,
-// gradients and states, 14 with 8-bit states and bf16 gradients), and with 8-bit states nearly as
+// tensors are cut into chunks of 2048 elements, of which a block takes a few, 8
+// neighbouring elements a thread.  Every element is read and written once: the
+// kernel is bound by HBM (28 bytes an element with fp32 weights, gradients and
+// states, 14 with 8-bit states and bf16 gradients), and with 8-bit states nearly as
 // much by its arithmetic.
 //
 // 8-bit states.  A block of 128 elements of a tensor has a power of two as its
 // scale, so that scaling is exact; m is stored in E4M3 and v in E5M2 (its square
-// root, which the update divides by, has then E4M3's relative step, and the
-// 31 binades of v reach 15 of the root).  A step changes v by a thousandth
-// where neighbouring codes are an eighth to a quarter apart: rounded to nearest, v would
-// stay where its first few steps left it while 1 - b2^t grows, and updates
-// would become many times too large.  Values are therefore rounded up or down
-// at random, in proportion, which keeps the averages' expectations.  The random bits are
+// root, which the update divides by, has then E4M3's relative step, and the 31
+// binades of v reach 15 of the root).  A step changes v by a thousandth where
+// neighbouring codes are an eighth to a quarter apart: rounded to nearest, v would
+// stay where its first few steps left it while 1 - b2^t grows, and updates would
+// become many times too large.  Values are therefore rounded up or down at random,
+// in proportion, which keeps the averages' expectations.  The random bits are
 // SplitMix64's (Steele, Lea and Flood 2014) of seed, step and element.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,13 +46,14 @@ constexpr int kEach = 8;  // neighbouring elements that a thread takes
 constexpr int kThreads = 256;
 constexpr int kChunk = kEach * kThreads;
 // With 8-bit states the arithmetic bounds the kernel and its latency asks for
-// warps: five blocks an SM, at 48 registers (304 M elements: 793 us; four blocks 821, three with the loads of two chunks under way 809).
+// warps: five blocks an SM, at 48 registers (304 M elements: 793 us; four blocks
+// 821, three with the loads of two chunks under way 809).
 template <bool EIGHT>
 constexpr int kBlocksPerSm = EIGHT ? 5 : 4;
-// Chunks that a block takes, where there are enough for many blocks: blocks that end and
-// make room spread the work better over SMs of unequal speed than ones that stay (304 M
-// elements, 32 bits: 1418 us with a resident grid, 1318 so), but each begins
-// with what its elements share.
+// Chunks that a block takes, where there are enough for many blocks: blocks that
+// end and make room spread the work better over SMs of unequal speed than ones that
+// stay (304 M elements, 32 bits: 1418 us with a resident grid, 1318 so), but each
+// begins with what its elements share.
 template <bool EIGHT>
 constexpr uint32_t kBlockChunks = EIGHT ? 32 : 8;
 
@@ -296,16 +297,16 @@ __device__ __forceinline__ float quotient(float m, float v, float root, float ep
   return m * q;
 }
 
-// TYPES: the tensors' PARAM_F32, GRAD_F32 and MASTER, which are the same for all of a
-// launch and whose addresses all allow units of 8 elements; or ANY_TYPES: each its own.
+// TYPES: the tensors' PARAM_F32, GRAD_F32 and MASTER, which are the same for all of
+// a launch and whose addresses all allow units of 8 elements; or ANY_TYPES: each
+// its own.
 template <bool EIGHT, int TYPES, int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<EIGHT>) adamw_kernel(const __grid_constant__ AdamTable<CAP> a) {
   griddep_wait();
   griddep_launch_dependents();
   const AdamScalars& s = a.s;
-  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
-  // (By each thread: by one for its block the others waited longer than this
-  // takes, 816 -> 934 us.)
+  // lr / (1 - b1^t), 1 / sqrt(1 - b2^t) (By each thread: by one for its block the
+  // others waited longer than this takes, 816 -> 934 us.)
   const int64_t steps = *s.steps + 1;
   const float grad_scale = s.grad_scale ? *s.grad_scale : 1.0f;
   const float lr = s.lr_at ? *s.lr_at : s.lr;

@@ -4,7 +4,7 @@
 //   y  = h w + b
 //   dx = rstd (u - mean_j u - h mean_j (u h))
 //   dw = sum_rows dy h,  db = sum_rows dy
-// Every kernel reads its matrices once and holds a row in registers, kElems
+// Rows of up to 16384 elements are read once and held in registers, kElems
 // elements a thread: the threads of a row (its lanes) are part of a warp, a warp,
 // or a block of up to 1024.  A lane keeps the same columns from row to row, so the
 // weight stays in its registers and the sums of dw and db are its own.  All sums
@@ -126,13 +126,13 @@ __device__ __forceinline__ float2 scaled(float2 x, float mean, float rstd) {
   else return mul2(add2(x, both(-mean)), both(rstd));
 }
 
-// A lane's units of a row, on their way from memory.  Units of 4 bytes or more
-// pass through shared memory: a lane copies its own units of DEPTH - 1 rows
-// ahead (cp.async) and reads them back itself, so nothing synchronises, no register
-// waits and far more is in flight than registers would hold.  bf16 rows off
-// 4 bytes are held in registers, one row ahead.  Forward, 10240 x 2048 bf16:
-// 23.4 us with one row ahead in registers, 16.4 so, 18.7 with one bulk copy a row, whose
-// arrival and release cost more instructions than the copies of 16 bytes.
+// A lane's units of a row, on their way from memory.  Units of 4 bytes or more pass
+// through shared memory: a lane copies its own units of DEPTH - 1 rows ahead
+// (cp.async) and reads them back itself, so nothing synchronises, no register waits
+// and far more is in flight than registers would hold.  bf16 rows off 4 bytes are
+// held in registers, one row ahead.  Forward, 10240 x 2048 bf16: 23.4 us with one
+// row ahead in registers, 16.4 so, 18.7 with one bulk copy a row, whose arrival and
+// release cost more instructions than the copies of 16 bytes.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   if constexpr (BYTES == 16)
@@ -213,7 +213,8 @@ struct RowUnits {
       if (in == end) in = first;
     } else {
 #pragma unroll
-      for (int i = 0; i < U; ++i) held[i] = exists && i < count ? load_unit_once<T, VEC>(next + i * apart) : Unit<T, VEC>{};
+      for (int i = 0; i < U; ++i)
+        held[i] = exists && i < count ? load_unit_once<T, VEC>(next + i * apart) : Unit<T, VEC>{};
     }
     next += step;
   }
@@ -247,10 +248,12 @@ __device__ __forceinline__ void group_sync(int group, int lanes, int groups) {
 }
 
 // The same columns of a vector (the weight or the bias); `fill` where there are
-// none.  In units where its address allows: read element by element, a warp's 32 lanes touch 32
-// sectors for each of 32 loads, and a grid's blocks spent half their time on that.
+// none.  In units where its address allows: read element by element, a warp's 32
+// lanes touch 32 sectors for each of 32 loads, and a grid's blocks spent half their
+// time on that.
 template <int VEC>
-__device__ __forceinline__ void unit_columns(const void* v, int f32, int units_fit, float fill, int at, float (&e)[VEC]) {
+__device__ __forceinline__ void unit_columns(const void* v, int f32, int units_fit, float fill, int at,
+                                             float (&e)[VEC]) {
 #pragma unroll
   for (int j = 0; j < VEC; ++j) e[j] = fill;
   if (!v) return;
@@ -291,10 +294,9 @@ __device__ __forceinline__ void store_row(T* row, int apart, int count, const fl
 }
 
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
-// apart.
-// THREADS: the most in a block.  1024, of rows past 8192: the weight does not fit
-// beside a row in 64 registers and is read again for each row, from L1, which it
-// has to itself: the next row waits in registers and not in shared memory.
+// apart. THREADS: the most in a block.  1024, of rows past 8192: the weight does
+// not fit beside a row in 64 registers and is read again for each row, from L1,
+// which it has to itself: the next row waits in registers and not in shared memory.
 // WARPS: a row has several warps, which are the block.
 template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
@@ -438,7 +440,8 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
     }
     const float rstd = reciprocal_root(block_sum(q, red) / static_cast<float>(a.d) + a.eps);
     for (int i = threadIdx.x; i < a.d; i += kSlowThreads)
-      y[i] = from_float<XT>(fmaf((to_float(x[i]) - mean) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f, a.b ? element(a.b, a.w_f32, i) : 0.0f));
+      y[i] = from_float<XT>(fmaf((to_float(x[i]) - mean) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f,
+                                 a.b ? element(a.b, a.w_f32, i) : 0.0f));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -446,14 +449,13 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
   }
 }
 
-// Backward.  As forward, with x and dy of a row; mean_j u and mean_j (u h) take
-// one barrier a row.  The lanes' sums of dw and db leave as a row of `part` for
-// each block.
-// THREADS 512: a block of several groups fills an SM by itself, so that `part`
-// has as many rows as there are SMs; the sums are in registers and the block's
-// groups join theirs in shared memory.  THREADS 1024 (rows past 8192, one group): the
-// sums are in shared memory, which only the lane itself reads and writes, and
-// nothing is loaded ahead.
+// Backward.  As forward, with x and dy of a row; mean_j u and mean_j (u h) take one
+// barrier a row.  The lanes' sums of dw and db leave as a row of `part` for each
+// block. THREADS 512: a block of several groups fills an SM by itself, so that
+// `part` has as many rows as there are SMs; the sums are in registers and the
+// block's groups join theirs in shared memory.  THREADS 1024 (rows past 8192, one
+// group): the sums are in shared memory, which only the lane itself reads and
+// writes, and nothing is loaded ahead.
 template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
@@ -686,9 +688,9 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
   a.part[(blockIdx.y * 2 + 1) * static_cast<int64_t>(a.d) + col] = db;
 }
 
-// Sums of the rows of `part`, in a fixed order: 32 threads a column, each a
-// range of rows, then the ranges in order.  Latency bounds it: with 8 threads a column, and
-// so 19 rows a range instead of 5, it took 2 us longer.
+// Sums of the rows of `part`, in a fixed order: 32 threads a column, each a range
+// of rows, then the ranges in order.  Latency bounds it: with 8 threads a column,
+// and so 19 rows a range instead of 5, it took 2 us longer.
 constexpr int kReduceSlices = 32;
 template <class DT>
 __global__ void __launch_bounds__(32 * kReduceSlices)
@@ -742,7 +744,7 @@ BackwardPlan backward_plan(int64_t rows, int64_t d, int num_sms) {
   p.lanes = lanes_for(d);
   // one block an SM: its registers, at 512 threads, and its shared memory are full
   const int64_t in_block = std::max<int64_t>(1, d > kMid ? 1 : std::min<int64_t>(512 / p.lanes, rows));
-  p.threads = static_cast<int>(p.lanes < 32 ? std::max<int64_t>(32, (in_block * p.lanes + 31) / 32 * 32) : in_block * p.lanes);
+  p.threads = static_cast<int>((in_block * p.lanes + 31) / 32 * 32);
   p.grid = std::min<int64_t>((rows * p.lanes + p.threads - 1) / p.threads, num_sms);
   p.groups = p.grid;
   return p;
@@ -795,7 +797,8 @@ cudaError_t with_types(int32_t x_dtype, int64_t vec, F f) {
 dgl_status prepare(dgl_norm_desc& n, bool backward, NormArgs& a, int64_t& vec) {
   const size_t xs = size_of(n.x_dtype), ws = size_of(n.w_dtype);
   vec = 16 / static_cast<int64_t>(xs);
-  if (!aligned(n.weight, ws) || !aligned(n.bias, ws) || !aligned(n.mean, 4) || !aligned(n.rstd, 4)) return DGL_ERR_ALIGN;
+  if (!aligned(n.weight, ws) || !aligned(n.bias, ws) || !aligned(n.mean, 4) || !aligned(n.rstd, 4))
+    return DGL_ERR_ALIGN;
   dgl_status st;
   if (n.rows > 0) {
     if ((st = check_matrix(n.x, n.ldx, n.rows, n.d, xs, vec)) != DGL_OK) return st;

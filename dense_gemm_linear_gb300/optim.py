@@ -74,6 +74,8 @@ class AdamW:
                     raise TypeError(f"master[{i}] is given beside a param of fp32")
                 t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
         sizes = [p.numel() for p in params]
+        if len({t.param for t in table if t.n}) != sum(1 for k in sizes if k):
+            raise ValueError("a tensor is given twice in params: the updates would race")
         blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
         m_type, v_type = _STATES[state_bits]
         scaled = state_bits == 8

@@ -474,7 +474,8 @@ dgl_status dgl_linear_distill(const dgl_head_desc* head, const int64_t* indices,
  * row of NaN and adds nothing.
  *
  * Sums are fp32 in an order fixed by the tokens, so that equal calls give equal
- * bits; a bf16 dW is rounded once.
+ * bits; a bf16 dW is rounded once.  An element that is added to gets one
+ * addition (or one for each 131072 tokens), which takes subnormal numbers for zero.
  */
 typedef struct dgl_embed_desc {
   int64_t T, V, d;
@@ -651,15 +652,16 @@ typedef struct dgl_adamw_desc {
  * probabilities that keep its expectation (to 2^-16 of a step between codes): rounded to the
  * nearest code, a v that changes by a thousandth a step would never move.  The
  * random numbers are a function of seed, t and the element's place among the
- * call's tensors, each padded to whole blocks: equal calls give equal bits.  A v above zero stays above
- * zero.  A state that is not finite is stored as NaN and does not affect the
- * others of its block.
+ * call's tensors, each padded to whole blocks: equal calls give equal bits.  A
+ * v above zero stays above zero.  A state that is not finite is stored as NaN
+ * and does not affect the others of its block.
  *
  * tensors: host array of `count` descriptors, read during the call only; no
  * two may overlap.  Every tensor is checked before anything is enqueued.
- * Enqueues one launch for each 336 tensors, allocates nothing, and may be
- * captured into a CUDA graph (each replay takes the next step).  count == 0
- * and empty tensors are allowed; the step is counted all the same.  Errors:
+ * Enqueues one launch for each kind of tensors (their types, with a master or
+ * not, in units or not) and 336 of it, allocates nothing, and may be captured
+ * into a CUDA graph (each replay takes the next step).  count == 0 and empty
+ * tensors are allowed; the step is counted all the same.  Errors:
  * DGL_ERR_ARG (null pointers, a negative n, a master beside an fp32 param, a
  * scalar out of its range, an unknown type), DGL_ERR_ALIGN, DGL_ERR_SHAPE (n
  * past 2^40), DGL_ERR_UNSUPPORTED, DGL_ERR_CUDA.

@@ -212,6 +212,39 @@ def test_extreme_gradients(dgl):
         assert p.isfinite().all()
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_no_eps(dgl, bits):
+    """Without eps the step is lr m / sqrt(v) whatever the gradients' size, and nothing where there was none."""
+    for size in (1.0, 1e-12, 3e-18):
+        p, g = torch.zeros(300, device="cuda"), torch.full((300,), size, device="cuda")
+        opt = dgl.AdamW([p], [g], lr=LR, eps=0.0, weight_decay=0.0, state_bits=bits)
+        opt.step()
+        # at 3e-18 v is 9e-39, where fp32 is left with 20 bits of it
+        assert torch.allclose(p, torch.full_like(p, -LR), rtol=1e-5)
+
+
+def test_kinds_mixed(dgl):
+    """Tensors of all types, on and off their units, in one call: each as in a call of its own, in 32 bits."""
+    together, alone = [], []
+    for seed, (p_dtype, g_dtype, master, offset) in enumerate(
+            [(F32, F32, False, 0), (BF16, F32, True, 0), (F32, BF16, False, 8), (BF16, BF16, False, 0), (BF16, BF16, True, 1),
+             (F32, F32, False, 1), (BF16, F32, True, 3)]):
+        params, grads = make([3000, 17], p_dtype, g_dtype, offset, seed)
+        for p, g in zip(params, grads):
+            m = p.float() if master else None
+            together.append((p, g, m))
+            alone.append((p.clone(), g.clone(), None if m is None else m.clone()))
+    opt = dgl.AdamW([t[0] for t in together], [t[1] for t in together], lr=LR, master=[t[2] for t in together])
+    for _ in range(3):
+        opt.step()
+    assert opt.steps.item() == 3
+    for (p, _, m), (q, g, n) in zip(together, alone):
+        one = dgl.AdamW([q], [g], lr=LR, master=[n])
+        for _ in range(3):
+            one.step()
+        assert torch.equal(p, q) and (m is None or torch.equal(m, n))
+
+
 def test_graph(dgl):
     """A captured step replayed takes the next step each time; the learning rate and the scale are read anew."""
     def fresh():

@@ -155,6 +155,23 @@ def test_strided_rows(dgl, dtype, d, pitch, offset):
         assert torch.allclose(p.double(), q.double(), rtol=2 * half_step(p.dtype) + 1e-5, atol=1e-4)
 
 
+@pytest.mark.parametrize("d", [64, 1024, 8192, 12288])
+@pytest.mark.parametrize("w_dtype", [BF16, F32])
+def test_weights_off_their_units(dgl, d, w_dtype):
+    """Weights and biases that begin anywhere, beside rows that are whole units; a norm without one of them."""
+    x, dy, w, b = make(200, d, BF16, w_dtype)
+    w1, b1 = torch.cat([w[:1], w])[1:], torch.cat([b[:3], b])[3:]
+    assert w1.data_ptr() % 16 and torch.equal(w1, w)
+    want, got = dgl.layer_norm(x, w, b), dgl.layer_norm(x, w1, b1)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    want = dgl.layer_norm_grad(dy, x, want[1], want[2], w)
+    got = dgl.layer_norm_grad(dy, x, got[1], got[2], w1)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    ones, zeros = torch.ones_like(w), torch.zeros_like(b)
+    assert torch.equal(dgl.layer_norm(x, None, b)[0], dgl.layer_norm(x, ones, b)[0])
+    assert torch.equal(dgl.layer_norm(x, w)[0], dgl.layer_norm(x, w, zeros)[0])
+
+
 @pytest.mark.parametrize("d", [96, 1000, 9000])
 def test_in_place(dgl, d):
     x, _, w, b = make(50, d, BF16, F32)

@@ -283,6 +283,6 @@ def test_helper_refusals(current, raw_stream):
                 lambda: dgl.AdamW([a["p"]], [a["g"]], exp_avg=[]),
                 lambda: dgl.AdamW([a["p"]], [a["g"]], exp_avg_scale=[a["m"]]),
                 lambda: dgl.AdamW([a["g"]], [a["g"]], master=[a["master"]]),
-                lambda: dgl.AdamW([a["p"].t()], [a["g"].t()]), lambda: dgl.AdamW([a["p"]]).step()):
+                lambda: dgl.AdamW([a["p"], a["p"]], [a["g"], a["g"]]), lambda: dgl.AdamW([a["p"].t()], [a["g"].t()]), lambda: dgl.AdamW([a["p"]]).step()):
         with pytest.raises((TypeError, ValueError)):
             bad()
