@@ -719,10 +719,10 @@ struct GradLayout {
   int each = 0;  // positions that a worker sums
 };
 
-// Positions that a worker sums: 16, or as many more as leave about 1500 threads an SM.
+// Positions that a worker sums: 8, or as many more as leave about 1500 threads an SM.
 int each_for(int64_t n, int64_t d, int64_t size) {
   const int64_t threads = n * round_up(d * size, 16) / 16;
-  return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(16, threads / (152 * 1500) / 8 * 8)));
+  return static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(8, round_up(threads / (152 * 1500), 8))));
 }
 
 GradLayout grad_layout(const dgl_embed_desc& e) {
