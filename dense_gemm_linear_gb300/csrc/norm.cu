@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     // (a row that does not exist, and columns past the row's, are zeros of dy and add nothing)
     float2 h[kElems / 2], g[kElems / 2];
     const float mean = next_mean, rstd = next_rstd;
+    next_mean = next_rstd = 0.0f;
     if (row < nrows - groups) next_mean = a.mean[row + groups], next_rstd = a.rstd[row + groups];
     if constexpr (kKeep) {
       copy_async_wait<DEPTH - 2>();

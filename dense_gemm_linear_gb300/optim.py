@@ -29,6 +29,14 @@ def _flat(t, name, device):
     return t.data_ptr()
 
 
+def _apart(table, *names):
+    """Refuses a tensor that is given twice where a step writes."""
+    at = [getattr(t, name) for t in table if t.n for name in names]
+    at = [p for p in at if p]
+    if len(set(at)) != len(at):
+        raise ValueError(f"a tensor is given twice among {', '.join(names)}: the updates would race")
+
+
 class AdamW:
     """AdamW (Adam with decoupled weight decay) over a list of tensors, all in one launch a step.
 
@@ -74,8 +82,7 @@ class AdamW:
                     raise TypeError(f"master[{i}] is given beside a param of fp32")
                 t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
         sizes = [p.numel() for p in params]
-        if len({t.param for t in table if t.n}) != sum(1 for k in sizes if k):
-            raise ValueError("a tensor is given twice in params: the updates would race")
+        _apart(table, "param", "master")
         blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
         m_type, v_type = _STATES[state_bits]
         scaled = state_bits == 8
@@ -85,6 +92,7 @@ class AdamW:
         self.exp_avg_sq = self._state("exp_avg_sq", exp_avg_sq, sizes, v_type, table)
         self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, blocks, _F32, table) if scaled else None
         self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, blocks, _F32, table) if scaled else None
+        _apart(table, "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
         self.steps = torch.zeros(1, dtype=torch.int64, device=device) if steps is None else steps
         self._ticket = torch.zeros(1, dtype=torch.int32, device=device)
         self._table = table

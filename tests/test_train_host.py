@@ -283,6 +283,9 @@ def test_helper_refusals(current, raw_stream):
                 lambda: dgl.AdamW([a["p"]], [a["g"]], exp_avg=[]),
                 lambda: dgl.AdamW([a["p"]], [a["g"]], exp_avg_scale=[a["m"]]),
                 lambda: dgl.AdamW([a["g"]], [a["g"]], master=[a["master"]]),
-                lambda: dgl.AdamW([a["p"], a["p"]], [a["g"], a["g"]]), lambda: dgl.AdamW([a["p"].t()], [a["g"].t()]), lambda: dgl.AdamW([a["p"]]).step()):
+                lambda: dgl.AdamW([a["p"], a["p"]], [a["g"], a["g"]]),
+                lambda: dgl.AdamW([a["p"], a["p"].clone()], [a["g"], a["g"]], master=[a["master"]] * 2),
+                lambda: dgl.AdamW([a["p"]], [a["g"]], exp_avg=[a["m"]], exp_avg_sq=[a["m"]], steps=a["steps"]),
+                lambda: dgl.AdamW([a["p"].t()], [a["g"].t()]), lambda: dgl.AdamW([a["p"]]).step()):
         with pytest.raises((TypeError, ValueError)):
             bad()
