@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import metrics  # noqa: F401  (pure-Python metric helpers)
 
@@ -165,12 +166,12 @@ def load_library(path: str | None = None):
     lib.dgl_linear_distill.argtypes = [ctypes.POINTER(HeadDesc), vp, vp, vp, i32, ctypes.c_float, vp]
     lib.dgl_linear_distill.restype = i32
     for name in ("dgl_embedding", "dgl_embedding_grad"):
-        getattr(lib, name).argtypes = [ctypes.POINTER(EmbedDesc), vp]
+        getattr(lib, name).argtypes = [vp, vp]  # a descriptor or its bytes
         getattr(lib, name).restype = i32
     lib.dgl_embedding_workspace.argtypes = [ctypes.POINTER(EmbedDesc), ctypes.POINTER(i64)]
     lib.dgl_embedding_workspace.restype = i32
     for name in ("dgl_layer_norm", "dgl_layer_norm_grad"):
-        getattr(lib, name).argtypes = [ctypes.POINTER(NormDesc), vp]
+        getattr(lib, name).argtypes = [vp, vp]
         getattr(lib, name).restype = i32
     lib.dgl_layer_norm_workspace.argtypes = [ctypes.POINTER(NormDesc), ctypes.POINTER(i64)]
     lib.dgl_layer_norm_workspace.restype = i32
@@ -198,6 +199,23 @@ def status_string(status: int) -> str:
         return load_library().dgl_status_string(status).decode()
     except ImportError:
         return "library not loaded"
+
+
+_FORMATS = {ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f", ctypes.c_int32: "i"}
+
+
+def _packer(kind):
+    """A function of all fields of a descriptor that returns its bytes, in a fifth of the time that the structure
+    takes to make."""
+    packed = struct.Struct("@" + "".join(_FORMATS[t] for _, t in kind._fields_) + "0q")  # (padded at its end)
+    assert packed.size == ctypes.sizeof(kind)
+    return packed.pack
+
+
+def _at(desc, kind):
+    if not isinstance(desc, kind):
+        raise TypeError(f"a {kind.__name__} is expected, got {type(desc).__name__}")
+    return ctypes.byref(desc)
 
 
 def _check(status: int, where: str):
@@ -283,12 +301,12 @@ def dgl_linear_distill(head: HeadDesc, indices, logits, teacher_lse, k, temperat
 
 def dgl_embedding(embed: EmbedDesc, stream=0) -> int:
     """Embedding lookup (see include/dgl.h)."""
-    return load_library().dgl_embedding(ctypes.byref(embed), stream)
+    return load_library().dgl_embedding(_at(embed, EmbedDesc), stream)
 
 
 def dgl_embedding_grad(embed: EmbedDesc, stream=0) -> int:
     """The gradient of an embedding (see include/dgl.h)."""
-    return load_library().dgl_embedding_grad(ctypes.byref(embed), stream)
+    return load_library().dgl_embedding_grad(_at(embed, EmbedDesc), stream)
 
 
 def dgl_embedding_workspace(embed: EmbedDesc) -> int:
@@ -300,12 +318,12 @@ def dgl_embedding_workspace(embed: EmbedDesc) -> int:
 
 def dgl_layer_norm(norm: NormDesc, stream=0) -> int:
     """Layer norm, forward (see include/dgl.h)."""
-    return load_library().dgl_layer_norm(ctypes.byref(norm), stream)
+    return load_library().dgl_layer_norm(_at(norm, NormDesc), stream)
 
 
 def dgl_layer_norm_grad(norm: NormDesc, stream=0) -> int:
     """Layer norm, backward (see include/dgl.h)."""
-    return load_library().dgl_layer_norm_grad(ctypes.byref(norm), stream)
+    return load_library().dgl_layer_norm_grad(_at(norm, NormDesc), stream)
 
 
 def dgl_layer_norm_workspace(norm: NormDesc) -> int:

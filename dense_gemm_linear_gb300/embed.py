@@ -11,9 +11,11 @@ import functools
 
 import torch
 
-from . import OUT_BF16, EmbedDesc, _check, dgl_embedding_workspace, load_library
-from .head import _byref, _on_stream
+from . import OUT_BF16, EmbedDesc, _check, _packer, dgl_embedding_workspace, load_library
+from .head import _on_stream
 from .norm import _TYPES, _buffer, _matrix, _meta, _vector
+
+_pack = _packer(EmbedDesc)
 
 
 def _count(tokens, device):
@@ -54,9 +56,9 @@ def embedding(tokens, W, *, scale=1.0, ignore_index=-100, out_dtype=None, out=No
     (T,), (V, d) = tokens.shape, W.shape
     if out is None:
         out = torch.empty((T, d), dtype=_TYPES[y_code], device=device)
-    e = EmbedDesc(T, V, d, tokens.data_ptr(), ignore_index, W.data_ptr(), None, ldw, out.data_ptr(), None, ldy, scale=scale,
-                  w_dtype=w_code, y_dtype=y_code)
-    st = load_library().dgl_embedding(_byref(e), torch._C._cuda_getCurrentRawStream(device))
+    e = _pack(T, V, d, tokens.data_ptr(), ignore_index, W.data_ptr(), 0, ldw, out.data_ptr(), 0, ldy, 0, 0, scale, w_code,
+              y_code, 0)
+    st = load_library().dgl_embedding(e, torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_embedding")
     return out
@@ -105,9 +107,9 @@ def embedding_grad(tokens, dY, V, *, scale=1.0, ignore_index=-100, dW=None, dw_d
     else:
         _buffer(workspace, device)
         size = workspace.nbytes
-    e = EmbedDesc(T, V, d, tokens.data_ptr(), ignore_index, None, dW.data_ptr(), ldw, None, dY.data_ptr(), ldy,
-                  workspace.data_ptr(), size, scale, dw_dtype, y_code, 1 if accumulate else 0)
-    st = load_library().dgl_embedding_grad(_byref(e), torch._C._cuda_getCurrentRawStream(device))
+    e = _pack(T, V, d, tokens.data_ptr(), ignore_index, 0, dW.data_ptr(), ldw, 0, dY.data_ptr(), ldy, workspace.data_ptr(),
+              size, scale, dw_dtype, y_code, 1 if accumulate else 0)
+    st = load_library().dgl_embedding_grad(e, torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_embedding_grad")
     return dW

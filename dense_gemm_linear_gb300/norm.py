@@ -12,10 +12,11 @@ import functools
 
 import torch
 
-from . import OUT_BF16, OUT_F32, NormDesc, _check, dgl_layer_norm_workspace, load_library
-from .head import _byref, _on_stream
+from . import OUT_BF16, OUT_F32, NormDesc, _check, _packer, dgl_layer_norm_workspace, load_library
+from .head import _on_stream
 
 _F32 = torch.float32
+_pack = _packer(NormDesc)
 _CODES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 _TYPES = {OUT_BF16: torch.bfloat16, OUT_F32: torch.float32}
 
@@ -118,10 +119,9 @@ def layer_norm(x, weight=None, bias=None, *, eps=1e-5, out=None, stream=None):
         out = torch.empty((rows, d), dtype=x.dtype, device=device)
     mean = torch.empty(rows, dtype=_F32, device=device)
     rstd = torch.empty(rows, dtype=_F32, device=device)
-    n = NormDesc(rows, d, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(),
-                 None if bias is None else bias.data_ptr(), out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), eps=eps,
-                 x_dtype=code, w_dtype=w_code)
-    st = load_library().dgl_layer_norm(_byref(n), torch._C._cuda_getCurrentRawStream(device))
+    n = _pack(rows, d, x.data_ptr(), ldx, 0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(),
+              out.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, eps, code, w_code, 0, 0)
+    st = load_library().dgl_layer_norm(n, torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_layer_norm")
     return out, mean, rstd
@@ -183,7 +183,7 @@ def layer_norm_grad(dy, x, mean, rstd, weight=None, *, need_dx=True, need_dw=Tru
         dweight = torch.empty(d, dtype=_TYPES[dw_dtype], device=device)
     if need_db and dbias is None:
         dbias = torch.empty(d, dtype=_TYPES[dw_dtype], device=device)
-    at = None
+    at = 0
     if size:
         if workspace is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=device)
@@ -191,11 +191,10 @@ def layer_norm_grad(dy, x, mean, rstd, weight=None, *, need_dx=True, need_dw=Tru
             _buffer(workspace, device)
             size = workspace.nbytes
         at = workspace.data_ptr()
-    n = NormDesc(rows, d, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(), None, None, 0, mean.data_ptr(),
-                 rstd.data_ptr(), dy.data_ptr(), lddy, dx.data_ptr() if need_dx else None, d,
-                 dweight.data_ptr() if need_dw else None, dbias.data_ptr() if need_db else None, at, size, 0.0, code, w_code,
-                 dw_dtype, 1 if accumulate else 0)
-    st = load_library().dgl_layer_norm_grad(_byref(n), torch._C._cuda_getCurrentRawStream(device))
+    n = _pack(rows, d, x.data_ptr(), ldx, 0 if weight is None else weight.data_ptr(), 0, 0, 0, mean.data_ptr(),
+              rstd.data_ptr(), dy.data_ptr(), lddy, dx.data_ptr() if need_dx else 0, d, dweight.data_ptr() if need_dw else 0,
+              dbias.data_ptr() if need_db else 0, at, size, 0.0, code, w_code, dw_dtype, 1 if accumulate else 0)
+    st = load_library().dgl_layer_norm_grad(n, torch._C._cuda_getCurrentRawStream(device))
     if st:
         _check(st, "dgl_layer_norm_grad")
     return dx, dweight, dbias

