@@ -209,7 +209,14 @@ def _packer(kind):
     takes to make."""
     packed = struct.Struct("@" + "".join(_FORMATS[t] for _, t in kind._fields_) + "0q")  # (padded at its end)
     assert packed.size == ctypes.sizeof(kind)
-    return packed.pack
+
+    def pack(*values):
+        try:
+            return packed.pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"an argument does not fit its field of {kind.__name__}: {e}") from None
+
+    return pack
 
 
 def _at(desc, kind):

@@ -277,6 +277,9 @@ def test_helper_refusals(current, raw_stream):
                 lambda: dgl.layer_norm_grad(dy, x, mean, rstd, w, need_dw=False, need_db=False, accumulate=True),
                 lambda: dgl.embedding(a["tokens"][:, None], a["W"]), lambda: dgl.embedding(a["tokens"], a["W"], out_dtype=3),
                 lambda: dgl.embedding(a["tokens"], a["W"], out=a["out"], out_dtype=dgl.OUT_F32),
+                lambda: dgl.embedding(a["tokens"], a["W"], ignore_index=None),
+                lambda: dgl.embedding(a["tokens"], a["W"], ignore_index=1 << 63),
+                lambda: dgl.layer_norm(x, w, eps="1e-5"),
                 lambda: dgl.embedding_grad(a["tokens"], a["dY"], V, accumulate=True),
                 lambda: dgl.embedding_grad(a["tokens"], a["dY"], V, dw_dtype=9),
                 lambda: dgl.embedding_grad(a["tokens"], a["dY"], V + 1, dW=a["dW"]),
