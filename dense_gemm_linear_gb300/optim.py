@@ -37,6 +37,27 @@ def _apart(table, *names):
         raise ValueError(f"a tensor is given twice among {', '.join(names)}: the updates would race")
 
 
+def _unmoved(tensors, places, indexes):
+    return [t.data_ptr() for t in tensors] == places
+
+
+# (torch's own form of the same takes half the time: 3 us for 98 tensors)
+_unmoved = getattr(torch._C, "_tensors_data_ptrs_at_indices_equal", _unmoved)
+
+
+def _kept(name):
+    """A list of tensors that the optimizer holds the memory of: handed out as aliases, replaced as a whole."""
+
+    def get(self):
+        held = self._held[name]
+        return None if held is None else tuple(None if t is None else t.detach() for t in held)
+
+    def replace(self, given):
+        self._lay(**{name: given})
+
+    return property(get, replace)
+
+
 class AdamW:
     """AdamW (Adam with decoupled weight decay) over a list of tensors, all in one launch a step.
 
@@ -49,10 +70,17 @@ class AdamW:
     fp32 scale for each 128 elements, rounded at random with `seed`.
 
     exp_avg, exp_avg_sq, in 8 bits also exp_avg_scale and exp_avg_sq_scale
-    (lists of 1-D tensors), and steps (int64 [1], the steps taken) are the state: made
+    (sequences of 1-D tensors), and steps (int64 [1], the steps taken) are the state: made
     as zeros when None, kept as attributes of those names, and enough with the
     params and masters to go on from a checkpoint.  All tensors are on the
     device that is current, then and at every step.
+
+    The optimizer holds the memory of its state and masters.  Their attributes are
+    tuples of aliases, through which values can be read and changed; assigning a
+    whole list (or steps, or grads) replaces the tensors, with the checks of the
+    start.  Where a param or a gradient given at the start has moved since the
+    last step (`p.data = ...`), all are checked again and its new memory is taken; the
+    old is let go then.  A captured step keeps the addresses of its capture.
     """
 
     def __init__(self, params, grads=None, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, master=None,
@@ -66,62 +94,114 @@ class AdamW:
         if state_bits not in _STATES:
             raise ValueError("state_bits must be 8 or 32")
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if len(decay) != n:
+            raise ValueError("weight_decay has one entry for each of params")
+        for i, p in enumerate(params):
+            _code(p, f"params[{i}]")
         if master is True:
             master = [p.detach().to(_F32, copy=True).contiguous() if p.dtype == torch.bfloat16 else None for p in params]
-        if len(decay) != n or (master is not None and len(master) != n):
-            raise ValueError("weight_decay and master have one entry for each of params")
-        self.device, self.params, self.master, self.state_bits = device, params, master, state_bits
-        self.lr = lr
-        table = (AdamWTensor * n)()
+        self.device, self.state_bits, self.lr = device, state_bits, lr
+        self._decay = decay
+        sizes = [p.numel() for p in params]
+        if state_bits == 8:
+            blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
+            exp_avg_scale = self._zeros(blocks, _F32) if exp_avg_scale is None else exp_avg_scale
+            exp_avg_sq_scale = self._zeros(blocks, _F32) if exp_avg_sq_scale is None else exp_avg_sq_scale
+        m_type, v_type = _STATES[state_bits]
+        self._ticket = torch.zeros(1, dtype=torch.int32, device=device)
+        self._desc = AdamWDesc(None, self._ticket.data_ptr(), None, None, 0.0, betas[0], betas[1], eps,
+                               seed & (2**64 - 1), state_bits)
+        self._held = {}
+        self._lay(params=params, grads=grads, master=master, exp_avg_scale=exp_avg_scale,
+                  exp_avg_sq_scale=exp_avg_sq_scale, exp_avg=self._zeros(sizes, m_type) if exp_avg is None else exp_avg,
+                  exp_avg_sq=self._zeros(sizes, v_type) if exp_avg_sq is None else exp_avg_sq,
+                  steps=torch.zeros(1, dtype=torch.int64, device=device) if steps is None else steps)
+
+    params = property(lambda self: tuple(self._held["params"]))
+    master = _kept("master")
+    exp_avg = _kept("exp_avg")
+    exp_avg_sq = _kept("exp_avg_sq")
+    exp_avg_scale = _kept("exp_avg_scale")
+    exp_avg_sq_scale = _kept("exp_avg_sq_scale")
+
+    @property
+    def grads(self):
+        grads = self._held["grads"]
+        return None if grads is None else tuple(grads)
+
+    @grads.setter
+    def grads(self, grads):
+        self._lay(grads=grads)
+
+    @property
+    def steps(self):
+        return self._held["steps"].detach()
+
+    @steps.setter
+    def steps(self, steps):
+        self._lay(steps=steps)
+
+    def _zeros(self, sizes, dtype):
+        """Tensors of a state, in one buffer, each in whole blocks of 128 elements."""
+        slots = [-(-k // ADAMW_BLOCK) * ADAMW_BLOCK for k in sizes]
+        whole = torch.zeros(sum(slots), dtype=torch.uint8 if dtype != _F32 else _F32, device=self.device).view(dtype)
+        return [s[:k] for s, k in zip(whole.split(slots), sizes)] if slots else []
+
+    def _lay(self, **given):
+        """Checks all tensors, those given in place of the ones held, and lays out the table of the library's calls."""
+        held = {**self._held, **given}
+        params, master, device = list(held["params"]), held["master"], self.device
+        if master is not None and len(master) != len(params):
+            raise ValueError("master has one entry for each of params")
+        table = (AdamWTensor * len(params))()
         for i, p in enumerate(params):
             t = table[i]
             t.param_dtype = _code(p, f"params[{i}]")
-            t.param, t.n, t.weight_decay = _flat(p, f"params[{i}]", device), p.numel(), decay[i]
+            t.param, t.n, t.weight_decay = _flat(p, f"params[{i}]", device), p.numel(), self._decay[i]
             if master is not None and master[i] is not None:
                 if p.dtype != torch.bfloat16:
                     raise TypeError(f"master[{i}] is given beside a param of fp32")
                 t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
-        sizes = [p.numel() for p in params]
         _apart(table, "param", "master")
+        sizes = [p.numel() for p in params]
         blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
-        m_type, v_type = _STATES[state_bits]
-        scaled = state_bits == 8
-        if not scaled and (exp_avg_scale is not None or exp_avg_sq_scale is not None):
+        m_type, v_type = _STATES[self.state_bits]
+        states = [("exp_avg", sizes, m_type), ("exp_avg_sq", sizes, v_type)]
+        if self.state_bits == 8:
+            states += [("exp_avg_scale", blocks, _F32), ("exp_avg_sq_scale", blocks, _F32)]
+        elif held["exp_avg_scale"] is not None or held["exp_avg_sq_scale"] is not None:
             raise ValueError("states of 32 bits have no scales")
-        self.exp_avg = self._state("exp_avg", exp_avg, sizes, m_type, table)
-        self.exp_avg_sq = self._state("exp_avg_sq", exp_avg_sq, sizes, v_type, table)
-        self.exp_avg_scale = self._state("exp_avg_scale", exp_avg_scale, blocks, _F32, table) if scaled else None
-        self.exp_avg_sq_scale = self._state("exp_avg_sq_scale", exp_avg_sq_scale, blocks, _F32, table) if scaled else None
-        _apart(table, "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
-        self.steps = torch.zeros(1, dtype=torch.int64, device=device) if steps is None else steps
-        self._ticket = torch.zeros(1, dtype=torch.int32, device=device)
-        self._table = table
-        self._desc = AdamWDesc(_packed(self.steps, "steps", torch.int64, (1,), device), self._ticket.data_ptr(), None,
-                               None, 0.0, betas[0], betas[1], eps, seed & (2**64 - 1), state_bits)
-        self.grads = None
+        for name, lengths, dtype in states:
+            self._state(name, held[name], lengths, dtype, table)
+        _apart(table, *(name for name, _, _ in states))
+        steps = _packed(held["steps"], "steps", torch.int64, (1,), device)
+        grads = None if held["grads"] is None else list(held["grads"])
         if grads is not None:
-            self._take(grads, table)
-            self.grads = list(grads)
+            self._take(grads, table, params)
+        # what is the optimizer's own is held by aliases, whose memory nothing but the optimizer lets go
+        for name, _, _ in states:
+            held[name] = [t.detach() for t in held[name]]
+        held.update(params=params, grads=grads, steps=held["steps"].detach(),
+                    master=None if master is None else [None if t is None else t.detach() for t in master])
+        watched = params + (grads or [])
+        self._held, self._table, self._desc.steps = held, table, steps
+        # the memory of those that may move stays taken until they are seen to have moved: no other tensor gets its address
+        self._watched, self._pinned = watched, [t.detach() for t in watched]
+        self._places, self._indexes = [t.data_ptr() for t in watched], list(range(len(watched)))
 
     def _state(self, name, given, sizes, dtype, table):
-        """A state's tensors and their addresses in the table.  Those made here lie in one buffer, each in whole
-        blocks of 128 elements."""
-        if given is None:
-            slots = [-(-k // ADAMW_BLOCK) * ADAMW_BLOCK for k in sizes]
-            whole = torch.zeros(sum(slots), dtype=torch.uint8 if dtype != _F32 else _F32, device=self.device).view(dtype)
-            given = [s[:k] for s, k in zip(whole.split(slots), sizes)] if slots else []
-        elif len(given) != len(sizes):
+        """A state's addresses in the table."""
+        if given is None or len(given) != len(sizes):
             raise ValueError(f"{name} has one entry for each of params")
         for i, (t, k) in enumerate(zip(given, sizes)):
             if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != k:
                 raise TypeError(f"{name}[{i}] must be a {dtype} CUDA tensor of {k} elements")
             setattr(table[i], name, _flat(t, f"{name}[{i}]", self.device))
-        return list(given)
 
-    def _take(self, grads, table):
-        if len(grads) != len(self.params):
+    def _take(self, grads, table, params):
+        if len(grads) != len(params):
             raise ValueError("grads has one entry for each of params")
-        for t, g, p in zip(table, grads, self.params):
+        for t, g, p in zip(table, grads, params):
             t.grad_dtype = _code(g, "a gradient")
             if g.shape != p.shape:
                 raise ValueError(f"a gradient of shape {tuple(g.shape)} for a param of shape {tuple(p.shape)}")
@@ -139,8 +219,10 @@ class AdamW:
         if stream is not None:
             with torch.cuda.stream(stream):
                 self.step(grads, lr=lr, grad_scale=grad_scale)
-            mine = [self.params, self.master, self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale,
-                    self.grads if grads is None else grads, [self.steps, self._ticket, lr, grad_scale]]
+            held = self._held
+            mine = [held["params"], held["master"], held["exp_avg"], held["exp_avg_sq"], held["exp_avg_scale"],
+                    held["exp_avg_sq_scale"], held["grads"] if grads is None else grads,
+                    [held["steps"], self._ticket, lr, grad_scale]]
             for t in (t for group in mine if group for t in group):
                 if isinstance(t, torch.Tensor):
                     t.record_stream(stream)
@@ -148,12 +230,14 @@ class AdamW:
         if torch.cuda.current_device() != self.device:
             raise ValueError(f"the optimizer is on cuda:{self.device}, but the current device is "
                              f"cuda:{torch.cuda.current_device()}")
+        if not _unmoved(self._watched, self._places, self._indexes):
+            self._lay()
         table, desc = self._table, self._desc
         if grads is not None:
             table = type(table)()
             ctypes.memmove(table, self._table, ctypes.sizeof(table))
-            self._take(grads, table)
-        elif self.grads is None:
+            self._take(grads, table, self._held["params"])
+        elif self._held["grads"] is None:
             raise ValueError("step needs the gradients: none were given at the start")
         if lr is None:
             lr = self.lr
