@@ -29,12 +29,13 @@ def _flat(t, name, device):
     return t.data_ptr()
 
 
-def _apart(table, *names):
-    """Refuses a tensor that is given twice where a step writes."""
-    at = [getattr(t, name) for t in table if t.n for name in names]
-    at = [p for p in at if p]
-    if len(set(at)) != len(at):
-        raise ValueError(f"a tensor is given twice among {', '.join(names)}: the updates would race")
+def _apart(written):
+    """Refuses memory that a step would write twice; written: (address, bytes, name) of all that it writes."""
+    end, last = 0, None
+    for at, size, name in sorted(w for w in written if w[1]):
+        if at < end:
+            raise ValueError(f"{name} and {last} overlap: the updates would race")
+        end, last = at + size, name
 
 
 def _unmoved(tensors, places, indexes):
@@ -73,7 +74,8 @@ class AdamW:
     (sequences of 1-D tensors), and steps (int64 [1], the steps taken) are the state: made
     as zeros when None, kept as attributes of those names, and enough with the
     params and masters to go on from a checkpoint.  All tensors are on the
-    device that is current, then and at every step.
+    device that is current, then and at every step.  What a step writes (params,
+    masters, state) overlaps nothing else that it reads or writes.
 
     The optimizer holds the memory of its state and masters.  Their attributes are
     tuples of aliases, through which values can be read and changed; assigning a
@@ -162,7 +164,6 @@ class AdamW:
                 if p.dtype != torch.bfloat16:
                     raise TypeError(f"master[{i}] is given beside a param of fp32")
                 t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
-        _apart(table, "param", "master")
         sizes = [p.numel() for p in params]
         blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
         m_type, v_type = _STATES[self.state_bits]
@@ -173,8 +174,10 @@ class AdamW:
             raise ValueError("states of 32 bits have no scales")
         for name, lengths, dtype in states:
             self._state(name, held[name], lengths, dtype, table)
-        _apart(table, *(name for name, _, _ in states))
         steps = _packed(held["steps"], "steps", torch.int64, (1,), device)
+        lists = [("params", params), ("master", master or ())] + [(name, held[name]) for name, _, _ in states]
+        _apart([(t.data_ptr(), t.nbytes, f"{name}[{i}]") for name, tensors in lists for i, t in enumerate(tensors)
+                if t is not None] + [(steps, 8, "steps"), (self._ticket.data_ptr(), 4, "the ticket")])
         grads = None if held["grads"] is None else list(held["grads"])
         if grads is not None:
             self._take(grads, table, params)

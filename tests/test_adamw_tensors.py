@@ -173,3 +173,48 @@ def test_memory_that_moved_is_not_taken_for_another(calls):
     params[0].data = others[0]
     opt.step()
     expect(calls[-1], opt)
+
+
+def views(dtype, *ranges):
+    whole = some(400, dtype)
+    return [whole[a:b] for a, b in ranges]
+
+
+@pytest.mark.parametrize("ranges,fine", [(((0, 40), (8, 48)), False), (((0, 40), (39, 60)), False), (((0, 40), (0, 40)), False),
+                                         (((8, 16), (0, 40)), False), (((0, 40), (40, 80)), True), (((40, 80), (0, 40)), True),
+                                         (((0, 40), (20, 20), (40, 80)), True)])
+def test_memory_that_would_be_written_twice(calls, ranges, fine):
+    """Tensors that share some memory are refused, neighbours and empty ones are not."""
+    def grads():
+        return [some(b - a) for a, b in ranges]
+
+    def attempt(params, **given):
+        if fine:
+            dgl.AdamW(params, grads(), **given).step()
+        else:
+            with pytest.raises(ValueError, match="overlap"):
+                dgl.AdamW(params, grads(), **given)
+
+    def apart(dtype):
+        return [some(b - a, dtype) for a, b in ranges]
+
+    attempt(views(F32, *ranges))
+    attempt(apart(BF16), master=views(F32, *ranges))
+    attempt(apart(F32), exp_avg=views(F32, *ranges))
+    attempt(apart(F32), exp_avg=views(E4M3, *ranges), exp_avg_sq=apart(E5M2))
+    attempt(apart(F32), exp_avg=views(E4M3, *ranges), exp_avg_sq=views(E5M2, *ranges))
+
+
+def test_memory_that_lists_share(calls):
+    """A param that is a part of a state, of a master or of the step counter's buffer; a replacement that overlaps."""
+    whole = some(400)
+    for given in (dict(exp_avg=[whole[100:300]]), dict(exp_avg_sq=[whole[0:200]]), dict(steps=whole[150:152].view(I64))):
+        with pytest.raises(ValueError, match="overlap"):
+            dgl.AdamW([whole[:200]], [some(200)], **given)
+    opt = dgl.AdamW([whole[:200]], [some(200)])
+    with pytest.raises(ValueError, match="overlap"):
+        opt.exp_avg = [whole[199:399]]
+    with pytest.raises(ValueError, match="overlap"):
+        opt.steps = opt.exp_avg[0][2:4].view(I64)
+    opt.exp_avg = [whole[200:]]
+    opt.step()
