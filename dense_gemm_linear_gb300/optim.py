@@ -219,6 +219,8 @@ class AdamW:
         of which each replay takes the next step.  The host's number for lr is
         then part of the graph; a tensor is read anew.
         """
+        if lr is None:
+            lr = self.lr
         if stream is not None:
             with torch.cuda.stream(stream):
                 self.step(grads, lr=lr, grad_scale=grad_scale)
@@ -242,8 +244,6 @@ class AdamW:
             self._take(grads, table, self._held["params"])
         elif self._held["grads"] is None:
             raise ValueError("step needs the gradients: none were given at the start")
-        if lr is None:
-            lr = self.lr
         if isinstance(lr, torch.Tensor):
             desc.lr, desc.lr_at = 0.0, _packed(lr, "lr", _F32, lr.shape if lr.numel() == 1 else (1,), self.device)
         else:

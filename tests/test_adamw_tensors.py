@@ -218,3 +218,22 @@ def test_memory_that_lists_share(calls):
         opt.steps = opt.exp_avg[0][2:4].view(I64)
     opt.exp_avg = [whole[200:]]
     opt.step()
+
+
+@pytest.mark.parametrize("how", ["of the optimizer", "of the step"])
+def test_a_step_on_another_stream_is_noted(calls, monkeypatch, how):
+    """Everything that the step reads or writes is marked as used on its stream, the learning rate's tensor too."""
+    import contextlib
+    noted = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(OnDevice, "record_stream", lambda self, s: noted.append((self.data_ptr(), s)), raising=False)
+    opt, params, grads = make()
+    lr, scale = some(1), some(1)
+    if how == "of the step":
+        opt.step(lr=lr, grad_scale=scale, stream="s")
+    else:
+        opt.lr = lr
+        opt.step(grad_scale=scale, stream="s")
+    used = [*params, *grads, *opt.master, *opt.exp_avg, *opt.exp_avg_sq, *opt.exp_avg_scale, *opt.exp_avg_sq_scale, opt.steps,
+            lr, scale]
+    assert {(t.data_ptr(), "s") for t in used} <= set(noted)
