@@ -144,8 +144,6 @@ template <int BYTES>
 __device__ __forceinline__ void store_shared_zero(uint32_t to) {
   if constexpr (BYTES == 16)
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
-  else if constexpr (BYTES == 8)
-    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0) : "memory");
   else
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(0) : "memory");
 }
@@ -157,8 +155,6 @@ __device__ __forceinline__ U load_shared(uint32_t from) {
                  : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
                  : "r"(from)
                  : "memory");
-  else if constexpr (sizeof(U) == 8)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "r"(from) : "memory");
   else
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(from) : "memory");
   return u;
@@ -780,11 +776,13 @@ dgl_status check_matrix(const void* p, int64_t& ld, int64_t rows, int64_t d, siz
   return DGL_OK;
 }
 
+// The units that there are kernels for: 16 bytes, of bf16 also 4, and single elements.
 template <class XT, class F>
 cudaError_t with_vec(int64_t vec, F f) {
   constexpr int kMost = 16 / static_cast<int>(sizeof(XT));
-  if (vec >= kMost) return f(XT{}, std::integral_constant<int, kMost>{});
-  if (vec >= 2 && sizeof(XT) == 2) return f(XT{}, std::integral_constant<int, 2>{});
+  if (vec == kMost) return f(XT{}, std::integral_constant<int, kMost>{});
+  if constexpr (sizeof(XT) == 2)
+    if (vec >= 2) return f(XT{}, std::integral_constant<int, 2>{});
   return f(XT{}, std::integral_constant<int, 1>{});
 }
 
