@@ -288,8 +288,10 @@ __device__ __forceinline__ uint2 encode8(const float2 (&f)[kEach / 2], const uin
 }
 
 // m / (sqrt(v) root + eps) by the hardware's approximations, off by a few units
-// in the last place.  They take subnormal numbers for zero: a v below 2^-126
-// is nothing beside an eps past 1e-18; without one its root is taken in full.
+// in the last place.  They take subnormal numbers for zero: a v below 2^-126,
+// which adds less than 2^-63 root, is nothing beside an eps past 2^-39 root (1.8e-12
+// for a root of 1, 5.8e-11 on the first step where beta2 is 0.999); with a smaller
+// one the root and the quotient are taken in full.
 __device__ __forceinline__ float quotient(float m, float v, float root, float eps) {
   float r, q;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<EIGHT>) adamw_kernel(co
       m[i] = add_apart(mul2(both(s.beta1), m[i]), mul2(both(s.rest1), g[i]));
       v[i] = add_apart(mul2(both(s.beta2), v[i]), mul2(both(s.rest2), mul2(g[i], g[i])));
     }
-    if (s.eps > 1e-18f) {
+    if (s.eps > 0x1p-39f * root) {
 #pragma unroll
       for (int i = 0; i < kEach / 2; ++i) {
         const float2 u = make_float2(quotient(m[i].x, v[i].x, root, s.eps), quotient(m[i].y, v[i].y, root, s.eps));
