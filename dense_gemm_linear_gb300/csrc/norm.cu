@@ -116,14 +116,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 
-// (x - mean) rstd.  Of bf16 values as one multiplication and addition, whose
-// rounding is a bf16's 2^-16th unless the mean is hundreds of times the spread,
-// where bf16 holds little of the row; of fp32 values as two steps, of which the
-// first is nearly exact.
-template <class T>
+// (x - mean) rstd, in two steps, of which the first is nearly exact.  (As x rstd -
+// mean rstd, one instruction, a rounding of mean rstd remains where the row is equal
+// elements or nearly so: 0.4 of 30000 with an eps of 1e-5.)
 __device__ __forceinline__ float2 scaled(float2 x, float mean, float rstd) {
-  if constexpr (sizeof(T) == 2) return fma2(x, both(rstd), both(-mean * rstd));
-  else return mul2(add2(x, both(-mean)), both(rstd));
+  return mul2(add2(x, both(-mean)), both(rstd));
 }
 
 // A lane's units of a row, on their way from memory.  Units of 4 bytes or more pass
@@ -276,6 +273,14 @@ __device__ __forceinline__ void lane_columns(const void* v, int f32, int units_f
   }
 }
 
+// Gives the elements past the lane's `count` units a value.
+template <int VEC>
+__device__ __forceinline__ void fill_row(float2 (&f)[kElems / 2], int count, float v) {
+#pragma unroll
+  for (int i = 0; i < kElems; ++i)
+    if (i / VEC >= count) put(f, i, v);
+}
+
 // row: the lane's first unit.
 template <class T, int VEC>
 __device__ __forceinline__ void store_row(T* row, int apart, int count, const float2 (&f)[kElems / 2]) {
@@ -289,11 +294,33 @@ __device__ __forceinline__ void store_row(T* row, int apart, int count, const fl
   }
 }
 
+// sum / n: the quotient that is nearest, but for ties.
+__device__ __forceinline__ float over(float sum, float n, float inv_n) {
+  const float v = sum * inv_n;
+  return fmaf(fmaf(-v, n, sum), inv_n, v);
+}
+
+// (to a few units in the last place; of a subnormal number 0)
+__device__ __forceinline__ float root(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
 // apart. THREADS: the most in a block.  1024, of rows past 8192: the weight does
 // not fit beside a row in 64 registers and is read again for each row, from L1,
 // which it has to itself: the next row waits in registers and not in shared memory.
 // WARPS: a row has several warps, which are the block.
+//
+// Equal elements are their mean, and h is 0, whatever their size and rstd; elements
+// far from zero beside their spread keep what they differ by.  A warp's sum of such bf16
+// elements is exact or nearly so, and over() takes back what a product with 1 / n
+// is rounded by.  A row of fp32 elements whose mean is past kFar times their
+// standard deviation is gone over again: the mean becomes what the elements are
+// away from the first one, summed, and the squares are taken around that.  (Done for
+// every row it took 13% longer where rows are off their units.)
+constexpr float kFar = 16.0f;
 template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
@@ -307,7 +334,7 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   const int in_block = blockDim.x / lanes, groups = gridDim.x * in_block, nrows = static_cast<int>(a.rows);
   int row = blockIdx.x * in_block + threadIdx.x / lanes;
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, in_warp = threadIdx.x & 31;
-  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const float d = static_cast<float>(a.d), inv_d = 1.0f / d;
 
   const int count = lane < units ? (units - lane + lanes - 1) / lanes : 0, apart = lanes * VEC;
   RowUnits<XT, VEC, kKeep> rows;
@@ -350,42 +377,103 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
     ahead -= groups;
     copy_async_commit();
     // the warp's (or group's) mean and squares around it, then the block's
-    float2 t = f[0];
+    float2 t = f[0], squares = both(0.0f);
 #pragma unroll
     for (int i = 1; i < kElems / 2; ++i) t = add2(t, f[i]);
-    const float s = lanes_sum<WARPS>(t.x + t.y, lanes);
-    float mean = s * inv_held;
-    float2 squares = both(0.0f);
-    if (full) {
+    float sum = lanes_sum<WARPS>(t.x + t.y, lanes), q, mean, centre;  // centre: what is still to be taken from f
+    if constexpr (sizeof(XT) == 2) {
+      const float m = over(sum, held, inv_held);
 #pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) {
-        const float2 c = add2(f[i], both(-mean));
-        squares = fma2(c, c, squares);
+      for (int i = 0; i < kElems / 2; ++i) f[i] = add2(f[i], both(-m));
+      if (!full) fill_row<VEC>(f, count, 0.0f);
+#pragma unroll
+      for (int i = 0; i < kElems / 2; ++i) squares = fma2(f[i], f[i], squares);
+      q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
+      mean = m;
+      if constexpr (WARPS) {
+        float2* r = red[turn & 1];  // two in turn: one barrier a row
+        if (in_warp == 0) r[warp] = make_float2(sum, q);
+        __syncthreads();
+        const float2 o = other < warps ? r[other] : both(0.0f);
+        sum = warps_sum(o.x, few);
+        mean = over(sum, d, inv_d);
+        const float c = fmaf(-mean, counted.x, o.x);
+        q = warps_sum(fmaf(c * counted.y, c, o.y), few);
       }
+      centre = (mean - m) + fmaf(-mean, d, sum) * inv_d;
+      if (!(fabsf(mean) < INFINITY)) mean = sum * inv_d;  // (an infinite sum's is infinite)
     } else {
+      mean = sum * inv_held;
+      if (full) {
 #pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) {
-        float2 c = add2(f[i], both(-mean));
-        if (2 * i / VEC >= count) c.x = 0.0f;
-        if ((2 * i + 1) / VEC >= count) c.y = 0.0f;
-        squares = fma2(c, c, squares);
+        for (int i = 0; i < kElems / 2; ++i) {
+          const float2 c = add2(f[i], both(-mean));
+          squares = fma2(c, c, squares);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kElems / 2; ++i) {
+          float2 c = add2(f[i], both(-mean));
+          if (2 * i / VEC >= count) c.x = 0.0f;
+          if ((2 * i + 1) / VEC >= count) c.y = 0.0f;
+          squares = fma2(c, c, squares);
+        }
       }
-    }
-    float q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
-    if constexpr (WARPS) {
-      float2* r = red[turn & 1];  // two in turn: one barrier a row
-      if (in_warp == 0) r[warp] = make_float2(s, q);
-      __syncthreads();
-      const float2 o = other < warps ? r[other] : both(0.0f);
-      mean = warps_sum(o.x, few) * inv_d;
-      const float c = fmaf(o.x, counted.y, -mean);
-      q = warps_sum(fmaf(counted.x * c, c, o.y), few);
+      q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
+      if constexpr (WARPS) {
+        float2* r = red[turn & 1];
+        if (in_warp == 0) r[warp] = make_float2(sum, q);
+        __syncthreads();
+        const float2 o = other < warps ? r[other] : both(0.0f);
+        mean = warps_sum(o.x, few) * inv_d;
+        const float c = fmaf(o.x, counted.y, -mean);
+        q = warps_sum(fmaf(counted.x * c, c, o.y), few);
+      }
+      centre = mean;
+      const bool far = fabsf(mean) < INFINITY && !(fabsf(mean) <= kFar * root(q * inv_d) && q < INFINITY);
+      if (WARPS ? far : __any_sync(0xffffffffu, far)) {  // (all threads of a row have the same sums)
+        const auto row_sums = [&](float a, float b) {
+          if constexpr (!WARPS) return make_float2(lanes_sum<false>(a, lanes), lanes_sum<false>(b, lanes));
+          const float v = warp_sums(a, b);
+          float2* r = red[turn & 1];
+          __syncthreads();
+          if (in_warp == 0) r[warp].x = v;
+          if (in_warp == 16) r[warp].y = v;
+          __syncthreads();
+          const float2 o = other < warps ? r[other] : both(0.0f);
+          return make_float2(warps_sum(o.x, few), warps_sum(o.y, few));
+        };
+        const auto move = [&](float by) {
+          t = squares = both(0.0f);
+#pragma unroll
+          for (int i = 0; i < kElems / 2; ++i) f[i] = add2(f[i], both(-by));
+          fill_row<VEC>(f, count, 0.0f);
+#pragma unroll
+          for (int i = 0; i < kElems / 2; ++i) {
+            t = add2(t, f[i]);
+            squares = fma2(f[i], f[i], squares);
+          }
+          return row_sums(t.x + t.y, squares.x + squares.y);
+        };
+        float2 sums = move(far ? mean : 0.0f);  // (a row beside it stays as it is)
+        const float shift = far ? over(sums.x, d, inv_d) : 0.0f;
+        sums = move(shift);
+        if (far) {
+          centre = sums.x * inv_d;
+          mean += shift + centre;
+          q = fmaf(-sums.x, centre, sums.y);
+        }
+      }
     }
     const float rstd = reciprocal_root(fmaf(q, inv_d, a.eps));
     if (row >= nrows) continue;
     if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) f[i] = fma2(scaled<XT>(f[i], mean, rstd), w[i], b[i]);
+      for (int i = 0; i < kElems / 2; ++i) {
+        // (what is left of bf16 elements is small: one instruction)
+        const float2 h = sizeof(XT) == 2 ? fma2(f[i], both(rstd), both(-centre * rstd)) : scaled(f[i], centre, rstd);
+        f[i] = fma2(h, w[i], b[i]);
+      }
       store_row<XT, VEC>(y, apart, count, f);
     } else {
 #pragma unroll
@@ -396,7 +484,7 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
         unit_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, at, w_unit);
         unit_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, at, b_unit);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) e[j] = fmaf((get(f, i * VEC + j) - mean) * rstd, w_unit[j], b_unit[j]);
+        for (int j = 0; j < VEC; ++j) e[j] = fmaf((get(f, i * VEC + j) - centre) * rstd, w_unit[j], b_unit[j]);
         store_unit<XT, VEC>(y + i * apart, e);
       }
     }
@@ -417,26 +505,58 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return t;
 }
 
-// Forward of rows wider than a block holds: a block a row, three passes over it
-// (the second and third from L2).
+__device__ __forceinline__ float2 block_sums(float a, float b, float2* red) {
+  const float v = warp_sums(a, b);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32].x = v;
+  if ((threadIdx.x & 31) == 16) red[threadIdx.x / 32].y = v;
+  __syncthreads();
+  float2 t = both(0.0f);
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) t = add2(t, red[i]);
+  return t;
+}
+
+// Forward of rows wider than a block holds, and of those past 8192 off their units: a
+// block a row, three passes over it (the second and third from L2).
 template <class XT>
 __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ float red[kSlowThreads / 32];
+  __shared__ float2 reds[kSlowThreads / 32];
+  const auto finite = [](float v) { return fabsf(v) < INFINITY ? v : 0.0f; };  // (an infinite mean stays one)
+  const auto within = [](float v) { return fabsf(v) < 0x1p100f ? v : 0.0f; };
+  const float d = static_cast<float>(a.d);
+  const float n = static_cast<float>((a.d - static_cast<int>(threadIdx.x) + kSlowThreads - 1) / kSlowThreads);
+  const XT* ahead = static_cast<const XT*>(a.x) + blockIdx.x * a.ldx;
+  float x_first = to_float(ahead[0]), x_own = to_float(ahead[threadIdx.x]);  // of the next row: its first, the thread's first
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
     XT* y = static_cast<XT*>(a.y) + row * a.ldy;
-    float s = 0.0f, q = 0.0f;
-    for (int i = threadIdx.x; i < a.d; i += kSlowThreads) s += to_float(x[i]);
-    const float mean = block_sum(s, red) / static_cast<float>(a.d);
-    for (int i = threadIdx.x; i < a.d; i += kSlowThreads) {
-      const float c = to_float(x[i]) - mean;
-      q = fmaf(c, c, q);
+    // `near`, the mean but for roundings, by what the elements are away from the
+    // thread's first and that from the row's; then sums of what they are away from it
+    const float first = within(x_first), own = within(x_own);
+    float t = 0.0f;
+    float2 sums = both(0.0f);  // of distances, of squares
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.d; i += kSlowThreads) t += to_float(x[i]) - own;
+    if (row + gridDim.x < a.rows) {
+      ahead = x + gridDim.x * a.ldx;
+      x_first = to_float(ahead[0]);
+      x_own = to_float(ahead[threadIdx.x]);
     }
-    const float rstd = reciprocal_root(block_sum(q, red) / static_cast<float>(a.d) + a.eps);
+    const float near = first + block_sum(fmaf(n, own - first, t), red) / d;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < a.d; i += kSlowThreads) {
+      const float c = to_float(x[i]) - near;
+      sums.x += c;
+      sums.y = fmaf(c, c, sums.y);
+    }
+    sums = block_sums(sums.x, sums.y, reds);
+    const float s = finite(sums.x), shift = s / d, mean = near + shift;
+    const float rstd = reciprocal_root(fmaf(-shift, s, sums.y) / d + a.eps);
     for (int i = threadIdx.x; i < a.d; i += kSlowThreads)
-      y[i] = from_float<XT>(fmaf((to_float(x[i]) - mean) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f,
+      y[i] = from_float<XT>(fmaf(((to_float(x[i]) - near) - shift) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f,
                                  a.b ? element(a.b, a.w_f32, i) : 0.0f));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -536,7 +656,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
       lane_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, lane, lanes, units, wv);
     }
 #pragma unroll
-    for (int i = 0; i < kElems / 2; ++i) h[i] = scaled<XT>(h[i], mean, rstd);
+    for (int i = 0; i < kElems / 2; ++i) h[i] = scaled(h[i], mean, rstd);
     if (want_w) {
       if constexpr (kKeep) {
 #pragma unroll
@@ -858,7 +978,8 @@ dgl_status run_forward(dgl_norm_desc n, cudaStream_t stream) {
   DeviceState* ds = nullptr;
   if ((st = get_device(&dev, &ds)) != DGL_OK) return st;
   if (n.rows == 0) return DGL_OK;
-  if (n.d > kWide) {
+  // (past 8192 single elements spill where a block holds the row: 4000 x 12287 290 us in fp32, 110 so)
+  if (n.d > kWide || (n.d > kMid && vec < (n.x_dtype == DGL_OUT_F32 ? 4 : 2))) {
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(n.rows, int64_t(4) * ds->num_sms));
     a.lanes = kSlowThreads;
     const cudaError_t e = with_types(n.x_dtype, 1, [&](auto x, auto) {
@@ -870,9 +991,10 @@ dgl_status run_forward(dgl_norm_desc n, cudaStream_t stream) {
   const cudaError_t e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
     using X = decltype(x);
     constexpr int kVec = decltype(v)::value;
-    return n.d > kMid      ? launch_forward<X, kVec, 1024, true>(a, ds->num_sms, stream)
-           : a.lanes > 32 ? launch_forward<X, kVec, 512, true>(a, ds->num_sms, stream)
-                          : launch_forward<X, kVec, 512, false>(a, ds->num_sms, stream);
+    if constexpr (kVec > 1)
+      if (n.d > kMid) return launch_forward<X, kVec, 1024, true>(a, ds->num_sms, stream);
+    return a.lanes > 32 ? launch_forward<X, kVec, 512, true>(a, ds->num_sms, stream)
+                        : launch_forward<X, kVec, 512, false>(a, ds->num_sms, stream);
   });
   return e == cudaSuccess ? DGL_OK : DGL_ERR_CUDA;
 }

@@ -537,7 +537,8 @@ dgl_status dgl_embedding_grad(const dgl_embed_desc* embed, void* stream);
  *   ws, ws_bytes: device scratch, 256-byte aligned, of at least the bytes that
  *   dgl_layer_norm_workspace reports; for dweight and dbias only.
  *
- * Sums and statistics are fp32, the variance a sum of squares around the mean.
+ * Sums and statistics are fp32, the variance a sum of squares around the mean; a
+ * row of equal elements has that element as its mean and h = 0.
  * A row's results depend on that row alone; the sums over rows have an order
  * fixed by rows and d, so that equal calls give equal bits.
  */
