@@ -60,7 +60,8 @@ def _kept(name):
 
 
 class AdamW:
-    """AdamW (Adam with decoupled weight decay) over a list of tensors, all in one launch a step.
+    """AdamW (Adam with decoupled weight decay) over a list of tensors: a launch a step for each kind of
+    them (types, with a master or not, in 16-byte units or not).
 
     params: bf16 or fp32 CUDA tensors, contiguous, updated in place.  grads: a
     gradient for each, bf16 or fp32, of the same shape: the buffers that every

@@ -13,7 +13,7 @@ A step runs, through the library alone but for the activation,
   dgl.layer_norm_grad         da and dh, with the norms' weights' gradients
   dgl.dgl_gemm_bf16_ex        dx = du A and dA = du^T x
   dgl.embedding_grad          added to the dE that the head's loss left
-  dgl.AdamW                   one launch for all tensors
+  dgl.AdamW                   a launch for each kind of tensors
 
 The tokens follow one another by a fixed random rule, which the model learns.
 

@@ -651,11 +651,12 @@ typedef struct dgl_adamw_desc {
  * into [2^7, 2^8), its largest v into [2^14, 2^15) (no scale is below 2^-118
  * and 2^-125).  Each value is rounded to the code below or above it with
  * probabilities that keep its expectation (to 2^-16 of a step between codes): rounded to the
- * nearest code, a v that changes by a thousandth a step would never move.  The
+ * nearest code, a v that changes by a thousandth a step would never move.  Only a v
+ * above zero and below the lowest code, 2^-16 of the scale, becomes that code.  The
  * random numbers are a function of seed, t and the element's place among the
  * call's tensors, each padded to whole blocks: equal calls give equal bits.  A
- * v above zero stays above zero.  A state that is not finite is stored as NaN
- * and does not affect the others of its block.
+ * state that is not finite is stored as NaN and does not affect the others of its
+ * block.
  *
  * tensors: host array of `count` descriptors, read during the call only; no
  * two may overlap.  Every tensor is checked before anything is enqueued.
