@@ -294,6 +294,11 @@ __device__ __forceinline__ void store_row(T* row, int apart, int count, const fl
   }
 }
 
+// What elements are taken from before they are summed: anything that neither
+// overflows nor is lost beside them.
+__device__ __forceinline__ float within(float v) { return fabsf(v) < 0x1p100f ? v : 0.0f; }
+__device__ __forceinline__ float finite(float v) { return fabsf(v) < INFINITY ? v : 0.0f; }
+
 // sum / n: the quotient that is nearest, but for ties.
 __device__ __forceinline__ float over(float sum, float n, float inv_n) {
   const float v = sum * inv_n;
@@ -307,6 +312,46 @@ __device__ __forceinline__ float root(float v) {
   return r;
 }
 
+// Where `far`, a row of fp32 elements by a group of lanes (WARPS: the block) from
+// memory, in the steps of norm_forward_wide_kernel; the lanes of a warp enter together.
+template <bool WARPS>
+__device__ __noinline__ void far_row(const NormArgs& a, int64_t row, int lane, int lanes, bool far, float2* red) {
+  const int in_warp = threadIdx.x & 31, end = far ? a.d : 0;
+  const float d = static_cast<float>(a.d);
+  const auto row_sums = [&](float u, float v) {
+    if constexpr (!WARPS) return make_float2(lanes_sum<false>(u, lanes), lanes_sum<false>(v, lanes));
+    const float sum = warp_sums(u, v);
+    __syncthreads();
+    if (in_warp == 0) red[threadIdx.x / 32].x = sum;
+    if (in_warp == 16) red[threadIdx.x / 32].y = sum;
+    __syncthreads();
+    const float2 o = in_warp < lanes / 32 ? red[in_warp] : both(0.0f);
+    return make_float2(warps_sum(o.x, false), warps_sum(o.y, false));
+  };
+  const float* x = static_cast<const float*>(a.x) + row * a.ldx;
+  float* y = static_cast<float*>(a.y) + row * a.ldy;
+  const float first = far ? within(x[0]) : 0.0f, own = lane < end ? within(x[lane]) : 0.0f;
+  const float n = lane < end ? static_cast<float>((end - lane + lanes - 1) / lanes) : 0.0f;
+  float t = 0.0f, s = 0.0f, q = 0.0f;
+  for (int i = lane; i < end; i += lanes) t += x[i] - own;
+  const float near = first + row_sums(fmaf(n, own - first, t), 0.0f).x / d;
+  for (int i = lane; i < end; i += lanes) {
+    const float c = x[i] - near;
+    s += c;
+    q = fmaf(c, c, q);
+  }
+  const float2 sums = row_sums(s, q);
+  s = finite(sums.x);
+  const float shift = s / d, rstd = reciprocal_root(fmaf(-shift, s, sums.y) / d + a.eps);
+  for (int i = lane; i < end; i += lanes)
+    y[i] = fmaf(((x[i] - near) - shift) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f,
+                a.b ? element(a.b, a.w_f32, i) : 0.0f);
+  if (lane == 0 && far) {
+    if (a.mean) a.mean[row] = near + shift;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+}
+
 // Forward.  A persistent grid; each group of lanes takes rows a grid's groups
 // apart. THREADS: the most in a block.  1024, of rows past 8192: the weight does
 // not fit beside a row in 64 registers and is read again for each row, from L1,
@@ -317,10 +362,11 @@ __device__ __forceinline__ float root(float v) {
 // far from zero beside their spread keep what they differ by.  A warp's sum of such bf16
 // elements is exact or nearly so, and over() takes back what a product with 1 / n
 // is rounded by.  A row of fp32 elements whose mean is past kFar times their
-// standard deviation is gone over again: the mean becomes what the elements are
-// away from the first one, summed, and the squares are taken around that.  (Done for
-// every row it took 13% longer where rows are off their units.)
-constexpr float kFar = 16.0f;
+// standard deviation is gone over again, by what its elements are away from a lane's
+// first: below, fp32's roundings of the sums move h by a few times kFar 2^-24.  (Done
+// so for every row it took 13% longer where rows are off their units; 8192 x 4096 take
+// 43 us, 264 where every row is far.)
+constexpr float kFar = 64.0f;
 template <class XT, int VEC, int THREADS, bool WARPS>
 __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
@@ -328,7 +374,8 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   constexpr bool kKeep = THREADS <= 512;
   constexpr int DEPTH = kKeep ? kDepth<XT, VEC> : 2;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 red[2][32];
+  __shared__ float2 red[2][32], red_far[sizeof(XT) == 4 ? 32 : 1];
+  __shared__ uint32_t block_pending;
   const int lanes = a.lanes, lane = threadIdx.x % lanes, units = a.d / VEC;
   // (rows fit 31 bits)
   const int in_block = blockDim.x / lanes, groups = gridDim.x * in_block, nrows = static_cast<int>(a.rows);
@@ -369,128 +416,117 @@ __global__ void __launch_bounds__(THREADS) norm_forward_kernel(const __grid_cons
   const int64_t y_step = groups * a.ldy;
   // all lanes of a warp go round together: the rows of its groups may end apart
   const int turns = (nrows + groups - 1) / groups;
-  for (int turn = 0; turn < turns; ++turn, row += groups, y += y_step) {
-    float2 f[kElems / 2];
-    copy_async_wait<DEPTH - 2>();
-    rows.get(f);
-    rows.load(ahead > 0);
-    ahead -= groups;
-    copy_async_commit();
-    // the warp's (or group's) mean and squares around it, then the block's
-    float2 t = f[0], squares = both(0.0f);
+  // Rows of fp32 elements that are far wait until 32 have been looked at: with their
+  // path inside the loop over rows, rows past 8192 took half as long again.
+  constexpr bool kWait = sizeof(XT) == 4;
+  for (int turn = 0; turn < turns;) {
+    uint32_t pending = 0;  // (WARPS: the block's, in shared memory)
+    if (kWait && WARPS && threadIdx.x == 0) block_pending = 0;
+    const int end = kWait ? min(turns, turn + 32) : turns;
+    for (; turn < end; ++turn, row += groups, y += y_step) {
+      bool far = false;
+      float2 f[kElems / 2];
+      copy_async_wait<DEPTH - 2>();
+      rows.get(f);
+      rows.load(ahead > 0);
+      ahead -= groups;
+      copy_async_commit();
+      // the warp's (or group's) mean and squares around it, then the block's
+      float2 t = f[0], squares = both(0.0f);
 #pragma unroll
-    for (int i = 1; i < kElems / 2; ++i) t = add2(t, f[i]);
-    float sum = lanes_sum<WARPS>(t.x + t.y, lanes), q, mean, centre;  // centre: what is still to be taken from f
-    if constexpr (sizeof(XT) == 2) {
-      const float m = over(sum, held, inv_held);
+      for (int i = 1; i < kElems / 2; ++i) t = add2(t, f[i]);
+      float sum = lanes_sum<WARPS>(t.x + t.y, lanes), q, mean, centre;  // centre: what is still to be taken from f
+      if constexpr (sizeof(XT) == 2) {
+        const float m = over(sum, held, inv_held);
 #pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) f[i] = add2(f[i], both(-m));
-      if (!full) fill_row<VEC>(f, count, 0.0f);
+        for (int i = 0; i < kElems / 2; ++i) f[i] = add2(f[i], both(-m));
+        if (!full) fill_row<VEC>(f, count, 0.0f);
 #pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) squares = fma2(f[i], f[i], squares);
-      q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
-      mean = m;
-      if constexpr (WARPS) {
-        float2* r = red[turn & 1];  // two in turn: one barrier a row
-        if (in_warp == 0) r[warp] = make_float2(sum, q);
-        __syncthreads();
-        const float2 o = other < warps ? r[other] : both(0.0f);
-        sum = warps_sum(o.x, few);
-        mean = over(sum, d, inv_d);
-        const float c = fmaf(-mean, counted.x, o.x);
-        q = warps_sum(fmaf(c * counted.y, c, o.y), few);
-      }
-      centre = (mean - m) + fmaf(-mean, d, sum) * inv_d;
-      if (!(fabsf(mean) < INFINITY)) mean = sum * inv_d;  // (an infinite sum's is infinite)
-    } else {
-      mean = sum * inv_held;
-      if (full) {
-#pragma unroll
-        for (int i = 0; i < kElems / 2; ++i) {
-          const float2 c = add2(f[i], both(-mean));
-          squares = fma2(c, c, squares);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kElems / 2; ++i) {
-          float2 c = add2(f[i], both(-mean));
-          if (2 * i / VEC >= count) c.x = 0.0f;
-          if ((2 * i + 1) / VEC >= count) c.y = 0.0f;
-          squares = fma2(c, c, squares);
-        }
-      }
-      q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
-      if constexpr (WARPS) {
-        float2* r = red[turn & 1];
-        if (in_warp == 0) r[warp] = make_float2(sum, q);
-        __syncthreads();
-        const float2 o = other < warps ? r[other] : both(0.0f);
-        mean = warps_sum(o.x, few) * inv_d;
-        const float c = fmaf(o.x, counted.y, -mean);
-        q = warps_sum(fmaf(counted.x * c, c, o.y), few);
-      }
-      centre = mean;
-      const bool far = fabsf(mean) < INFINITY && !(fabsf(mean) <= kFar * root(q * inv_d) && q < INFINITY);
-      if (WARPS ? far : __any_sync(0xffffffffu, far)) {  // (all threads of a row have the same sums)
-        const auto row_sums = [&](float a, float b) {
-          if constexpr (!WARPS) return make_float2(lanes_sum<false>(a, lanes), lanes_sum<false>(b, lanes));
-          const float v = warp_sums(a, b);
-          float2* r = red[turn & 1];
-          __syncthreads();
-          if (in_warp == 0) r[warp].x = v;
-          if (in_warp == 16) r[warp].y = v;
+        for (int i = 0; i < kElems / 2; ++i) squares = fma2(f[i], f[i], squares);
+        q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
+        mean = m;
+        if constexpr (WARPS) {
+          float2* r = red[turn & 1];  // two in turn: one barrier a row
+          if (in_warp == 0) r[warp] = make_float2(sum, q);
           __syncthreads();
           const float2 o = other < warps ? r[other] : both(0.0f);
-          return make_float2(warps_sum(o.x, few), warps_sum(o.y, few));
-        };
-        const auto move = [&](float by) {
-          t = squares = both(0.0f);
-#pragma unroll
-          for (int i = 0; i < kElems / 2; ++i) f[i] = add2(f[i], both(-by));
-          fill_row<VEC>(f, count, 0.0f);
+          sum = warps_sum(o.x, few);
+          mean = over(sum, d, inv_d);
+          const float c = fmaf(-mean, counted.x, o.x);
+          q = warps_sum(fmaf(c * counted.y, c, o.y), few);
+        }
+        centre = (mean - m) + fmaf(-mean, d, sum) * inv_d;
+        if (!(fabsf(mean) < INFINITY)) mean = sum * inv_d;  // (an infinite sum's is infinite)
+      } else {
+        mean = sum * inv_held;
+        if (full) {
 #pragma unroll
           for (int i = 0; i < kElems / 2; ++i) {
-            t = add2(t, f[i]);
-            squares = fma2(f[i], f[i], squares);
+            const float2 c = add2(f[i], both(-mean));
+            squares = fma2(c, c, squares);
           }
-          return row_sums(t.x + t.y, squares.x + squares.y);
-        };
-        float2 sums = move(far ? mean : 0.0f);  // (a row beside it stays as it is)
-        const float shift = far ? over(sums.x, d, inv_d) : 0.0f;
-        sums = move(shift);
-        if (far) {
-          centre = sums.x * inv_d;
-          mean += shift + centre;
-          q = fmaf(-sums.x, centre, sums.y);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kElems / 2; ++i) {
+            float2 c = add2(f[i], both(-mean));
+            if (2 * i / VEC >= count) c.x = 0.0f;
+            if ((2 * i + 1) / VEC >= count) c.y = 0.0f;
+            squares = fma2(c, c, squares);
+          }
+        }
+        q = lanes_sum<WARPS>(squares.x + squares.y, lanes);
+        if constexpr (WARPS) {
+          float2* r = red[turn & 1];
+          if (in_warp == 0) r[warp] = make_float2(sum, q);
+          __syncthreads();
+          const float2 o = other < warps ? r[other] : both(0.0f);
+          mean = warps_sum(o.x, few) * inv_d;
+          const float c = fmaf(o.x, counted.y, -mean);
+          q = warps_sum(fmaf(counted.x * c, c, o.y), few);
+        }
+        centre = mean;
+        far = fabsf(mean) < INFINITY && !(fabsf(mean) <= kFar * root(q * inv_d) && q < INFINITY);
+        if constexpr (!WARPS) pending |= far ? 1u << (turn & 31) : 0;
+        else if (far && threadIdx.x == 0) block_pending |= 1u << (turn & 31);
+      }
+      const float rstd = reciprocal_root(fmaf(q, inv_d, a.eps));
+      if (row >= nrows || far) continue;
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kElems / 2; ++i) {
+          // (what is left of bf16 elements is small: one instruction)
+          const float2 h = sizeof(XT) == 2 ? fma2(f[i], both(rstd), both(-centre * rstd)) : scaled(f[i], centre, rstd);
+          f[i] = fma2(h, w[i], b[i]);
+        }
+        store_row<XT, VEC>(y, apart, count, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kElems / VEC; ++i) {
+          if (i >= count) continue;
+          const int at = (lane + i * lanes) * VEC;
+          float e[VEC], w_unit[VEC], b_unit[VEC];
+          unit_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, at, w_unit);
+          unit_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, at, b_unit);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) e[j] = fmaf((get(f, i * VEC + j) - centre) * rstd, w_unit[j], b_unit[j]);
+          store_unit<XT, VEC>(y + i * apart, e);
         }
       }
-    }
-    const float rstd = reciprocal_root(fmaf(q, inv_d, a.eps));
-    if (row >= nrows) continue;
-    if constexpr (kKeep) {
-#pragma unroll
-      for (int i = 0; i < kElems / 2; ++i) {
-        // (what is left of bf16 elements is small: one instruction)
-        const float2 h = sizeof(XT) == 2 ? fma2(f[i], both(rstd), both(-centre * rstd)) : scaled(f[i], centre, rstd);
-        f[i] = fma2(h, w[i], b[i]);
-      }
-      store_row<XT, VEC>(y, apart, count, f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kElems / VEC; ++i) {
-        if (i >= count) continue;
-        const int at = (lane + i * lanes) * VEC;
-        float e[VEC], w_unit[VEC], b_unit[VEC];
-        unit_columns<VEC>(a.w, a.w_f32, a.w_fits, 1.0f, at, w_unit);
-        unit_columns<VEC>(a.b, a.w_f32, a.w_fits, 0.0f, at, b_unit);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) e[j] = fmaf((get(f, i * VEC + j) - centre) * rstd, w_unit[j], b_unit[j]);
-        store_unit<XT, VEC>(y + i * apart, e);
+      if (lane == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
       }
     }
-    if (lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+    if constexpr (kWait) {
+      // (WARPS: all threads of a row have the same sums)
+      if constexpr (WARPS) __syncthreads();
+      const uint32_t all = WARPS ? block_pending : __reduce_or_sync(0xffffffffu, pending);
+      if constexpr (WARPS) pending = all;
+      for (uint32_t any = all; any != 0; any &= any - 1) {
+        const int k = __ffs(any) - 1, back = ((turn - 1) & 31) + 1 - k;
+        far_row<WARPS>(a, row - static_cast<int64_t>(back) * groups, lane, lanes, pending >> k & 1, red_far);
+      }
+      if constexpr (WARPS) __syncthreads();
     }
   }
 }
@@ -524,12 +560,10 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
   griddep_launch_dependents();
   __shared__ float red[kSlowThreads / 32];
   __shared__ float2 reds[kSlowThreads / 32];
-  const auto finite = [](float v) { return fabsf(v) < INFINITY ? v : 0.0f; };  // (an infinite mean stays one)
-  const auto within = [](float v) { return fabsf(v) < 0x1p100f ? v : 0.0f; };
   const float d = static_cast<float>(a.d);
   const float n = static_cast<float>((a.d - static_cast<int>(threadIdx.x) + kSlowThreads - 1) / kSlowThreads);
   const XT* ahead = static_cast<const XT*>(a.x) + blockIdx.x * a.ldx;
-  float x_first = to_float(ahead[0]), x_own = to_float(ahead[threadIdx.x]);  // of the next row: its first, the thread's first
+  float x_first = to_float(ahead[0]), x_own = to_float(ahead[threadIdx.x]);  // the next row's first, the thread's first
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const XT* x = static_cast<const XT*>(a.x) + row * a.ldx;
     XT* y = static_cast<XT*>(a.y) + row * a.ldy;
@@ -553,7 +587,7 @@ __global__ void __launch_bounds__(kSlowThreads) norm_forward_wide_kernel(const _
       sums.y = fmaf(c, c, sums.y);
     }
     sums = block_sums(sums.x, sums.y, reds);
-    const float s = finite(sums.x), shift = s / d, mean = near + shift;
+    const float s = finite(sums.x), shift = s / d, mean = near + shift;  // (an infinite mean stays one)
     const float rstd = reciprocal_root(fmaf(-shift, s, sums.y) / d + a.eps);
     for (int i = threadIdx.x; i < a.d; i += kSlowThreads)
       y[i] = from_float<XT>(fmaf(((to_float(x[i]) - near) - shift) * rstd, a.w ? element(a.w, a.w_f32, i) : 1.0f,
@@ -1032,7 +1066,7 @@ dgl_status run_backward(dgl_norm_desc n, cudaStream_t stream) {
     groups = plan.groups;
     a.lanes = plan.lanes;
     a.part = part;
-      cudaError_t e = cudaSuccess;
+    cudaError_t e = cudaSuccess;
     if (n.d > kWide) {
       if (n.dx)
         e = with_types(n.x_dtype, 1, [&](auto x, auto) {
@@ -1047,7 +1081,7 @@ dgl_status run_backward(dgl_norm_desc n, cudaStream_t stream) {
       e = with_types(n.x_dtype, vec, [&](auto x, auto v) {
         using X = decltype(x);
         constexpr int kVec = decltype(v)::value;
-            return n.d > kMid      ? launch_backward<X, kVec, 1024, true>(a, plan, stream)
+        return n.d > kMid     ? launch_backward<X, kVec, 1024, true>(a, plan, stream)
                : a.lanes > 32 ? launch_backward<X, kVec, 512, true>(a, plan, stream)
                               : launch_backward<X, kVec, 512, false>(a, plan, stream);
       });

@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from . import ADAMW_BLOCK, AdamWDesc, AdamWTensor, _check, load_library
+from . import ADAMW_BLOCK, OUT_F32, AdamWDesc, AdamWTensor, _check, load_library
 from .head import _not_here, _packed
 from .norm import _CODES
 
@@ -13,29 +13,30 @@ _F32 = torch.float32
 _STATES = {32: (_F32, _F32), 8: (torch.float8_e4m3fn, torch.float8_e5m2)}
 
 
-def _code(t, name):
+def _code(t, name, i):
     code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if code is None:
-        raise TypeError(f"{name} must be a bf16 or fp32 CUDA tensor")
+        raise TypeError(f"{name}[{i}] must be a bf16 or fp32 CUDA tensor")
     return code
 
 
-def _flat(t, name, device):
+def _flat(t, name, i, device):
     """Checks a contiguous tensor on the current device; returns its address."""
     if not isinstance(t, torch.Tensor) or t.get_device() != device:
-        _not_here(t, name, device)
+        _not_here(t, f"{name}[{i}]", device)
     if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name}[{i}] must be contiguous")
     return t.data_ptr()
 
 
 def _apart(written):
-    """Refuses memory that a step would write twice; written: (address, bytes, name) of all that it writes."""
+    """Refuses memory that a step would write twice; written: (address, bytes, list, place) of all that it writes."""
     end, last = 0, None
-    for at, size, name in sorted(w for w in written if w[1]):
-        if at < end:
-            raise ValueError(f"{name} and {last} overlap: the updates would race")
-        end, last = at + size, name
+    for at, size, name, i in sorted(written):
+        if at < end and size:
+            raise ValueError(f"{name}[{i}] and {last[0]}[{last[1]}] overlap: the updates would race")
+        if size:
+            end, last = at + size, (name, i)
 
 
 def _unmoved(tensors, places, indexes):
@@ -99,8 +100,6 @@ class AdamW:
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
         if len(decay) != n:
             raise ValueError("weight_decay has one entry for each of params")
-        for i, p in enumerate(params):
-            _code(p, f"params[{i}]")
         if master is True:
             master = [p.detach().to(_F32, copy=True).contiguous() if p.dtype == torch.bfloat16 else None for p in params]
         self.device, self.state_bits, self.lr = device, state_bits, lr
@@ -157,15 +156,17 @@ class AdamW:
         if master is not None and len(master) != len(params):
             raise ValueError("master has one entry for each of params")
         table = (AdamWTensor * len(params))()
-        for i, p in enumerate(params):
-            t = table[i]
-            t.param_dtype = _code(p, f"params[{i}]")
-            t.param, t.n, t.weight_decay = _flat(p, f"params[{i}]", device), p.numel(), self._decay[i]
+        sizes, written = [], []
+        for i, (t, p, decay) in enumerate(zip(table, params, self._decay)):
+            t.param_dtype = code = _code(p, "params", i)
+            t.param, t.n, t.weight_decay = at, n, _ = _flat(p, "params", i, device), p.numel(), decay
+            sizes.append(n)
+            written.append((at, n * (4 if code == OUT_F32 else 2), "params", i))
             if master is not None and master[i] is not None:
-                if p.dtype != torch.bfloat16:
+                if code == OUT_F32:
                     raise TypeError(f"master[{i}] is given beside a param of fp32")
-                t.master = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
-        sizes = [p.numel() for p in params]
+                t.master = at = _packed(master[i], f"master[{i}]", _F32, p.shape, device)
+                written.append((at, n * 4, "master", i))
         blocks = [-(-k // ADAMW_BLOCK) for k in sizes]
         m_type, v_type = _STATES[self.state_bits]
         states = [("exp_avg", sizes, m_type), ("exp_avg_sq", sizes, v_type)]
@@ -174,42 +175,45 @@ class AdamW:
         elif held["exp_avg_scale"] is not None or held["exp_avg_sq_scale"] is not None:
             raise ValueError("states of 32 bits have no scales")
         for name, lengths, dtype in states:
-            self._state(name, held[name], lengths, dtype, table)
+            self._state(name, held[name], lengths, dtype, table, written)
         steps = _packed(held["steps"], "steps", torch.int64, (1,), device)
-        lists = [("params", params), ("master", master or ())] + [(name, held[name]) for name, _, _ in states]
-        _apart([(t.data_ptr(), t.nbytes, f"{name}[{i}]") for name, tensors in lists for i, t in enumerate(tensors)
-                if t is not None] + [(steps, 8, "steps"), (self._ticket.data_ptr(), 4, "the ticket")])
+        _apart(written + [(steps, 8, "steps", 0), (self._ticket.data_ptr(), 4, "the ticket", 0)])
         grads = None if held["grads"] is None else list(held["grads"])
         if grads is not None:
             self._take(grads, table, params)
         # what is the optimizer's own is held by aliases, whose memory nothing but the optimizer lets go
         for name, _, _ in states:
-            held[name] = [t.detach() for t in held[name]]
-        held.update(params=params, grads=grads, steps=held["steps"].detach(),
-                    master=None if master is None else [None if t is None else t.detach() for t in master])
+            held[name] = [t.data for t in held[name]]
+        held.update(params=params, grads=grads, steps=held["steps"].data,
+                    master=None if master is None else [None if t is None else t.data for t in master])
         watched = params + (grads or [])
         self._held, self._table, self._desc.steps = held, table, steps
         # the memory of those that may move stays taken until they are seen to have moved: no other tensor gets its address
-        self._watched, self._pinned = watched, [t.detach() for t in watched]
-        self._places, self._indexes = [t.data_ptr() for t in watched], list(range(len(watched)))
+        self._watched, self._pinned = watched, [t.untyped_storage() for t in watched]
+        self._places = [t.param for t in table] + ([t.grad for t in table] if grads is not None else [])
+        self._places, self._indexes = [at or 0 for at in self._places], list(range(len(watched)))
 
-    def _state(self, name, given, sizes, dtype, table):
+    def _state(self, name, given, sizes, dtype, table, written):
         """A state's addresses in the table."""
         if given is None or len(given) != len(sizes):
             raise ValueError(f"{name} has one entry for each of params")
+        device, each = self.device, dtype.itemsize
         for i, (t, k) in enumerate(zip(given, sizes)):
             if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() != k:
                 raise TypeError(f"{name}[{i}] must be a {dtype} CUDA tensor of {k} elements")
-            setattr(table[i], name, _flat(t, f"{name}[{i}]", self.device))
+            at = _flat(t, name, i, device)
+            setattr(table[i], name, at)
+            written.append((at, k * each, name, i))
 
     def _take(self, grads, table, params):
         if len(grads) != len(params):
             raise ValueError("grads has one entry for each of params")
-        for t, g, p in zip(table, grads, params):
-            t.grad_dtype = _code(g, "a gradient")
+        device = self.device
+        for i, (t, g, p) in enumerate(zip(table, grads, params)):
+            t.grad_dtype = _code(g, "grads", i)
             if g.shape != p.shape:
-                raise ValueError(f"a gradient of shape {tuple(g.shape)} for a param of shape {tuple(p.shape)}")
-            t.grad = _flat(g, "a gradient", self.device)
+                raise ValueError(f"grads[{i}] of shape {tuple(g.shape)} for a param of shape {tuple(p.shape)}")
+            t.grad = _flat(g, "grads", i, device)
 
     def step(self, grads=None, *, lr=None, grad_scale=None, stream=None):
         """One step, of the gradients given or of those given at the start.
