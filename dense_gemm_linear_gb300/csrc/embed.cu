@@ -189,7 +189,8 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, uint2* items, int
     for (int i = 0; i < EACH; ++i) {
       const uint32_t digit = key[i] >> shift & mask;
       // the lanes with this digit, by a vote on each of its bits (a match
-      // instruction took longer: 131072 tokens 60 us with it, 55 so)
+      // instruction took longer: 131072 tokens 60 us with it, 55 so, and 50 with the
+      // last pass below)
       uint32_t same = 0xffffffffu;
 #pragma unroll
       for (int bit = 0; bit < kDigitBits; ++bit) {

@@ -128,8 +128,9 @@ __device__ __forceinline__ float2 scaled(float2 x, float mean, float rstd) {
 // (cp.async) and reads them back itself, so nothing synchronises, no register waits
 // and far more is in flight than registers would hold.  bf16 rows off 4 bytes are
 // held in registers, one row ahead.  Forward, 10240 x 2048 bf16: 23.4 us with one
-// row ahead in registers, 16.4 so, 18.7 with one bulk copy a row, whose arrival and
-// release cost more instructions than the copies of 16 bytes.
+// row ahead in registers, 16.4 so (17.0 with what has been added since), 18.7 with
+// one bulk copy a row, whose arrival and release cost more instructions than the
+// copies of 16 bytes.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   if constexpr (BYTES == 16)
