@@ -92,8 +92,9 @@ struct AdamScalars {
 };
 
 // Room in a launch's parameters (at most 32764 bytes); few tensors take the
-// small table, whose parameters are quicker to hand over.
-constexpr int kFewTensors = 40, kManyTensors = 336;
+// small table, whose parameters are quicker to hand over (a step of 49 tensors from
+// Python 10.4 us with the large one, 9.1 so; of 6 5.7 either with 40 places or 120).
+constexpr int kFewTensors = 120, kManyTensors = 336;
 
 template <int CAP>
 struct AdamTable {
