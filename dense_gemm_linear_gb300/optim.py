@@ -93,6 +93,8 @@ class AdamW:
         device = torch.cuda.current_device()
         params = list(params)
         n = len(params)
+        for i, p in enumerate(params):
+            _code(p, "params", i)
         if exp_avg is not None and len(exp_avg) and exp_avg[0].dtype != _F32:
             state_bits = 8
         if state_bits not in _STATES:
@@ -159,7 +161,8 @@ class AdamW:
         sizes, written = [], []
         for i, (t, p, decay) in enumerate(zip(table, params, self._decay)):
             t.param_dtype = code = _code(p, "params", i)
-            t.param, t.n, t.weight_decay = at, n, _ = _flat(p, "params", i, device), p.numel(), decay
+            at, n = _flat(p, "params", i, device), p.numel()
+            t.param, t.n, t.weight_decay = at, n, decay
             sizes.append(n)
             written.append((at, n * (4 if code == OUT_F32 else 2), "params", i))
             if master is not None and master[i] is not None:
@@ -190,8 +193,7 @@ class AdamW:
         self._held, self._table, self._desc.steps = held, table, steps
         # the memory of those that may move stays taken until they are seen to have moved: no other tensor gets its address
         self._watched, self._pinned = watched, [t.untyped_storage() for t in watched]
-        self._places = [t.param for t in table] + ([t.grad for t in table] if grads is not None else [])
-        self._places, self._indexes = [at or 0 for at in self._places], list(range(len(watched)))
+        self._places, self._indexes = [t.data_ptr() for t in watched], list(range(len(watched)))
 
     def _state(self, name, given, sizes, dtype, table, written):
         """A state's addresses in the table."""

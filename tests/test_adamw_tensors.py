@@ -237,3 +237,10 @@ def test_a_step_on_another_stream_is_noted(calls, monkeypatch, how):
     used = [*params, *grads, *opt.master, *opt.exp_avg, *opt.exp_avg_sq, *opt.exp_avg_scale, *opt.exp_avg_sq_scale, opt.steps,
             lr, scale]
     assert {(t.data_ptr(), "s") for t in used} <= set(noted)
+
+
+def test_params_that_are_no_tensors(calls):
+    for bad in ([3.0], ["p"], [None], [torch.nn.Linear(2, 2)], [some(8, I64)]):
+        for given in (dict(), dict(master=True), dict(state_bits=8)):
+            with pytest.raises(TypeError, match="params"):
+                dgl.AdamW(bad, **given)
